@@ -1,0 +1,157 @@
+// kv_compact: the cache rows of an accepted path move to the front of their
+// tree's slots, in every layer at once.
+//
+// "Phi-4: quality transfer and interrupted throughput studies": the intro
+// fixes the cache format and the 40-layer geometry; a verified tree of
+// drafted tokens leaves its accepted rows scattered over the last positions
+// of each sequence, and the next step needs them in order.
+//
+// For sequence b with n nodes at positions base .. base + n - 1 and an
+// accepted path of m nodes, row base + path[j] goes to base + j.  A path
+// increases strictly, so path[j] >= j: rows only move down, and a warp that
+// moves them in order of j, reading a group of rows whole before it writes
+// them, never overwrites a row that is still to be read (a later row j' sits
+// at path[j'] >= j' > every j written so far).
+//
+// HBM-bound copy.  One warp per (layer, sequence, KV head); a row is 24
+// pieces of 16 bytes (16 of K, 8 of V), and a group of 4 rows puts 3
+// loads in flight per lane.
+#include "k16v8_device.cuh"
+
+namespace k16v8 {
+namespace compact {
+
+constexpr int kWarpsPerCta = 8;
+constexpr int kPieces = kHeadDim * 3 / 16;  // 24 pieces of 16 bytes per row
+constexpr int kGroupRows = 4;
+constexpr int kPerLane = kPieces * kGroupRows / 32;
+
+// The base position and node count of sequence b, or false (nothing to do).
+__device__ __forceinline__ bool sequence(const int32_t *qo_indptr, const int32_t *seq_lens, int b,
+                                         int32_t maxp, int32_t max_path, int &base, int &n) {
+  const int q0 = __ldg(qo_indptr + b), L = __ldg(seq_lens + b);
+  n = __ldg(qo_indptr + b + 1) - q0;
+  base = L - n;
+  return q0 >= 0 && n >= 0 && n <= L && n <= max_path && L <= maxp * kPage;
+}
+
+__global__ void __launch_bounds__(kWarpsPerCta * 32) kv_compact_kernel(
+    const uint64_t *__restrict__ k_ptrs, const uint64_t *__restrict__ v_ptrs, int32_t layers,
+    const int32_t *__restrict__ block_table, int32_t maxp, const int32_t *__restrict__ seq_lens,
+    const int32_t *__restrict__ qo_indptr, const int32_t *__restrict__ path, int32_t max_path,
+    const int32_t *__restrict__ path_len, int32_t batch, int32_t hkv, int32_t num_pages,
+    int32_t *__restrict__ new_lens, int32_t *dev_error) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int64_t items = static_cast<int64_t>(layers) * batch * hkv;
+  for (int64_t item = blockIdx.x * static_cast<int64_t>(kWarpsPerCta) + (threadIdx.x >> 5);
+       item < items; item += static_cast<int64_t>(gridDim.x) * kWarpsPerCta) {
+    const int g = static_cast<int>(item % hkv);
+    const int b = static_cast<int>(item / hkv % batch);
+    const int layer = static_cast<int>(item / hkv / batch);
+    const bool report = layer == 0 && g == 0;  // one warp per sequence
+    int base, n;
+    const int m = __ldg(path_len + b);
+    if (!sequence(qo_indptr, seq_lens, b, maxp, max_path, base, n)) {
+      if (report && lane == 0) {
+        flag_error(dev_error, K16V8_DEVERR_SEQLEN);
+        if (new_lens) new_lens[b] = __ldg(seq_lens + b);
+      }
+      continue;
+    }
+    // the path: strictly increasing nodes of this tree
+    const int32_t *pb = path + static_cast<int64_t>(b) * max_path;
+    bool good = m >= 0 && m <= n;
+    for (int j = lane; j < min(m, n); j += 32) {
+      const int p = __ldg(pb + j), before = j > 0 ? __ldg(pb + j - 1) : -1;
+      good &= p > before && p < n;
+    }
+    good = __all_sync(0xffffffffu, good);
+    if (report && lane == 0) {
+      if (!good) flag_error(dev_error, K16V8_DEVERR_TREE);
+      if (new_lens) new_lens[b] = good ? base + m : __ldg(seq_lens + b);
+    }
+    if (!good) continue;
+    uint8_t *kc = reinterpret_cast<uint8_t *>(__ldg(k_ptrs + layer));
+    uint8_t *vc = reinterpret_cast<uint8_t *>(__ldg(v_ptrs + layer));
+    const int32_t *bt = block_table + static_cast<int64_t>(b) * maxp;
+    // byte offset of position pos's row in a cache of one-byte elements, -1
+    // for a page id outside the pool
+    auto row_of = [&](int pos) -> int64_t {
+      const int page = __ldg(bt + pos / kPage);
+      if (page < 0 || page >= num_pages) {
+        flag_error(dev_error, K16V8_DEVERR_PAGE);
+        return -1;
+      }
+      return ((static_cast<int64_t>(page) * hkv + g) * kPage + pos % kPage) * kHeadDim;
+    };
+    for (int j0 = 0; j0 < m; j0 += kGroupRows) {
+      uint4 piece[kPerLane];
+      uint4 *to[kPerLane];
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i) {
+        const int x = i * 32 + lane, j = j0 + x / kPieces, c = x % kPieces;
+        to[i] = nullptr;
+        if (j >= m) continue;
+        const int p = __ldg(pb + j);
+        if (p == j) continue;  // in place already
+        const int64_t src = row_of(base + p), dst = row_of(base + j);
+        if (src < 0 || dst < 0) continue;
+        uint8_t *cache = c < 16 ? kc : vc;
+        const int64_t width = c < 16 ? 2 : 1;
+        const int64_t at = c < 16 ? 16 * c : 16 * (c - 16);
+        piece[i] = *reinterpret_cast<const uint4 *>(cache + src * width + at);
+        to[i] = reinterpret_cast<uint4 *>(cache + dst * width + at);
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kPerLane; ++i)
+        if (to[i]) *to[i] = piece[i];
+      __syncwarp();
+    }
+  }
+}
+
+}  // namespace compact
+}  // namespace k16v8
+
+using namespace k16v8;
+
+extern "C" int32_t k16v8_kv_compact(const uint64_t *k_caches, const uint64_t *v_caches,
+                                    int32_t num_layers, const int32_t *block_table,
+                                    int32_t max_pages_per_seq, const int32_t *seq_lens,
+                                    const int32_t *qo_indptr, const int32_t *path,
+                                    int32_t max_nodes, const int32_t *path_len, int32_t batch,
+                                    int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+                                    int32_t *new_seq_lens, int32_t *dev_error, void *stream) {
+  if (num_layers < 0 || batch < 0 || max_nodes < 0 || max_pages_per_seq < 0 ||
+      num_kv_heads <= 0 || num_pages <= 0)
+    return K16V8_ERR_INVALID_ARG;
+  if (max_pages_per_seq > 0x7fffffff / kPage) return K16V8_ERR_INVALID_ARG;
+  if (head_dim != kHeadDim || max_nodes > K16V8_MAX_TREE_NODES)
+    return K16V8_ERR_UNSUPPORTED_SHAPE;
+  if (batch == 0 || num_layers == 0) return K16V8_OK;
+  if (!k_caches || !v_caches || !block_table || !seq_lens || !qo_indptr || !path_len ||
+      (max_nodes > 0 && !path))
+    return K16V8_ERR_INVALID_ARG;
+  if (!k16v8_aligned(k_caches, 8) || !k16v8_aligned(v_caches, 8) ||
+      !k16v8_aligned(block_table, 4) || !k16v8_aligned(seq_lens, 4) ||
+      !k16v8_aligned(qo_indptr, 4) || !k16v8_aligned(path, 4) || !k16v8_aligned(path_len, 4) ||
+      (new_seq_lens && !k16v8_aligned(new_seq_lens, 4)))
+    return K16V8_ERR_INVALID_ARG;
+  // other warps still read seq_lens when the new lengths are written
+  if (new_seq_lens && new_seq_lens < seq_lens + batch && seq_lens < new_seq_lens + batch)
+    return K16V8_ERR_INVALID_ARG;
+  const int sms = k16v8_sm_count();
+  if (sms <= 0) return K16V8_ERR_CUDA;
+  const int64_t items = static_cast<int64_t>(num_layers) * batch * num_kv_heads;
+  int64_t blocks = (items + compact::kWarpsPerCta - 1) / compact::kWarpsPerCta;
+  const int64_t cap = static_cast<int64_t>(sms) * 8;
+  if (blocks > cap) blocks = cap;
+  return k16v8_launch_pdl(compact::kv_compact_kernel, dim3(static_cast<unsigned>(blocks)),
+                          dim3(compact::kWarpsPerCta * 32), 0, static_cast<cudaStream_t>(stream),
+                          k_caches, v_caches, num_layers, block_table, max_pages_per_seq, seq_lens,
+                          qo_indptr, path, max_nodes, path_len, batch, num_kv_heads, num_pages,
+                          new_seq_lens, dev_error);
+}

@@ -26,11 +26,14 @@ K16V8_ERR_STATIC_SCRATCH_LIMIT = 6
 STATIC_SCRATCH_BYTES = 32 << 20
 K16V8_F16 = 0
 K16V8_F32 = 1
+K16V8_BF16 = 2
 DECODE_METADATA_READY = 1
 DEVERR_SLOT, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_TIMEOUT, DEVERR_INTERNAL = 1, 2, 4, 8, 16
+DEVERR_POSITION, DEVERR_TREE = 32, 64
 PAGE_SIZE = 16
 HEAD_DIM = 128
 MAX_SPLIT_CHUNK = 8192  # K16V8_MAX_SPLIT_CHUNK
+MAX_TREE_NODES = 64  # K16V8_MAX_TREE_NODES
 
 # Every symbol include/k16v8.h declares, with its ctypes signature.
 _P = ctypes.c_void_p
@@ -92,6 +95,16 @@ SIGNATURES = {
     "k16v8_paged_prefill_attention_wait_test": (_i32, [_P, _P, _i32, _i32, _P, _P, _P, _P,
                                                        _i32, _P, _i32, _i32, _i32, _i32, _i32,
                                                        _f32, _P, _P, _P, _P]),
+    "k16v8_rope_kv_append": (_i32, [_P, _i64, _P, _i64, _P, _i64, _i32, _P, _P, _i32, _i32, _f32,
+                                    _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P]),
+    "k16v8_tree_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "k16v8_paged_tree_attention": (_i32, [_P, _P, _i32, _i32, _P, _P, _P, _P, _P, _i32, _P, _i32,
+                                          _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz, _P, _P, _P,
+                                          _P]),
+    "k16v8_tree_verify": (_i32, [_P, _i64, _P, _i64, _P, _P, _P, _i32, _i32, _P, _i32, _i32, _P,
+                                 _P, _P, _P, _P]),
+    "k16v8_kv_compact": (_i32, [_P, _P, _i32, _P, _i32, _P, _P, _P, _i32, _P, _i32, _i32, _i32,
+                                _i32, _P, _P, _P]),
     "k16v8_read_device_error": (_i32, [_P, _P, ctypes.POINTER(_i32)]),
     "k16v8_status_string": (ctypes.c_char_p, [_i32]),
 }
@@ -148,6 +161,39 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with dense rows")
     return t.stride(0)
+
+
+def _device(t: torch.Tensor) -> int:
+    """The current device, on which the tensors of a call have to be."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {t.device}")
+    return dev
+
+
+def _dense(t, name: str, dtype, shape, dev: int) -> int:
+    """Address of a dense tensor of this type and shape on device dev."""
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != dev):
+        raise ValueError(f"{name} must be a dense {dtype} tensor of shape {tuple(shape)} on "
+                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)}"
+                         f"{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, dtype, shape, dev: int):
+    """Address and token stride of [tokens, heads, head_dim] with dense rows
+    (a slice of a wider row is fine)."""
+    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
+            or t.stride(2) != 1 or t.stride(1) != shape[2]
+            or (shape[0] > 1 and t.stride(0) < shape[1] * shape[2])):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} with dense rows on cuda:{dev}, got "
+                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+
+
+def _error_word(dev_error, dev: int):
+    return None if dev_error is None else _dense(dev_error, "dev_error", torch.int32, (1,), dev)
 
 
 # ---- kv_append ---------------------------------------------------------------
@@ -443,6 +489,150 @@ def k16v8_paged_decode_append_attention_balanced(q, k_new, v_new, k_cache, v_cac
     _append_balanced("k16v8_paged_decode_append_attention_balanced", q, k_new, v_new, k_cache,
                      v_cache, v_scale, block_table, seq_lens, sm_scale, workspace, out, lse,
                      dev_error, stream, flags)
+
+
+# ---- speculative step ------------------------------------------------------------
+
+_X_DTYPES = {torch.float16: K16V8_F16, torch.float32: K16V8_F32, torch.bfloat16: K16V8_BF16}
+
+
+def k16v8_rope_kv_append(q, k, v, positions, inv_freq, slot_mapping, v_scale, q_out, k_cache,
+                         v_cache, interleaved=False, attn_factor=1.0, dev_error=None,
+                         stream=None) -> None:
+    """Rotary positions fused with the cache write: q [T,Hq,D] (or None), k, v
+    [T,Hkv,D] of one type (fp16, fp32 or bf16; token strides may exceed the
+    row, e.g. slices of a fused QKV); positions int32 [T]; inv_freq fp32
+    [rotary_dim/2] (see rope.rope_inv_freq); slot_mapping int64 [T]; q_out
+    fp16 [T,Hq,D] (q itself if that is dense fp16); caches as for
+    k16v8_kv_append."""
+    T, hkv, d = k.shape
+    dt, dev = k.dtype, _device(k)
+    if dt not in _X_DTYPES:
+        raise ValueError(f"k must be fp16, fp32 or bf16, got {dt}")
+    hq = 0 if q is None else q.shape[1]
+    q_ptr, q_ts = (None, 0) if q is None else _rows(q, "q", dt, (T, hq, d), dev)
+    k_ptr, k_ts = _rows(k, "k", dt, (T, hkv, d), dev)
+    v_ptr, v_ts = _rows(v, "v", dt, (T, hkv, d), dev)
+    cache = (k_cache.shape[0], hkv, PAGE_SIZE, d)
+    st = load_library().k16v8_rope_kv_append(
+        q_ptr, q_ts, k_ptr, k_ts, v_ptr, v_ts, _X_DTYPES[dt],
+        _dense(positions, "positions", torch.int32, (T,), dev),
+        _dense(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev),
+        2 * inv_freq.numel(), 1 if interleaved else 0, attn_factor,
+        _dense(slot_mapping, "slot_mapping", torch.int64, (T,), dev), T,
+        _dense(v_scale, "v_scale", torch.float32, (hkv,), dev),
+        None if q is None else _dense(q_out, "q_out", torch.float16, (T, hq, d), dev),
+        _dense(k_cache, "k_cache", torch.float16, cache, dev),
+        _dense(v_cache, "v_cache", torch.uint8, cache, dev), cache[0], hq, hkv, d,
+        _error_word(dev_error, dev), _stream(stream))
+    _check("k16v8_rope_kv_append", st)
+
+
+def k16v8_tree_workspace_size(total_q, batch, max_nodes, num_qo_heads, num_kv_heads, head_dim,
+                              max_seq_len) -> int:
+    """Bytes of workspace k16v8_paged_tree_attention needs for these sizes on
+    the current device (0: none)."""
+    return int(load_library().k16v8_tree_workspace_size(
+        total_q, batch, max_nodes, num_qo_heads, num_kv_heads, head_dim, max_seq_len))
+
+
+def k16v8_paged_tree_attention(q, qo_indptr, max_nodes, tree_mask, k_cache, v_cache, v_scale,
+                               block_table, seq_lens, max_seq_len, sm_scale, workspace, out,
+                               lse=None, dev_error=None, stream=None) -> None:
+    """Attention of drafted trees: q fp16 [total_q,Hq,D], ragged by qo_indptr
+    int32 [B+1], the nodes being the last positions of the cache; tree_mask
+    int64 [total_q], bit j of a node's word set where it sees node j of its
+    tree (tree_step.tree_masks builds it from the parents).  workspace uint8
+    of k16v8_tree_workspace_size bytes, or None where that is 0."""
+    total_q, hq, d = q.shape
+    dev = _device(q)
+    P, hkv = k_cache.shape[0], k_cache.shape[1]
+    B = seq_lens.shape[0]
+    cache = (P, hkv, PAGE_SIZE, d)
+    maxp = block_table.shape[1]
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws_bytes = workspace.numel() * workspace.element_size()
+        ws = _dense(workspace, "workspace", workspace.dtype, workspace.shape, dev)
+    st = load_library().k16v8_paged_tree_attention(
+        _dense(q, "q", torch.float16, (total_q, hq, d), dev),
+        _dense(qo_indptr, "qo_indptr", torch.int32, (B + 1,), dev), total_q, max_nodes,
+        _dense(tree_mask, "tree_mask", torch.int64, (total_q,), dev),
+        _dense(k_cache, "k_cache", torch.float16, cache, dev),
+        _dense(v_cache, "v_cache", torch.uint8, cache, dev),
+        _dense(v_scale, "v_scale", torch.float32, (hkv,), dev),
+        _dense(block_table, "block_table", torch.int32, (B, maxp), dev), maxp,
+        _dense(seq_lens, "seq_lens", torch.int32, (B,), dev), max_seq_len, B, hq, hkv, d, P,
+        sm_scale, ws, ws_bytes, _dense(out, "out", torch.float16, (total_q, hq, d), dev),
+        None if lse is None else _dense(lse, "lse", torch.float32, (total_q, hq), dev),
+        _error_word(dev_error, dev), _stream(stream))
+    _check("k16v8_paged_tree_attention", st)
+
+
+def k16v8_tree_verify(target_probs, draft_probs, tokens, parents, qo_indptr, max_nodes, uniforms,
+                      path, path_len, next_token, dev_error=None, stream=None) -> None:
+    """Accepted path and next token of every tree: target_probs, draft_probs
+    fp32 [total_q,V] (rows may be strided; draft_probs None where the drafts
+    were not sampled); tokens, parents int32 [total_q]; uniforms fp32
+    [total_q] in [0, 1); writes path int32 [B,max_nodes], path_len int32 [B],
+    next_token int32 [B]."""
+    total_q, V = target_probs.shape
+    dev = _device(target_probs)
+    B = path_len.shape[0]
+    strides = []
+    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+        if t is None:
+            strides.append(0)
+            continue
+        if (t.dtype is not torch.float32 or t.shape != (total_q, V) or t.get_device() != dev
+                or (V > 1 and t.stride(1) != 1) or (total_q > 1 and t.stride(0) < V)):
+            raise ValueError(f"{name} must be float32 {(total_q, V)} with dense rows on cuda:{dev}, "
+                             f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
+        strides.append(t.stride(0) if total_q > 1 else 0)
+    st = load_library().k16v8_tree_verify(
+        target_probs.data_ptr(), strides[0], _ptr(draft_probs), strides[1],
+        _dense(tokens, "tokens", torch.int32, (total_q,), dev),
+        _dense(parents, "parents", torch.int32, (total_q,), dev),
+        _dense(qo_indptr, "qo_indptr", torch.int32, (B + 1,), dev), total_q, max_nodes,
+        _dense(uniforms, "uniforms", torch.float32, (total_q,), dev), V, B,
+        _dense(path, "path", torch.int32, (B, max_nodes), dev),
+        _dense(path_len, "path_len", torch.int32, (B,), dev),
+        _dense(next_token, "next_token", torch.int32, (B,), dev), _error_word(dev_error, dev),
+        _stream(stream))
+    _check("k16v8_tree_verify", st)
+
+
+def layer_pointers(caches) -> torch.Tensor:
+    """Device array of the layers' cache addresses for k16v8_kv_compact (the
+    caches must outlive it)."""
+    return torch.tensor([c.data_ptr() for c in caches], dtype=torch.int64,
+                        device=caches[0].device)
+
+
+def k16v8_kv_compact(k_ptrs, v_ptrs, num_pages, num_kv_heads, head_dim, block_table, seq_lens,
+                     qo_indptr, path, path_len, new_seq_lens=None, dev_error=None,
+                     stream=None) -> None:
+    """Move the accepted rows of every tree to the front of its positions in
+    all layers (k_ptrs, v_ptrs: layer_pointers of the caches, each of
+    num_pages pages); path int32 [B,max_nodes], path_len int32 [B] from
+    k16v8_tree_verify; new_seq_lens int32 [B] (not seq_lens itself)."""
+    dev = _device(k_ptrs)
+    layers = k_ptrs.shape[0]
+    B, max_nodes = path.shape
+    maxp = block_table.shape[1]
+    st = load_library().k16v8_kv_compact(
+        _dense(k_ptrs, "k_ptrs", torch.int64, (layers,), dev),
+        _dense(v_ptrs, "v_ptrs", torch.int64, (layers,), dev), layers,
+        _dense(block_table, "block_table", torch.int32, (B, maxp), dev), maxp,
+        _dense(seq_lens, "seq_lens", torch.int32, (B,), dev),
+        _dense(qo_indptr, "qo_indptr", torch.int32, (B + 1,), dev),
+        _dense(path, "path", torch.int32, (B, max_nodes), dev), max_nodes,
+        _dense(path_len, "path_len", torch.int32, (B,), dev), B, num_kv_heads, head_dim,
+        num_pages,
+        None if new_seq_lens is None else _dense(new_seq_lens, "new_seq_lens", torch.int32, (B,),
+                                                 dev),
+        _error_word(dev_error, dev), _stream(stream))
+    _check("k16v8_kv_compact", st)
 
 
 def k16v8_read_device_error(dev_error, stream=None) -> int:

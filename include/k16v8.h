@@ -50,6 +50,8 @@ extern "C" {
 #define K16V8_HEAD_DIM 128
 #define K16V8_GQA_GROUP 4
 #define K16V8_MAX_SPLIT_CHUNK 8192
+#define K16V8_MAX_TREE_NODES 64   /* nodes of one sequence's drafted tree */
+#define K16V8_MAX_VOCAB (1 << 24) /* probabilities per row of tree_verify */
 
 typedef enum {
     K16V8_OK = 0,
@@ -61,7 +63,7 @@ typedef enum {
     K16V8_ERR_STATIC_SCRATCH_LIMIT = 6 /* problem too large for the built-in scratch */
 } k16v8_status;
 
-typedef enum { K16V8_F16 = 0, K16V8_F32 = 1 } k16v8_dtype;
+typedef enum { K16V8_F16 = 0, K16V8_F32 = 1, K16V8_BF16 = 2 } k16v8_dtype;
 
 /* Bits of the device error word. */
 #define K16V8_DEVERR_SLOT 0x1    /* kv_append: slot >= num_pages*16 */
@@ -69,6 +71,8 @@ typedef enum { K16V8_F16 = 0, K16V8_F32 = 1 } k16v8_dtype;
 #define K16V8_DEVERR_SEQLEN 0x4  /* seq_len < 0, > max_seq_len, or > 16*max_pages_per_seq */
 #define K16V8_DEVERR_TIMEOUT 0x8 /* a bounded wait on an async copy gave up */
 #define K16V8_DEVERR_INTERNAL 0x10 /* a kernel's own layout check failed; nothing was written */
+#define K16V8_DEVERR_POSITION 0x20 /* rope_kv_append: position < 0 or >= 2^24 */
+#define K16V8_DEVERR_TREE 0x40   /* a parent, token or path entry that is none of its tree */
 
 /*
  * kv_append -- "the candidate also gathers values and writes the compressed
@@ -509,6 +513,168 @@ int32_t k16v8_paged_prefill_attention_wait_test(
     int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t batch, int32_t num_qo_heads,
     int32_t num_kv_heads, int32_t head_dim, int32_t num_pages, float sm_scale, void *out,
     float *lse, int32_t *dev_error, void *stream);
+
+/*
+ * Speculative step.  A sequence's drafted tree has n nodes: node 0 is its
+ * last committed token, node i > 0 hangs on node parents[i] < i.  The nodes
+ * take the last n cached positions (base = seq_len - n, node i at base + i)
+ * and rows qo_indptr[b] .. qo_indptr[b+1] - 1 of every ragged array; rows
+ * beyond qo_indptr[batch] are neither read nor written.  A step:
+ * k16v8_rope_kv_append writes the nodes (positions base + depth, slots of
+ * base + i), k16v8_paged_tree_attention attends, k16v8_tree_verify picks the
+ * accepted path and the next token, k16v8_kv_compact moves the accepted rows
+ * to base, base + 1, ....  No counterpart on the page; the cache format and
+ * the geometry are its intro's.
+ */
+
+/*
+ * rope_kv_append -- rotary positions fused with k16v8_kv_append.
+ *
+ * Pair i (0 <= i < rotary_dim/2) of a head x at position p is turned by the
+ * angle p * inv_freq[i] (formed beyond fp32, so far positions keep their
+ * angle); with c = attn_factor * cos, s = attn_factor * sin:
+ *   a' = a c - b s,  b' = b c + a s
+ *   interleaved = 0: a = x[i], b = x[i + rotary_dim/2]   (half layout)
+ *   interleaved = 1: a = x[2i], b = x[2i + 1]
+ * Dims rotary_dim .. head_dim - 1 pass through.  For every token t with slot
+ * s = slot_mapping[t] >= 0:
+ *   q_out[t][h][:] = fp16(rotated q[t][h])          every query head
+ *   k_cache[s/16][h][s%16][:] = fp16(rotated k[t][h])
+ *   v_cache[s/16][h][s%16][:] = E4M3_rn_satfinite(fl32(v[t][h][:]) / v_scale[h])
+ * (one rounding from fp32 each; a value beyond fp16's range becomes inf).  A
+ * token with a negative slot is padding: nothing of it is read or written.  A
+ * slot at or above num_pages*16 flags K16V8_DEVERR_SLOT, a position outside
+ * [0, 2^24) K16V8_DEVERR_POSITION, and the token is skipped.  Duplicate slots
+ * in one call leave an unspecified one of the writers.
+ *
+ *   q, k, v       device, [num_tokens][heads][head_dim] of x_dtype (fp16,
+ *                 fp32 or bf16), token strides in elements (0 = dense), e.g.
+ *                 slices of one fused projection
+ *   positions     device int32 [num_tokens]
+ *   inv_freq      device fp32 [rotary_dim/2], already scaled for long contexts
+ *   rotary_dim    a multiple of 16 in [16, head_dim]
+ *   attn_factor   finite; 1 without scaling
+ *   q_out         device fp16 [num_tokens][num_qo_heads][head_dim]; may be q
+ *                 itself when q is dense fp16.  num_qo_heads = 0: keys and
+ *                 values only (q, q_out NULL)
+ * q, k, v, q_out, caches: 16-byte aligned; token strides multiples of 16 bytes.
+ */
+int32_t k16v8_rope_kv_append(const void *q, int64_t q_token_stride, const void *k,
+                             int64_t k_token_stride, const void *v, int64_t v_token_stride,
+                             int32_t x_dtype, const int32_t *positions, const float *inv_freq,
+                             int32_t rotary_dim, int32_t interleaved, float attn_factor,
+                             const int64_t *slot_mapping, int32_t num_tokens,
+                             const float *v_scale, void *q_out, void *k_cache, uint8_t *v_cache,
+                             int32_t num_pages, int32_t num_qo_heads, int32_t num_kv_heads,
+                             int32_t head_dim, int32_t *dev_error, void *stream);
+
+/*
+ * paged_tree_attention -- attention of every node of every tree over the
+ * paged cache, which must already hold the nodes.  Node i of sequence b sees
+ * the positions below base and position base + j exactly when bit j of
+ * tree_mask[qo_indptr[b] + i] is set (bits >= n are ignored; set a node's own
+ * bit for it to see itself, an ancestor's for each of its ancestors).  Over
+ * what it sees, with s_j = sm_scale * q.k_j and v_j = v_scale[h/4] * e4m3(v8_j):
+ *   lse = ln sum exp(s_j),  out = sum exp(s_j - lse) v_j
+ * A row that sees nothing gives out = 0, lse = -inf.  What is stored at a
+ * position that a row does not see (NaN, inf) does not reach that row.
+ *
+ *   q            device fp16 [total_q][num_qo_heads][head_dim], 16-B aligned
+ *   qo_indptr    device int32 [batch+1]
+ *   max_nodes    host hint: the largest tree, <= K16V8_MAX_TREE_NODES
+ *   tree_mask    device uint64 [total_q]
+ *   seq_lens     device int32 [batch], the nodes included, <= max_seq_len
+ *   workspace    device, 256-B aligned, k16v8_tree_workspace_size(...) bytes
+ *                for the same arguments on the same device (0: NULL allowed);
+ *                needs no initialisation.  Calls that overlap on the GPU must
+ *                not share one.
+ *   out, lse     as for k16v8_paged_prefill_attention (lse may be NULL)
+ * A sequence with rows outside [0, total_q), n > max_nodes, n > seq_len or
+ * seq_len > max_seq_len flags K16V8_DEVERR_SEQLEN and is skipped; a page id
+ * outside the pool flags K16V8_DEVERR_PAGE and its positions are seen by no
+ * row.
+ */
+size_t k16v8_tree_workspace_size(int32_t total_q, int32_t batch, int32_t max_nodes,
+                                 int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+                                 int32_t max_seq_len);
+
+int32_t k16v8_paged_tree_attention(const void *q, const int32_t *qo_indptr, int32_t total_q,
+                                   int32_t max_nodes, const uint64_t *tree_mask,
+                                   const void *k_cache, const uint8_t *v_cache,
+                                   const float *v_scale, const int32_t *block_table,
+                                   int32_t max_pages_per_seq, const int32_t *seq_lens,
+                                   int32_t max_seq_len, int32_t batch, int32_t num_qo_heads,
+                                   int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+                                   float sm_scale, void *workspace, size_t workspace_bytes,
+                                   void *out, float *lse, int32_t *dev_error, void *stream);
+
+/*
+ * tree_verify -- which nodes the target accepts (rejection sampling that
+ * leaves the target's distribution unchanged) and the token after them.
+ *
+ * Row i of target_probs is the target's distribution of the token after node
+ * i, row i of draft_probs the distribution from which node i's children were
+ * drawn independently (NULL: children that were not sampled).  The walk starts
+ * at node 0 with weights r = target_probs[0], Z = 1.  The children c of the
+ * current node are tried in index order, x = tokens[c]:
+ *   draft_probs given: accepted when u[c] * q[x] * Z < r[x]; else
+ *                      r <- max(r - Z q, 0), Z <- sum r
+ *   draft_probs NULL:  accepted when u[c] * Z < r[x]; else r[x] <- 0, Z <- sum r
+ * An accepted child becomes the current node (r its row, Z = 1).  Where no
+ * child is left, next_token is the smallest j with r_0 + ... + r_j > u[0] * sum r.
+ * Should r have no weight left, the node's own row is used; a row without any
+ * weight gives -1.  Weights are summed exactly in units of 2^-60, so the
+ * results do not depend on how the work is split.
+ *
+ *   target_probs, draft_probs  device fp32 [total_q][vocab_size], row strides
+ *                 in elements (0 = vocab_size); values in [0, 1] (others are
+ *                 clamped, NaN counts as 0), rows that sum to about 1
+ *   tokens        device int32 [total_q] (node 0's is not read)
+ *   parents       device int32 [total_q], indices within the tree (node 0's is
+ *                 not read)
+ *   uniforms      device fp32 [total_q] in [0, 1): u above
+ *   path          device int32 [batch][max_nodes]: the accepted nodes, 0 first,
+ *                 then -1
+ *   path_len      device int32 [batch] (0: no tree)
+ *   next_token    device int32 [batch] (-1: no tree)
+ * A node whose parent is not an earlier node of its tree, or whose token is
+ * outside [0, vocab_size), flags K16V8_DEVERR_TREE and is never reached; rows
+ * outside [0, total_q) or n > max_nodes flag K16V8_DEVERR_SEQLEN and give
+ * path_len 0.
+ */
+int32_t k16v8_tree_verify(const float *target_probs, int64_t target_row_stride,
+                          const float *draft_probs, int64_t draft_row_stride,
+                          const int32_t *tokens, const int32_t *parents,
+                          const int32_t *qo_indptr, int32_t total_q, int32_t max_nodes,
+                          const float *uniforms, int32_t vocab_size, int32_t batch,
+                          int32_t *path, int32_t *path_len, int32_t *next_token,
+                          int32_t *dev_error, void *stream);
+
+/*
+ * kv_compact -- after verification: cache row base + path[b][j] moves to
+ * base + j for every j < path_len[b], every KV head and every layer, in one
+ * launch; new_seq_lens[b] = base + path_len[b].  Other rows keep their bytes
+ * (those of rejected nodes among them).
+ *
+ *   k_caches, v_caches  device arrays of num_layers device addresses, the
+ *                 layers' caches (distinct buffers of num_pages pages that
+ *                 share the block table)
+ *   seq_lens      device int32 [batch], the nodes included
+ *   qo_indptr     device int32 [batch+1]: n = qo_indptr[b+1] - qo_indptr[b]
+ *   path          device int32 [batch][max_nodes], strictly increasing
+ *   new_seq_lens  device int32 [batch] or NULL; not seq_lens itself
+ * A path that does not increase strictly within its tree flags
+ * K16V8_DEVERR_TREE, a sequence with n > seq_len, n > max_nodes or
+ * seq_len > 16*max_pages_per_seq K16V8_DEVERR_SEQLEN: nothing of it moves and
+ * its length stays.  A row whose page id is outside the pool is not moved
+ * (K16V8_DEVERR_PAGE).  num_layers = 0 or batch = 0: nothing is launched.
+ */
+int32_t k16v8_kv_compact(const uint64_t *k_caches, const uint64_t *v_caches, int32_t num_layers,
+                         const int32_t *block_table, int32_t max_pages_per_seq,
+                         const int32_t *seq_lens, const int32_t *qo_indptr, const int32_t *path,
+                         int32_t max_nodes, const int32_t *path_len, int32_t batch,
+                         int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+                         int32_t *new_seq_lens, int32_t *dev_error, void *stream);
 
 /*
  * Wait for `stream`, then copy the device error word to *host_value and
