@@ -89,10 +89,10 @@ __device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
 // cos and sin of position * freq, times factor.
 __device__ __forceinline__ float2 turn(int32_t position, float freq, float factor) {
   const float p = static_cast<float>(position);
-  const float rh = freq * kInv2PiHi;
-  const float rl = fmaf(freq, kInv2PiHi, -rh) + freq * kInv2PiLo;
-  const float th = p * rh;
-  const float tl = fmaf(p, rh, -th) + p * rl;
+  const float rh = __fmul_rn(freq, kInv2PiHi);  // products that are not to be contracted
+  const float rl = fmaf(freq, kInv2PiLo, fmaf(freq, kInv2PiHi, -rh));
+  const float th = __fmul_rn(p, rh);
+  const float tl = fmaf(p, rl, fmaf(p, rh, -th));
   const float frac = (th - rintf(th)) + tl;
   float s, c;
   sincospif(2.f * frac, &s, &c);

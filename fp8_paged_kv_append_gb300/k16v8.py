@@ -152,8 +152,8 @@ def _ptr(t):
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: building the Stream object costs 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -161,6 +161,10 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
         raise ValueError(f"{name} must be [tokens, heads, head_dim] with dense rows")
     return t.stride(0)
+
+
+_F16, _F32, _U8, _I32, _I64 = (torch.float16, torch.float32, torch.uint8, torch.int32,
+                                torch.int64)
 
 
 def _device(t: torch.Tensor) -> int:
@@ -173,27 +177,29 @@ def _device(t: torch.Tensor) -> int:
 
 def _dense(t, name: str, dtype, shape, dev: int) -> int:
     """Address of a dense tensor of this type and shape on device dev."""
-    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
-            or t.get_device() != dev):
-        raise ValueError(f"{name} must be a dense {dtype} tensor of shape {tuple(shape)} on "
-                         f"cuda:{dev}, got {t.dtype} {tuple(t.shape)}"
-                         f"{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a dense {dtype} tensor of shape {tuple(shape)} on "
+                     f"cuda:{dev}, got {t.dtype} {tuple(t.shape)}"
+                     f"{'' if t.is_contiguous() else ' (strided)'} on {t.device}")
 
 
-def _rows(t, name: str, dtype, shape, dev: int):
-    """Address and token stride of [tokens, heads, head_dim] with dense rows
-    (a slice of a wider row is fine)."""
-    if (t.dtype is not dtype or t.shape != shape or t.get_device() != dev
-            or t.stride(2) != 1 or t.stride(1) != shape[2]
-            or (shape[0] > 1 and t.stride(0) < shape[1] * shape[2])):
-        raise ValueError(f"{name} must be {dtype} {tuple(shape)} with dense rows on cuda:{dev}, got "
-                         f"{t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+def _rows(t, name: str, dtype, shape, dev: int) -> int:
+    """Token stride of [tokens, heads, head_dim] with dense rows (a slice of a
+    wider row is fine), 0 for a single token."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+        ts, hs, ds = t.stride()
+        if ds == 1 and (hs == shape[2] or shape[1] == 1):
+            if shape[0] <= 1:
+                return 0
+            if ts >= shape[1] * shape[2]:
+                return ts
+    raise ValueError(f"{name} must be {dtype} {tuple(shape)} with dense rows on cuda:{dev}, got "
+                     f"{t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
 
 
 def _error_word(dev_error, dev: int):
-    return None if dev_error is None else _dense(dev_error, "dev_error", torch.int32, (1,), dev)
+    return None if dev_error is None else _dense(dev_error, "dev_error", _I32, (1,), dev)
 
 
 # ---- kv_append ---------------------------------------------------------------
@@ -510,20 +516,24 @@ def k16v8_rope_kv_append(q, k, v, positions, inv_freq, slot_mapping, v_scale, q_
     if dt not in _X_DTYPES:
         raise ValueError(f"k must be fp16, fp32 or bf16, got {dt}")
     hq = 0 if q is None else q.shape[1]
-    q_ptr, q_ts = (None, 0) if q is None else _rows(q, "q", dt, (T, hq, d), dev)
-    k_ptr, k_ts = _rows(k, "k", dt, (T, hkv, d), dev)
-    v_ptr, v_ts = _rows(v, "v", dt, (T, hkv, d), dev)
+    if q is None:
+        q_ptr, q_ts, out_ptr = None, 0, None
+    else:
+        q_ptr, q_ts = q.data_ptr(), _rows(q, "q", dt, (T, hq, d), dev)
+        out_ptr = _dense(q_out, "q_out", _F16, (T, hq, d), dev)
+    row, tokens = (T, hkv, d), (T,)
     cache = (k_cache.shape[0], hkv, PAGE_SIZE, d)
+    half = inv_freq.numel()
     st = load_library().k16v8_rope_kv_append(
-        q_ptr, q_ts, k_ptr, k_ts, v_ptr, v_ts, _X_DTYPES[dt],
-        _dense(positions, "positions", torch.int32, (T,), dev),
-        _dense(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), dev),
-        2 * inv_freq.numel(), 1 if interleaved else 0, attn_factor,
-        _dense(slot_mapping, "slot_mapping", torch.int64, (T,), dev), T,
-        _dense(v_scale, "v_scale", torch.float32, (hkv,), dev),
-        None if q is None else _dense(q_out, "q_out", torch.float16, (T, hq, d), dev),
-        _dense(k_cache, "k_cache", torch.float16, cache, dev),
-        _dense(v_cache, "v_cache", torch.uint8, cache, dev), cache[0], hq, hkv, d,
+        q_ptr, q_ts, k.data_ptr(), _rows(k, "k", dt, row, dev), v.data_ptr(),
+        _rows(v, "v", dt, row, dev), _X_DTYPES[dt],
+        _dense(positions, "positions", _I32, tokens, dev),
+        _dense(inv_freq, "inv_freq", _F32, (half,), dev), 2 * half, 1 if interleaved else 0,
+        attn_factor, _dense(slot_mapping, "slot_mapping", _I64, tokens, dev), T,
+        _dense(v_scale, "v_scale", _F32, (hkv,), dev),
+        out_ptr,
+        _dense(k_cache, "k_cache", _F16, cache, dev),
+        _dense(v_cache, "v_cache", _U8, cache, dev), cache[0], hq, hkv, d,
         _error_word(dev_error, dev), _stream(stream))
     _check("k16v8_rope_kv_append", st)
 
@@ -555,18 +565,31 @@ def k16v8_paged_tree_attention(q, qo_indptr, max_nodes, tree_mask, k_cache, v_ca
         ws_bytes = workspace.numel() * workspace.element_size()
         ws = _dense(workspace, "workspace", workspace.dtype, workspace.shape, dev)
     st = load_library().k16v8_paged_tree_attention(
-        _dense(q, "q", torch.float16, (total_q, hq, d), dev),
-        _dense(qo_indptr, "qo_indptr", torch.int32, (B + 1,), dev), total_q, max_nodes,
-        _dense(tree_mask, "tree_mask", torch.int64, (total_q,), dev),
-        _dense(k_cache, "k_cache", torch.float16, cache, dev),
-        _dense(v_cache, "v_cache", torch.uint8, cache, dev),
-        _dense(v_scale, "v_scale", torch.float32, (hkv,), dev),
-        _dense(block_table, "block_table", torch.int32, (B, maxp), dev), maxp,
-        _dense(seq_lens, "seq_lens", torch.int32, (B,), dev), max_seq_len, B, hq, hkv, d, P,
-        sm_scale, ws, ws_bytes, _dense(out, "out", torch.float16, (total_q, hq, d), dev),
-        None if lse is None else _dense(lse, "lse", torch.float32, (total_q, hq), dev),
+        _dense(q, "q", _F16, (total_q, hq, d), dev),
+        _dense(qo_indptr, "qo_indptr", _I32, (B + 1,), dev), total_q, max_nodes,
+        _dense(tree_mask, "tree_mask", _I64, (total_q,), dev),
+        _dense(k_cache, "k_cache", _F16, cache, dev),
+        _dense(v_cache, "v_cache", _U8, cache, dev),
+        _dense(v_scale, "v_scale", _F32, (hkv,), dev),
+        _dense(block_table, "block_table", _I32, (B, maxp), dev), maxp,
+        _dense(seq_lens, "seq_lens", _I32, (B,), dev), max_seq_len, B, hq, hkv, d, P,
+        sm_scale, ws, ws_bytes, _dense(out, "out", _F16, (total_q, hq, d), dev),
+        None if lse is None else _dense(lse, "lse", _F32, (total_q, hq), dev),
         _error_word(dev_error, dev), _stream(stream))
     _check("k16v8_paged_tree_attention", st)
+
+
+def _prob_rows(t, name: str, shape, dev: int) -> int:
+    """Row stride of fp32 [total_q, V] with dense rows, 0 for a single row."""
+    if t.dtype is _F32 and t.shape == shape and t.get_device() == dev:
+        rs, cs = t.stride()
+        if cs == 1 or shape[1] == 1:
+            if shape[0] <= 1:
+                return 0
+            if rs >= shape[1]:
+                return rs
+    raise ValueError(f"{name} must be float32 {tuple(shape)} with dense rows on cuda:{dev}, got "
+                     f"{t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
 
 
 def k16v8_tree_verify(target_probs, draft_probs, tokens, parents, qo_indptr, max_nodes, uniforms,
@@ -579,25 +602,18 @@ def k16v8_tree_verify(target_probs, draft_probs, tokens, parents, qo_indptr, max
     total_q, V = target_probs.shape
     dev = _device(target_probs)
     B = path_len.shape[0]
-    strides = []
-    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
-        if t is None:
-            strides.append(0)
-            continue
-        if (t.dtype is not torch.float32 or t.shape != (total_q, V) or t.get_device() != dev
-                or (V > 1 and t.stride(1) != 1) or (total_q > 1 and t.stride(0) < V)):
-            raise ValueError(f"{name} must be float32 {(total_q, V)} with dense rows on cuda:{dev}, "
-                             f"got {t.dtype} {tuple(t.shape)}, strides {t.stride()} on {t.device}")
-        strides.append(t.stride(0) if total_q > 1 else 0)
+    shape, rows, seqs = (total_q, V), (total_q,), (B,)
     st = load_library().k16v8_tree_verify(
-        target_probs.data_ptr(), strides[0], _ptr(draft_probs), strides[1],
-        _dense(tokens, "tokens", torch.int32, (total_q,), dev),
-        _dense(parents, "parents", torch.int32, (total_q,), dev),
-        _dense(qo_indptr, "qo_indptr", torch.int32, (B + 1,), dev), total_q, max_nodes,
-        _dense(uniforms, "uniforms", torch.float32, (total_q,), dev), V, B,
-        _dense(path, "path", torch.int32, (B, max_nodes), dev),
-        _dense(path_len, "path_len", torch.int32, (B,), dev),
-        _dense(next_token, "next_token", torch.int32, (B,), dev), _error_word(dev_error, dev),
+        target_probs.data_ptr(), _prob_rows(target_probs, "target_probs", shape, dev),
+        None if draft_probs is None else draft_probs.data_ptr(),
+        0 if draft_probs is None else _prob_rows(draft_probs, "draft_probs", shape, dev),
+        _dense(tokens, "tokens", _I32, rows, dev),
+        _dense(parents, "parents", _I32, rows, dev),
+        _dense(qo_indptr, "qo_indptr", _I32, (B + 1,), dev), total_q, max_nodes,
+        _dense(uniforms, "uniforms", _F32, rows, dev), V, B,
+        _dense(path, "path", _I32, (B, max_nodes), dev),
+        _dense(path_len, "path_len", _I32, seqs, dev),
+        _dense(next_token, "next_token", _I32, seqs, dev), _error_word(dev_error, dev),
         _stream(stream))
     _check("k16v8_tree_verify", st)
 
@@ -621,15 +637,15 @@ def k16v8_kv_compact(k_ptrs, v_ptrs, num_pages, num_kv_heads, head_dim, block_ta
     B, max_nodes = path.shape
     maxp = block_table.shape[1]
     st = load_library().k16v8_kv_compact(
-        _dense(k_ptrs, "k_ptrs", torch.int64, (layers,), dev),
-        _dense(v_ptrs, "v_ptrs", torch.int64, (layers,), dev), layers,
-        _dense(block_table, "block_table", torch.int32, (B, maxp), dev), maxp,
-        _dense(seq_lens, "seq_lens", torch.int32, (B,), dev),
-        _dense(qo_indptr, "qo_indptr", torch.int32, (B + 1,), dev),
-        _dense(path, "path", torch.int32, (B, max_nodes), dev), max_nodes,
-        _dense(path_len, "path_len", torch.int32, (B,), dev), B, num_kv_heads, head_dim,
+        _dense(k_ptrs, "k_ptrs", _I64, (layers,), dev),
+        _dense(v_ptrs, "v_ptrs", _I64, (layers,), dev), layers,
+        _dense(block_table, "block_table", _I32, (B, maxp), dev), maxp,
+        _dense(seq_lens, "seq_lens", _I32, (B,), dev),
+        _dense(qo_indptr, "qo_indptr", _I32, (B + 1,), dev),
+        _dense(path, "path", _I32, (B, max_nodes), dev), max_nodes,
+        _dense(path_len, "path_len", _I32, (B,), dev), B, num_kv_heads, head_dim,
         num_pages,
-        None if new_seq_lens is None else _dense(new_seq_lens, "new_seq_lens", torch.int32, (B,),
+        None if new_seq_lens is None else _dense(new_seq_lens, "new_seq_lens", _I32, (B,),
                                                  dev),
         _error_word(dev_error, dev), _stream(stream))
     _check("k16v8_kv_compact", st)

@@ -51,7 +51,7 @@ extern "C" {
 #define K16V8_GQA_GROUP 4
 #define K16V8_MAX_SPLIT_CHUNK 8192
 #define K16V8_MAX_TREE_NODES 64   /* nodes of one sequence's drafted tree */
-#define K16V8_MAX_VOCAB (1 << 24) /* probabilities per row of tree_verify */
+#define K16V8_MAX_VOCAB (1 << 19) /* probabilities per row of tree_verify */
 
 typedef enum {
     K16V8_OK = 0,
@@ -623,8 +623,8 @@ int32_t k16v8_paged_tree_attention(const void *q, const int32_t *qo_indptr, int3
  * An accepted child becomes the current node (r its row, Z = 1).  Where no
  * child is left, next_token is the smallest j with r_0 + ... + r_j > u[0] * sum r.
  * Should r have no weight left, the node's own row is used; a row without any
- * weight gives -1.  Weights are summed exactly in units of 2^-60, so the
- * results do not depend on how the work is split.
+ * weight gives -1.  Weights are rounded to units of 2^-44 and summed exactly, so
+ * the results do not depend on how the work is split.
  *
  *   target_probs, draft_probs  device fp32 [total_q][vocab_size], row strides
  *                 in elements (0 = vocab_size); values in [0, 1] (others are

@@ -1,6 +1,6 @@
 """Verification of drafted trees against the definition in exact arithmetic
 (fractions of the fp32 inputs), so accepted paths and next tokens have to be
-equal: the kernel counts weights in units of 2^-60, and a drawn number that
+equal: the kernel counts weights in units of 2^-44, and a drawn number that
 falls between two running sums closer than that is not met by these seeds."""
 from fractions import Fraction
 
@@ -266,3 +266,22 @@ def test_binding_refuses_wrong_tensors(K):
                     ("next_token", nxt[:1])):
         with pytest.raises(ValueError):
             K.k16v8_tree_verify(**{**good, name: t})
+
+
+@pytest.mark.parametrize("V", [3, 129, 1023, 20001])
+def test_rows_off_the_16_byte_grid(K, V):
+    """Strides and starts that put the rows of p and q on different boundaries."""
+    p, q, tokens, parents, indptr, u = make(V, [6, 3, 5], V, 3, near=0.8)
+    want = run(K, p, q, tokens, parents, indptr, u, 6)
+    for sp, op, sq, oq in ((1, 0, 2, 0), (0, 1, 0, 1), (3, 2, 1, 3), (0, 0, 0, 2)):
+        def put(a, stride, off):
+            flat = torch.full((a.shape[0] * (V + stride) + off + 8,), 0.5, device=dev())
+            view = flat[off:off + a.shape[0] * (V + stride)].view(a.shape[0], V + stride)[:, :V]
+            view.copy_(to_dev(a))
+            return view
+        path = torch.zeros((3, 6), dtype=torch.int32, device=dev())
+        plen, nxt = (torch.zeros(3, dtype=torch.int32, device=dev()) for _ in range(2))
+        K.k16v8_tree_verify(put(p, sp, op), put(q, sq, oq), to_dev(tokens), to_dev(parents),
+                            to_dev(indptr), 6, to_dev(u), path, plen, nxt)
+        for x, y in zip((path, plen, nxt), want):
+            assert np.array_equal(x.cpu().numpy(), y)

@@ -78,7 +78,7 @@ def test_tree_workspace_size_is_zero_for_refused_shapes(lib):
 
 @pytest.mark.parametrize("change,status", [
     (dict(batch=-1), 1), (dict(total_q=-1), 1), (dict(max_nodes=-1), 1), (dict(vocab=0), 1),
-    (dict(max_nodes=65), 2), (dict(vocab=(1 << 24) + 1), 2), (dict(ts=99), 1), (dict(ds=99), 1),
+    (dict(max_nodes=65), 2), (dict(vocab=(1 << 19) + 1), 2), (dict(ts=99), 1), (dict(ds=99), 1),
     (dict(target=None), 1), (dict(tokens=None), 1), (dict(parents=None), 1),
     (dict(indptr=None), 1), (dict(u=None), 1), (dict(path=None), 1), (dict(path_len=None), 1),
     (dict(nxt=None), 1), (dict(target=A + 2), 1), (dict(draft=A + 2), 1), (dict(tokens=A + 2), 1),
