@@ -48,15 +48,14 @@
 #include <algorithm>
 #include <cmath>
 
-#include <cudaTypedefs.h>
-
 #include "k16v8_device.cuh"
 #include "tc_sm100.cuh"
+#include "tensor_map.cuh"
 
 namespace k16v8 {
 namespace prefill {
 
-constexpr int kQTok = 32;                   // query tokens per tile
+constexpr int kQTok = 32;                   // query tokens per tile (the TMA box of map_rows)
 constexpr int kRows = kQTok * kGroup;       // 128 MMA rows per tile
 constexpr int kKv = 128;                    // KV positions per tile
 constexpr int kPagesPerTile = kKv / kPage;  // 8
@@ -708,19 +707,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(
 
 // ---- host side ------------------------------------------------------------
 
-static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    cudaDriverEntryPointQueryResult q;
-    void *p = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }
-  return fn;
-}
-
 static int32_t set_smem_attr() {
   static bool configured[64] = {false};
   int dev = 0;
@@ -811,49 +797,10 @@ static int32_t prefill_launch(
   const uint64_t k_rows = static_cast<uint64_t>(num_pages) * num_kv_heads * kPage;
   if (k_rows >= (1ull << 31)) return K16V8_ERR_INVALID_ARG;
 
-  PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
-  if (!encode) return K16V8_ERR_CUDA;
-  CUtensorMap mq, mk;
-  {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim),
-                                static_cast<cuuint64_t>(num_qo_heads),
-                                static_cast<cuuint64_t>(total_q)};
-    const cuuint64_t strides[2] = {kHeadDim * 2ull,
-                                   static_cast<cuuint64_t>(num_qo_heads) * kHeadDim * 2ull};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kGroup), static_cast<cuuint32_t>(kQTok)};
-    const cuuint32_t es[3] = {1, 1, 1};
-    if (encode(&mq, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(q), dims, strides, box,
-               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return K16V8_ERR_CUDA;
-  }
-  {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kHeadDim), k_rows};
-    const cuuint64_t strides[1] = {kHeadDim * 2ull};
-    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(kPage)};
-    const cuuint32_t es[2] = {1, 1};
-    if (encode(&mk, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void *>(k_cache), dims,
-               strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return K16V8_ERR_CUDA;
-  }
-  CUtensorMap mo;  // the output, same geometry and box as the query
-  {
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim),
-                                static_cast<cuuint64_t>(num_qo_heads),
-                                static_cast<cuuint64_t>(total_q)};
-    const cuuint64_t strides[2] = {kHeadDim * 2ull,
-                                   static_cast<cuuint64_t>(num_qo_heads) * kHeadDim * 2ull};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kGroup), static_cast<cuuint32_t>(kQTok)};
-    const cuuint32_t es[3] = {1, 1, 1};
-    if (encode(&mo, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, out, dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return K16V8_ERR_CUDA;
-  }
+  CUtensorMap mq, mk, mo;  // the output has the query's geometry and box
+  if (!map_rows(&mq, q, num_qo_heads, total_q) || !map_keys(&mk, k_cache, k_rows) ||
+      !map_rows(&mo, out, num_qo_heads, total_q))
+    return K16V8_ERR_CUDA;
   int32_t st = set_smem_attr();
   if (st != K16V8_OK) return st;
   const PrefillWs w = prefill_ws(kv_splits, max_qlen, batch, num_kv_heads, max_seq_len);

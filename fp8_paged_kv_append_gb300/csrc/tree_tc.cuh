@@ -1,0 +1,734 @@
+// Tree attention on the tensor cores: the split kernel for trees of more than
+// a few nodes (see tree_attention.cu for the operator).
+//
+// One CTA per SM, all 512 columns of tensor memory.  The work is the flat
+// list of (sequence, KV head, 128-position tile), cut into one equal range
+// per CTA; a range holds whole segments ((sequence, KV head) pairs) and at
+// most two cut ones, whose rows go to the workspace for the merge.
+//
+// The 4 query heads of the GQA group times 32 nodes are the 128 rows of an
+// MMA tile (row = node * 4 + head).  Two score tiles S_0, S_1 and two output
+// tiles O_0, O_1 (128 columns each; P, fp16, over the first half of its S)
+// let one tile's softmax overlap the other's MMAs:
+//  * trees of up to 32 nodes: one row tile; KV tiles alternate between slots 0
+//    and 1, each with its own running max, sum and O, joined at the end of the
+//    piece.  K and V are read once and every MMA row block works on another
+//    KV tile;
+//  * wider trees: two row tiles, both over every KV tile.
+// A unit is one (KV tile, slot): S = Q K^T, softmax, O += P V.
+//
+// Warp roles (16 warps): 0-3 / 4-7 softmax of slot 0 / 1, one thread per row;
+// 8, 10, 11, 14 dequantise V (E4M3 pages -> fp16 MN-major half tiles); 9 issues
+// the MMAs; 13 loads Q and K pages (TMA); 12 loads the E4M3 pages (bulk
+// copies); 15 walks the CTA's pieces and hands them to the others.  Every
+// hand-off is an mbarrier, every wait is bounded.
+//
+// What it is built around (cycles at 1.96 GHz, from time stamps of one CTA; a
+// KV tile at the full memory rate takes 2,150):
+//  * The softmax loops are kept rolled up: each warp runs its role's code once
+//    per tile, and unrolled over the 128 columns that code came from the far
+//    side of the instruction cache (4,000 cycles a tile, against 2,100).
+//  * The whole MMA warp walks the units and one elected lane issues: operands
+//    stay in uniform registers (3,030 -> 1,900 cycles a unit).
+//  * A bulk or tensor copy takes its lane ~90 cycles to issue, so K and V have
+//    a warp each, and asking L2 for pages ahead of time costs more than it
+//    hides (143 against 131 us on 8 nodes at 128K).
+//  * A copy lands ~2,000-3,000 cycles after it is issued: three stages each
+//    (two of K for wide trees, whose tiles take longer).
+//  * A piece's description takes several memory round trips to work out: one
+//    warp does that ahead of time.
+#pragma once
+
+#include "k16v8_device.cuh"
+#include "tc_sm100.cuh"
+#include "tree_plan.cuh"
+
+namespace k16v8 {
+namespace tree {
+namespace tcore {
+
+constexpr int kNodes = 32;                   // nodes per row tile
+constexpr int kRows = kNodes * kGroup;       // 128
+constexpr int kKv = 128;                     // positions per KV tile
+constexpr int kPagesPerTile = kKv / kPage;   // 8
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 9, kLoadVWarp = 12, kLoadKWarp = 13, kPieceWarp = 15;
+constexpr int kDequantWarps = 4;
+constexpr int kDequantThreads = kDequantWarps * 32;
+constexpr int kPieceRing = 4;
+constexpr int kPieceReaders = 8 + kDequantWarps + 3;  // warps
+
+// 0xff in every byte of w that is an E4M3 NaN (0x7f or 0xff).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+// Rank of a dequant warp among them, or -1.
+__device__ __forceinline__ int dequant_rank(int warp) {
+  return warp == 8 ? 0 : warp == 10 ? 1 : warp == 11 ? 2 : warp == 14 ? 3 : -1;
+}
+
+constexpr uint32_t kQBytes = kRows * 256;
+constexpr uint32_t kKBlk = kKv * 128;          // [128 pos][64 dims] fp16
+constexpr uint32_t kKStage = 2 * kKBlk;
+constexpr uint32_t kVstStage = kKv * 128;      // [128 pos][128] E4M3
+constexpr int kVstStages = 3;
+constexpr int kHalf = kKv / 2;                 // positions of a V half tile
+constexpr uint32_t kVBlk = kHalf * 128;        // [64 pos][64 dims] fp16
+constexpr uint32_t kVHalf = 2 * kVBlk;
+constexpr int kVHalves = 3;
+constexpr uint32_t kTmemCols = 512;  // S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512)
+
+// kWide: trees of more than 32 nodes may be among the batch.
+template <bool kWide>
+struct Smem {
+  static constexpr int kQSlots = kWide ? 2 : 1;
+  static constexpr int kKStages = kWide ? 2 : 3;
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + kQSlots * kQBytes;
+  static constexpr uint32_t kVst = kK + kKStages * kKStage;
+  static constexpr uint32_t kV = kVst + kVstStages * kVstStage;
+  static constexpr uint32_t kBar = kV + kVHalves * kVHalf;
+  static constexpr uint32_t kPieces = kBar + 384;
+  static constexpr uint32_t kInfo = kPieces + kPieceRing * sizeof(Piece);
+  static constexpr uint32_t kNan = kInfo + 16 * 4;   // tree nodes with NaN value codes
+  static constexpr uint32_t kStat = kNan + 4 * 8;    // [slot][max, sum][row]
+  static constexpr uint32_t kBytes = kStat + 2 * 2 * kRows * 4;
+  static_assert(kBytes <= 227 * 1024, "one CTA's shared memory");
+  static_assert(sizeof(int64_t) * (kMaxBatch + 1) <= kBar, "the scan's scratch");
+  static_assert(kInfo % 8 == 0 && kNan % 8 == 0 && kStat % 16 == 0, "alignment");
+};
+static_assert(sizeof(int64_t) * 33 <= 384, "the scan's warp sums, before the barriers live");
+
+enum {
+  kBarQFull = 0,      // +slot
+  kBarQEmpty = 2,     // +slot
+  kBarKFull = 4,      // +stage
+  kBarKEmpty = 7,     // +stage
+  kBarVstFull = 10,   // +stage
+  kBarVstEmpty = 13,  // +stage, kDequantThreads arrivals
+  kBarVFull = 16,     // +half, kDequantThreads arrivals
+  kBarVEmpty = 19,    // +half
+  kBarSFull = 22,     // +slot
+  kBarPFull = 24,     // +slot, 128 arrivals
+  kBarODone = 26,     // +slot
+  kBarOEmpty = 28,    // 8 arrivals: both O tiles have been read
+  kBarJoin = 29,      // 256 arrivals: both slots' statistics are in shared memory
+  kBarPiece = 30,     // +ring entry: described
+  kBarTaken = 34,     // +ring entry: kPieceReaders arrivals
+  kBarDrain = 38,
+  kNumBars = 39
+};
+static_assert(kNumBars * 8 + 16 <= 384, "barriers");
+
+// Position in a ring of n stages: the stage, and the parity of its phase.
+template <int n>
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  bool wrapped = false;  // every stage has been used once
+  __device__ __forceinline__ void next() {
+    if (++s == n) {
+      s = 0;
+      phase ^= 1;
+      wrapped = true;
+    }
+  }
+};
+
+// As in prefill: a wait that runs out raises the CTA-wide abort flag, which
+// the suspending waits poll; every role leaves its loops on a failed wait.
+__device__ __forceinline__ bool cta_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                         int32_t *dev_error, bool spin = false) {
+  if (*abort_flag) return false;
+  if (spin) {
+    if (mbar_spin_bounded(bar, parity)) return true;
+  } else {
+    for (uint32_t i = 0; i < kMaxPolls; ++i) {
+      if (mbar_try_wait(bar, parity)) return true;
+      if ((i & 1023u) == 1023u && *abort_flag) return false;
+    }
+  }
+  *abort_flag = 1;
+  flag_error(dev_error, K16V8_DEVERR_TIMEOUT);
+  return false;
+}
+
+// Visible columns 32c .. 32c + 31 of a tile whose first position is base - d,
+// for a row with tree mask m (bits below n only): bits of the word.
+__device__ __forceinline__ uint32_t visible(int c, int d, uint64_t m) {
+  const int rel = 32 * c - d;  // position of the word's first column behind base
+  if (rel <= -32) return 0xffffffffu;
+  if (rel >= 64) return 0u;
+  if (rel < 0) return ((1u << -rel) - 1u) | static_cast<uint32_t>(m << -rel);
+  return static_cast<uint32_t>(m >> rel);
+}
+
+// Page id of page `lane` of a piece's tile t: -1 outside the pool, -2 behind
+// the last position (and for lanes without a page).
+__device__ __forceinline__ int page_id(const Args &a, const Piece &p, int t, int lane) {
+  const int page = t * kPagesPerTile + lane;
+  if (lane >= kPagesPerTile || page * kPage >= p.L) return -2;
+  const int pid = __ldg(a.block_table + static_cast<int64_t>(p.b) * a.maxp + page);
+  return pid >= 0 && pid < a.num_pages ? pid : -1;
+}
+
+template <bool kWide>
+__global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
+    const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+    const Args a) {
+  using M = Smem<kWide>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *sQ = smem_raw + M::kQ;
+  uint8_t *sK = smem_raw + M::kK;
+  uint8_t *sVst = smem_raw + M::kVst;
+  uint8_t *sV = smem_raw + M::kV;
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + M::kBar);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kNumBars) + 1;
+  Piece *pieces = reinterpret_cast<Piece *>(smem_raw + M::kPieces);
+  // rejected pages of a tile: for the softmax (by tile, 8 of them) and for the
+  // dequantisation (by stage)
+  volatile uint32_t *info = reinterpret_cast<volatile uint32_t *>(smem_raw + M::kInfo);
+  volatile uint32_t *info_v = info + 8;
+  uint32_t *nan_nodes = reinterpret_cast<uint32_t *>(smem_raw + M::kNan);  // [4][2], by piece
+  float *stat = reinterpret_cast<float *>(smem_raw + M::kStat);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hq = a.hkv * kGroup;
+  pdl_wait();
+  if (tid == kPieceWarp * 32) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (smem_addr(smem_raw) & 1023u) {
+    if (tid == 0) flag_error(a.dev_error, K16V8_DEVERR_INTERNAL);
+    return;
+  }
+  // ---- this CTA's range of the work (scratch: the operand stages) ----
+  constexpr Shape kShape{kKv, kNodes};
+  const Range range = plan_range(a, kShape, reinterpret_cast<int64_t *>(smem_raw),
+                                 reinterpret_cast<int64_t *>(smem_raw + M::kBar));
+  if (range.lo >= range.hi) return;  // uniform over the CTA
+
+  if (warp == kLoadKWarp && lane == 0) {
+    tc::prefetch_tensormap(&tmap_q);
+    tc::prefetch_tensormap(&tmap_k);
+  }
+  if (warp == 0) {
+    tc::tmem_alloc(tmem_slot, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int i = 0; i < kNumBars; ++i) {
+      uint32_t count = 1;
+      if (i >= kBarVstEmpty && i < kBarVEmpty) count = kDequantThreads;
+      if (i == kBarPFull || i == kBarPFull + 1) count = kRows;
+      if (i == kBarJoin) count = 2 * kRows;
+      if (i == kBarOEmpty) count = 8;
+      if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
+      mbar_init(&bars[i], count);
+    }
+    *abort_flag = 0;
+    for (int i = 0; i < 8; ++i) nan_nodes[i] = 0;
+    fence_barrier_init();
+  }
+  fence_proxy_async();  // the scan's scratch becomes operand stages
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  auto wait = [&](int bar, uint32_t parity, bool spin = false) {
+    return cta_wait(&bars[bar], parity, abort_flag, a.dev_error, spin);
+  };
+  // The next piece, for a whole warp; false at the end (or after an abort).
+  auto get_piece = [&](Piece &pc, Ring<kPieceRing> &r, bool spin = false) {
+    if (!__all_sync(kFull, wait(kBarPiece + r.s, r.phase, spin))) return false;
+    pc = pieces[r.s];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[kBarTaken + r.s]);
+    r.next();
+    return pc.tiles > 0;
+  };
+
+  if (warp < 8) {
+    // ================= softmax of slot w =================
+    const int w = warp >> 2;
+    const int r = tid & 127;
+    const float qk_scale = a.sm_scale * kLog2e;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + w * 128;
+    const uint32_t tO = tmem + 256 + w * 128;
+    const uint32_t tOther = tmem + 256 + (w ^ 1) * 128;
+    Piece pc;
+    Ring<kPieceRing> ring;
+    uint32_t units = 0, other = 0;  // of this slot and of the other one, so far
+    uint32_t tiles = 0;             // of the CTA so far
+    bool ok = true;
+    for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
+      const bool two = kWide && pc.n > kNodes;  // two row tiles
+      const int node = (two ? w * kNodes : 0) + (r >> 2);
+      const bool row_valid = node < pc.n;
+      const bool warp_live = (two ? w * kNodes : 0) + (warp & 3) * 8 < pc.n;
+      const uint64_t mask = row_valid ? __ldg(a.tree_mask + pc.q0 + node) & pc.node_bits() : 0;
+      const int mine = two ? pc.tiles : (pc.tiles + 1 - w) / 2;
+      const int theirs = two ? 0 : (pc.tiles + w) / 2;  // units of the other slot to join
+      float m_used = -INFINITY, l = 0.f;
+      for (int k = 0; k < mine; ++k, ++units) {
+        if (!__all_sync(kFull, wait(kBarSFull + w, units & 1))) {
+          ok = false;
+          break;
+        }
+        if (!warp_live) {
+          mbar_arrive(&bars[kBarPFull + w]);
+          continue;
+        }
+        tc::fence_after_sync();
+        const int tile = two ? k : 2 * k + w;
+        const int d = pc.base() - (pc.t0 + tile) * kKv;  // prefix columns of this tile
+        const uint32_t bad = info[(tiles + tile) & 7];
+        const bool need_mask = d < kKv || bad;
+        // columns 32c .. 32c + 31 that this row sees
+        auto seen = [&](int c) {
+          uint32_t v = visible(c, d, mask);
+          if (bad >> (2 * c) & 1) v &= 0xffff0000u;
+          if (bad >> (2 * c + 1) & 1) v &= 0x0000ffffu;
+          return v;
+        };
+        // pass 1: row max
+        float rmax = -INFINITY;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          uint32_t sr[2][32];
+          tc::tmem_ld32(tS + lane_base + h * 64, sr[0]);
+          tc::tmem_ld32(tS + lane_base + h * 64 + 32, sr[1]);
+          tc::tmem_wait_ld();
+          if (need_mask) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t v = seen(2 * h + c);
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (v >> e & 1) rmax = fmaxf(rmax, __uint_as_float(sr[c][e]));
+            }
+          } else {
+            float m4[4] = {rmax, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sr[c][e]));
+            rmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+          }
+        }
+        rmax *= qk_scale;
+        float alpha = 1.f;
+        if (rmax > m_used + 8.f) {
+          alpha = ex2(m_used - rmax);
+          m_used = rmax;
+        }
+        if (k > 0 && __any_sync(kFull, alpha != 1.f)) {
+          if (!__all_sync(kFull, wait(kBarODone + w, (units - 1) & 1))) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tc::tmem_ld32(tO + lane_base + c * 32, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st32(tO + lane_base + c * 32, o);
+          }
+        }
+        // pass 2: p = 2^(s * scale - m), fp32 row sum, P (fp16) over the S columns read
+        const float neg = m_used == -INFINITY ? 0.f : -m_used;
+        const float2 sc2 = make_float2(qk_scale, qk_scale);
+        const float2 nm2 = make_float2(neg, neg);
+        float2 ps2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t sr[32];
+          tc::tmem_ld32(tS + lane_base + c * 32, sr);
+          tc::tmem_wait_ld();
+          uint32_t pk[16];
+          const uint32_t v = need_mask ? seen(c) : kFull;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(
+                make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sc2, nm2);
+            float2 pp = make_float2(ex2(x.x), ex2(x.y));
+            if (need_mask) {
+              if (!(v >> (2 * e) & 1)) pp.x = 0.f;
+              if (!(v >> (2 * e + 1) & 1)) pp.y = 0.f;
+            }
+            ps2 = __fadd2_rn(ps2, pp);
+            const __half2 hh = __floats2half2_rn(pp.x, pp.y);
+            pk[e] = *reinterpret_cast<const uint32_t *>(&hh);
+          }
+          tc::tmem_st16(tS + lane_base + c * 16, pk);
+        }
+        tc::tmem_wait_st();
+        l = l * alpha + (ps2.x + ps2.y);
+        tc::fence_before_sync();
+        mbar_arrive(&bars[kBarPFull + w]);
+      }
+      if (!ok) break;
+      tiles += pc.tiles;
+      other += two ? pc.tiles : (pc.tiles + w) / 2;
+      // ---- end of the piece: this slot's O, and with one row tile the other's ----
+      if (mine > 0) ok = __all_sync(kFull, wait(kBarODone + w, (units - 1) & 1));
+      if (ok && theirs > 0) ok = __all_sync(kFull, wait(kBarODone + (w ^ 1), (other - 1) & 1));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const int pn = (p_idx & 3) * 2;
+      const uint64_t nan_mask = nan_nodes[pn] | static_cast<uint64_t>(nan_nodes[pn + 1]) << 32;
+      float f_own = 1.f, f_other = 0.f;
+      float m_all = m_used, l_all = l;
+      if (!two) {
+        stat[(w * 2 + 0) * kRows + r] = m_used;
+        stat[(w * 2 + 1) * kRows + r] = l;
+      }
+      mbar_arrive(&bars[kBarJoin]);
+      ok = __all_sync(kFull, wait(kBarJoin, p_idx & 1));
+      if (!ok) break;
+      if (tid < 2) nan_nodes[pn + tid] = 0;
+      if (!two) {
+        const float m_o = stat[((w ^ 1) * 2 + 0) * kRows + r];
+        const float l_o = stat[((w ^ 1) * 2 + 1) * kRows + r];
+        m_all = fmaxf(m_used, m_o);
+        // (a slot whose scores were all NaN keeps max -inf: its NaN sum decides)
+        f_own = m_used == -INFINITY ? (l != l ? l : 0.f) : ex2(m_used - m_all);
+        f_other = m_o == -INFINITY ? (l_o != l_o ? l_o : 0.f) : ex2(m_o - m_all);
+        l_all = f_own * l + f_other * l_o;
+      }
+      const bool dead = !(l_all > 0.f) && l_all == l_all;  // the row sees nothing
+      const float inv = dead ? 0.f : __ldg(a.v_scale + pc.g) / l_all;
+      const float lse = dead ? -INFINITY : (m_all + lg2(l_all)) * kLn2;
+      const float g_own = f_own * inv, g_other = f_other * inv;
+      // with one row tile, slot w's warps write dims 64w .. 64w + 63 of every row
+      const int c_lo = two ? 0 : 2 * w, c_hi = two ? 4 : 2 * w + 2;
+      const int row = (two ? w * kRows : 0) + r;  // of the segment
+      const int64_t orow = static_cast<int64_t>(pc.q0 + node) * hq + pc.g * kGroup + (r & 3);
+      if (warp_live) {
+#pragma unroll 1
+        for (int c = c_lo; c < c_hi; ++c) {
+          float o[32];
+          {
+            uint32_t x[32];
+            if (mine > 0) {
+              tc::tmem_ld32(tO + lane_base + c * 32, x);
+              tc::tmem_wait_ld();
+            }
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = mine > 0 ? __uint_as_float(x[e]) * g_own : 0.f;
+            if (theirs > 0) {
+              tc::tmem_ld32(tOther + lane_base + c * 32, x);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(x[e]), g_other, o[e]);
+            }
+          }
+          // NaN value codes of nodes this row sees
+          for (uint64_t nm = mask & nan_mask; nm; nm &= nm - 1) {
+            const int pos = pc.base() + __ffsll(static_cast<long long>(nm)) - 1;
+            const int page = __ldg(a.block_table + static_cast<int64_t>(pc.b) * a.maxp + pos / kPage);
+            if (page < 0 || page >= a.num_pages) continue;
+            const uint8_t *vr = a.v_cache + ((static_cast<int64_t>(page) * a.hkv + pc.g) * kPage +
+                                             pos % kPage) * kHeadDim + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if ((__ldg(vr + e) & 0x7f) == 0x7f) o[e] = NAN;
+          }
+          if (row_valid && pc.whole) {
+            uint4 *po = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __half2 hh = __floats2half2_rn(o[q * 8 + 2 * e], o[q * 8 + 2 * e + 1]);
+                pk[e] = *reinterpret_cast<const uint32_t *>(&hh);
+              }
+              po[q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+          } else if (row_valid) {
+            float4 *po = a.part_o + (static_cast<int64_t>(pc.slot) * 32 + c * 8) * a.max_rows + row;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              po[static_cast<int64_t>(q) * a.max_rows] =
+                  make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+        }
+        if (row_valid && (two || w == 0)) {
+          if (!pc.whole)
+            a.part_lse[static_cast<int64_t>(pc.slot) * a.max_rows + row] = lse;
+          else if (a.lse)
+            a.lse[orow] = lse;
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarOEmpty]);  // O is read: the next piece may write it
+    }
+    pdl_launch_dependents();
+  } else if (dequant_rank(warp) >= 0) {
+    // ================= V dequantisation =================
+    const int dt = dequant_rank(warp) * 32 + lane;
+    Piece pc;
+    Ring<kPieceRing> ring;
+    Ring<kVstStages> src;
+    Ring<kVHalves> dst;
+    bool ok = true;
+    for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
+      for (int t = pc.t0; ok && t < pc.t1; ++t) {
+        ok = wait(kBarVstFull + src.s, src.phase);
+        const int live = pc.L - t * kKv;       // positions of the tile in the sequence
+        const int tree0 = pc.base() - t * kKv;  // those from here on are nodes
+        const uint32_t bad = info_v[src.s];
+        const uint8_t *vst = sVst + src.s * kVstStage;
+#pragma unroll 1
+        for (int h = 0; ok && h < 2; ++h) {
+          if (dst.wrapped) ok = wait(kBarVEmpty + dst.s, dst.phase ^ 1);
+          if (!ok) break;
+          uint8_t *vdst = sV + dst.s * kVHalf;
+#pragma unroll
+          for (int i = 0; i < kHalf * 8 / kDequantThreads; ++i) {  // chunks of 16 E4M3 values
+            const int id = i * kDequantThreads + dt;
+            const int hp = id >> 3, c16 = id & 7, pos = h * kHalf + hp;
+            uint4 lo = make_uint4(0, 0, 0, 0), hi = make_uint4(0, 0, 0, 0);
+            if (pos < live && !(bad >> (pos >> 4) & 1)) {
+              uint4 raw = *reinterpret_cast<const uint4 *>(vst + pos * 128 + c16 * 16);
+              if (pos >= tree0) {  // a node: its NaN codes must not reach rows that do not see it
+                const uint32_t n0 = nan_bytes(raw.x), n1 = nan_bytes(raw.y), n2 = nan_bytes(raw.z),
+                               n3 = nan_bytes(raw.w);
+                if (n0 | n1 | n2 | n3) {
+                  raw = make_uint4(raw.x & ~n0, raw.y & ~n1, raw.z & ~n2, raw.w & ~n3);
+                  const int rel = pos - tree0;
+                  atomicOr(&nan_nodes[(p_idx & 3) * 2 + (rel >> 5)], 1u << (rel & 31));
+                }
+              }
+              const uint32_t wv[4] = {raw.x, raw.y, raw.z, raw.w};
+              uint32_t hv[8];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const __half2 u = e4m3x2_to_half2(static_cast<uint16_t>(wv[q] & 0xffffu));
+                const __half2 v = e4m3x2_to_half2(static_cast<uint16_t>(wv[q] >> 16));
+                hv[2 * q] = *reinterpret_cast<const uint32_t *>(&u);
+                hv[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&v);
+              }
+              lo = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+              hi = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+            }
+            const uint32_t off = hp * 128 + (c16 & 3) * 32;
+            uint8_t *blk = vdst + (c16 >> 2) * kVBlk;
+            *reinterpret_cast<uint4 *>(blk + tc::sw128(off)) = lo;
+            *reinterpret_cast<uint4 *>(blk + tc::sw128(off + 16)) = hi;
+          }
+          fence_proxy_async();
+          mbar_arrive(&bars[kBarVFull + dst.s]);
+          dst.next();
+        }
+        if (!ok) break;
+        mbar_arrive(&bars[kBarVstEmpty + src.s]);
+        src.next();
+      }
+    }
+  } else if (warp == kLoadVWarp) {
+    // ================= V loads =================
+    Piece pc;
+    Ring<kPieceRing> ring;
+    Ring<kVstStages> dst;
+    uint32_t issued = 0;
+    bool ok = true;
+    while (ok && get_piece(pc, ring)) {
+      int pid = page_id(a, pc, pc.t0, lane);
+      for (int t = pc.t0; t < pc.t1; ++t) {
+        if (dst.wrapped) ok = __all_sync(kFull, wait(kBarVstEmpty + dst.s, dst.phase ^ 1));
+        if (!ok) break;
+        const uint32_t bad = __ballot_sync(kFull, pid == -1);
+        const uint32_t bytes = __popc(__ballot_sync(kFull, pid >= 0)) * 2048u;
+        if (lane == 0) {
+          if (bad) flag_error(a.dev_error, K16V8_DEVERR_PAGE);
+          info_v[dst.s] = bad;
+          mbar_arrive_expect_tx(&bars[kBarVstFull + dst.s], bytes);
+        }
+        __syncwarp();
+        if (pid >= 0)
+          bulk_g2s(sVst + dst.s * kVstStage + lane * 2048,
+                   a.v_cache + (static_cast<int64_t>(pid) * a.hkv + pc.g) * kPage * kHeadDim, 2048,
+                   &bars[kBarVstFull + dst.s]);
+        if (t + 1 < pc.t1) pid = page_id(a, pc, t + 1, lane);
+        __syncwarp();
+        dst.next();
+        ++issued;
+      }
+    }
+    // let the copies issued last land before shared memory is released
+    if (lane == 0)
+      for (uint32_t i = issued < kVstStages ? 0 : issued - kVstStages; i < issued; ++i)
+        mbar_wait_bounded(&bars[kBarVstFull + i % kVstStages], (i / kVstStages) & 1);
+    __syncwarp();
+  } else if (warp == kLoadKWarp) {
+    // ================= Q and K loads =================
+    Piece pc;
+    Ring<kPieceRing> ring;
+    Ring<M::kKStages> dst;
+    uint32_t issued = 0, uses[2] = {0, 0};
+    bool ok = true;
+    for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
+      int pid = page_id(a, pc, pc.t0, lane);
+      for (int t = pc.t0; ok && t < pc.t1; ++t) {
+        if (dst.wrapped) ok = __all_sync(kFull, wait(kBarKEmpty + dst.s, dst.phase ^ 1));
+        if (!ok) break;
+        const uint32_t bad = __ballot_sync(kFull, pid == -1);
+        const uint32_t bytes = __popc(__ballot_sync(kFull, pid >= 0)) * 4096u;
+        if (lane == 0) {
+          info[issued & 7] = bad;
+          mbar_arrive_expect_tx(&bars[kBarKFull + dst.s], bytes);
+        }
+        __syncwarp();
+        if (pid >= 0) {
+          uint8_t *k_dst = sK + dst.s * kKStage + lane * 2048;
+          const int row = (pid * a.hkv + pc.g) * kPage;
+          tc::tma_load_2d(k_dst, &tmap_k, 0, row, &bars[kBarKFull + dst.s]);
+          tc::tma_load_2d(k_dst + kKBlk, &tmap_k, 64, row, &bars[kBarKFull + dst.s]);
+        }
+        if (t + 1 < pc.t1) pid = page_id(a, pc, t + 1, lane);
+        __syncwarp();
+        dst.next();
+        ++issued;
+        if (t == pc.t0) {  // the query, behind the first tile's copies
+          const bool two = kWide && pc.n > kNodes;
+          for (int i = 0; ok && i < (two ? 2 : 1); ++i) {
+            const int qs = two ? i : (kWide ? p_idx & 1 : 0);
+            if (uses[qs] > 0) ok = __all_sync(kFull, wait(kBarQEmpty + qs, (uses[qs] - 1) & 1));
+            if (!ok) break;
+            ++uses[qs];
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars[kBarQFull + qs], kQBytes);
+              for (int h = 0; h < 2; ++h)
+                tc::tma_load_3d(sQ + qs * kQBytes + h * (kQBytes / 2), &tmap_q, 64 * h,
+                                pc.g * kGroup, pc.q0 + (two ? i * kNodes : 0),
+                                &bars[kBarQFull + qs]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) {
+      constexpr uint32_t n = M::kKStages;
+      for (uint32_t i = issued < n ? 0 : issued - n; i < issued; ++i)
+        mbar_wait_bounded(&bars[kBarKFull + i % n], (i / n) & 1);
+      for (int s = 0; s < 2; ++s)
+        if (uses[s] > 0) mbar_wait_bounded(&bars[kBarQFull + s], (uses[s] - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ================= MMA issue =================
+    // The whole warp walks the units, so every operand stays uniform; one lane
+    // issues.
+    const bool leader = tc::elect_one();
+    constexpr uint32_t kIdescQK = tc::idesc_f16_f32(kRows, kKv, false, false);
+    constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kRows, kHeadDim, false, true);
+    const uint64_t dq = tc::smem_desc_sw128(smem_addr(sQ), 16, 1024);
+    const uint64_t dk = tc::smem_desc_sw128(smem_addr(sK), 16, 1024);
+    const uint64_t dv = tc::smem_desc_sw128(smem_addr(sV), kVBlk, 1024);
+    Piece pc;
+    Ring<kPieceRing> ring;
+    Ring<M::kKStages> kr;  // next K stage to use
+    Ring<kVHalves> vr;     // next V half to use
+    uint32_t uses[2] = {0, 0}, units[2] = {0, 0};
+    bool ok = true;
+    for (uint32_t p_idx = 0; ok && get_piece(pc, ring, true); ++p_idx) {
+      const bool two = kWide && pc.n > kNodes;
+      const int n_units = two ? 2 * pc.tiles : pc.tiles;
+      // S of unit u: slot u & 1, tile u (or u / 2); two units share a K stage
+      // when there are two row tiles
+      auto issue_s = [&](int u) {
+        const int w = u & 1;
+        if ((!two || w == 0) && !wait(kBarKFull + kr.s, kr.phase, true)) return false;
+        tc::fence_after_sync();
+        const int qs = two ? w : (kWide ? p_idx & 1 : 0);
+        const uint64_t a0 = dq + static_cast<uint64_t>(qs * (kQBytes / 16));
+        const uint64_t b0 = dk + static_cast<uint64_t>(kr.s * (kKStage / 16));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t ao = static_cast<uint64_t>((kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2);
+          const uint64_t bo = static_cast<uint64_t>((kk >> 2) * (kKBlk / 16) + (kk & 3) * 2);
+          if (leader) tc::mma_f16_ss(tmem + w * 128, a0 + ao, b0 + bo, kIdescQK, kk > 0);
+        }
+        if (leader) tc::mma_commit(&bars[kBarSFull + w]);
+        if (!two || w == 1) {
+          if (leader) tc::mma_commit(&bars[kBarKEmpty + kr.s]);
+          kr.next();
+        }
+        // the last S that reads this query
+        if (leader && u + (two ? 2 : 1) >= n_units) tc::mma_commit(&bars[kBarQEmpty + qs]);
+        return true;
+      };
+      for (int i = 0; ok && i < (two ? 2 : 1); ++i) {
+        const int qs = two ? i : (kWide ? p_idx & 1 : 0);
+        ok = wait(kBarQFull + qs, uses[qs] & 1, true);
+        ++uses[qs];
+      }
+      if (!ok) break;
+      ok = issue_s(0) && (n_units < 2 || issue_s(1));
+      for (int u = 0; ok && u < n_units; ++u) {
+        const int w = u & 1;
+        ok = wait(kBarPFull + w, units[w] & 1, true);
+        if (ok && u == 0 && p_idx > 0)  // the last piece's O tiles have been read
+          ok = wait(kBarOEmpty, (p_idx - 1) & 1, true);
+        if (!ok) break;
+        ++units[w];
+        tc::fence_after_sync();
+        const Ring<kVHalves> v0 = vr;  // both row tiles read the same halves
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!two || w == 0) {
+            ok = wait(kBarVFull + vr.s, vr.phase, true);
+            if (!ok) break;
+            tc::fence_after_sync();
+          }
+          const uint64_t b0 = dv + static_cast<uint64_t>(vr.s * (kVHalf / 16));
+#pragma unroll
+          for (int kk = 0; kk < kHalf / 16; ++kk)
+            if (leader)
+              tc::mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + (h * (kHalf / 16) + kk) * 8,
+                             b0 + static_cast<uint64_t>(kk * 128), kIdescPV,
+                             u >= 2 || h > 0 || kk > 0);
+          if (leader && (!two || w == 1)) tc::mma_commit(&bars[kBarVEmpty + vr.s]);
+          vr.next();
+        }
+        if (two && w == 0) vr = v0;
+        if (!ok) break;
+        if (leader) tc::mma_commit(&bars[kBarODone + w]);
+        if (u + 2 < n_units) ok = issue_s(u + 2);
+      }
+    }
+    // every MMA issued has to land before tensor memory is released
+    if (leader) tc::mma_commit(&bars[kBarDrain]);
+    mbar_wait_bounded(&bars[kBarDrain], 0);
+    __syncwarp();
+  } else if (warp == kPieceWarp) {
+    // ================= the CTA's pieces =================
+    if (lane == 0) {
+      Ring<kPieceRing> ring;
+      walk_pieces(a, kShape, range, true, [&](const Piece &p) {
+        if (ring.wrapped && !wait(kBarTaken + ring.s, ring.phase ^ 1)) return false;
+        pieces[ring.s] = p;
+        mbar_arrive(&bars[kBarPiece + ring.s]);
+        ring.next();
+        return true;
+      });
+    }
+    __syncwarp();
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace tcore
+}  // namespace tree
+}  // namespace k16v8

@@ -272,7 +272,8 @@ def test_binding_refuses_wrong_tensors(K):
     good = dict(q=to_dev(c.q), qo_indptr=to_dev(c.indptr), max_nodes=4, tree_mask=to_dev(c.mask),
                 k_cache=to_dev(c.kc), v_cache=to_dev(c.vc), v_scale=to_dev(c.vs),
                 block_table=to_dev(c.bt), seq_lens=to_dev(c.lens), max_seq_len=40, sm_scale=0.1,
-                workspace=torch.empty(1 << 22, dtype=torch.uint8, device=dev()),
+                workspace=torch.empty(K.k16v8_tree_workspace_size(4, 1, 4, 8, 2, 128, 40),
+                                      dtype=torch.uint8, device=dev()),
                 out=torch.empty((4, 8, 128), dtype=torch.float16, device=dev()))
     K.k16v8_paged_tree_attention(**good)
     for name in ("q", "qo_indptr", "tree_mask", "k_cache", "v_cache", "v_scale", "block_table",
@@ -281,6 +282,9 @@ def test_binding_refuses_wrong_tensors(K):
         for bad in (t.double() if t.dtype != torch.float64 else t.float(), t.cpu(), t[..., None]):
             with pytest.raises((ValueError, IndexError)):
                 K.k16v8_paged_tree_attention(**{**good, name: bad})
+    for ws in (None, good["workspace"][:-1]):
+        with pytest.raises(K.K16V8Error):
+            K.k16v8_paged_tree_attention(**{**good, "workspace": ws})
     with pytest.raises(K.K16V8Error):
         K.k16v8_paged_tree_attention(**{**good, "max_nodes": 65})
     with pytest.raises(K.K16V8Error):
