@@ -1,6 +1,5 @@
 // Attention of drafted token trees over the paged K16/V8 cache: the calls
-// and the merge of cut segments (the split kernel: tree_tc.cuh, the cut:
-// tree_plan.cuh).
+// and the merge of cut segments (the split kernel: tree_tc.cuh, the cut: tree_plan.cuh).
 //
 // "Phi-4: quality transfer and interrupted throughput studies": the intro
 // gives the format (FP16 K, E4M3 V with per-head scales) and the geometry (40
@@ -20,55 +19,70 @@ namespace k16v8 {
 namespace tree {
 
 // Joins the pieces of the segment that begins in CTA blockIdx.x and is cut:
-// o = sum_p e^(lse_p - lse) o_p, lse = log sum_p e^lse_p.  A lane per row, a
-// warp per 32 dims, so the loads of a warp are 512-byte runs.
+// o = sum_p e^(lse_p - lse) o_p, lse = log sum_p e^lse_p.  A block takes 32
+// rows x 32 dims: a lane per row, a warp per 8 dims, so a warp's loads are
+// 512-byte runs.  Bound by latency: the first pieces' rows are asked for
+// before the LSEs are in hand, and eight pieces are in flight at a time.
+constexpr int kMergeFlight = 8;
 __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
+  extern __shared__ float lse_of[];  // [piece][32 rows]
   pdl_wait();
   pdl_launch_dependents();
   const int4 cut = __ldg(a.cut + blockIdx.x);
   if (cut.x < 0) return;
+  const int first = blockIdx.x, pieces = cut.z - first + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = blockIdx.y * 32 + lane, chunk = (blockIdx.z * 4 + warp) * 2;
+  auto slot = [&](int p) { return 2 * static_cast<int64_t>(first + p) + (p == 0 ? 1 : 0); };
+  float4 x[kMergeFlight][2];
+  auto load = [&](int p0) {
+#pragma unroll
+    for (int u = 0; u < kMergeFlight; ++u) {
+      if (p0 + u >= pieces) continue;
+      const float4 *po = a.part_o + (slot(p0 + u) * 32 + chunk) * a.max_rows + row;
+      x[u][0] = __ldg(po);
+      x[u][1] = __ldg(po + a.max_rows);
+    }
+  };
+  load(0);
+  for (int p = warp; p < pieces; p += 4)
+    lse_of[p * 32 + lane] = __ldg(a.part_lse + slot(p) * a.max_rows + row);
   const int q0 = __ldg(a.qo_indptr + cut.x), n = __ldg(a.qo_indptr + cut.x + 1) - q0;
-  const int row = blockIdx.y * 32 + (threadIdx.x & 31), warp = threadIdx.x >> 5;
-  if (row >= n * kGroup) return;
-  const int first = blockIdx.x, last = cut.z;
-  auto slot = [&](int p) { return 2 * static_cast<int64_t>(p) + (p == first ? 1 : 0); };
+  __syncthreads();
   float M = -INFINITY;
-#pragma unroll 4
-  for (int p = first; p <= last; ++p) M = fmaxf(M, __ldg(a.part_lse + slot(p) * a.max_rows + row));
+  for (int p = 0; p < pieces; ++p) M = fmaxf(M, lse_of[p * 32 + lane]);
   float S = 0.f;
-  float4 acc[8];
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int p0 = 0; p0 < pieces; p0 += kMergeFlight) {
+    if (p0 > 0) load(p0);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int p = first; p <= last; ++p) {
-    const float l = __ldg(a.part_lse + slot(p) * a.max_rows + row);
-    const float4 *po = a.part_o + (slot(p) * 32 + warp * 8) * a.max_rows + row;
-    const float w = l == -INFINITY ? 0.f : ex2((l - M) * kLog2e);
-    S += w;
+    for (int u = 0; u < kMergeFlight; ++u) {
+      if (p0 + u >= pieces) continue;
+      const float l = lse_of[(p0 + u) * 32 + lane];
+      if (l == -INFINITY) continue;
+      const float w = ex2((l - M) * kLog2e);
+      S += w;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float4 x = __ldg(po + static_cast<int64_t>(i) * a.max_rows);
-      acc[i].x = fmaf(w, x.x, acc[i].x);
-      acc[i].y = fmaf(w, x.y, acc[i].y);
-      acc[i].z = fmaf(w, x.z, acc[i].z);
-      acc[i].w = fmaf(w, x.w, acc[i].w);
+      for (int i = 0; i < 2; ++i) {
+        acc[i].x = fmaf(w, x[u][i].x, acc[i].x);
+        acc[i].y = fmaf(w, x[u][i].y, acc[i].y);
+        acc[i].z = fmaf(w, x[u][i].z, acc[i].z);
+        acc[i].w = fmaf(w, x[u][i].w, acc[i].w);
+      }
     }
   }
+  if (row >= n * kGroup) return;
   const bool dead = S == 0.f;  // the row sees nothing
   const float inv = dead ? 0.f : 1.f / S;
   const int64_t orow =
       static_cast<int64_t>(q0 + row / kGroup) * a.hkv * kGroup + cut.y * kGroup + row % kGroup;
-  uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + warp * 32);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 x = acc[2 * i], y = acc[2 * i + 1];
-    const __half2 h[4] = {__floats2half2_rn(x.x * inv, x.y * inv),
-                          __floats2half2_rn(x.z * inv, x.w * inv),
-                          __floats2half2_rn(y.x * inv, y.y * inv),
-                          __floats2half2_rn(y.z * inv, y.w * inv)};
-    dst[i] = *reinterpret_cast<const uint4 *>(h);
-  }
-  if (warp == 0 && a.lse) a.lse[orow] = dead ? -INFINITY : M + lg2(S) * kLn2;
+  const __half2 h[4] = {__floats2half2_rn(acc[0].x * inv, acc[0].y * inv),
+                        __floats2half2_rn(acc[0].z * inv, acc[0].w * inv),
+                        __floats2half2_rn(acc[1].x * inv, acc[1].y * inv),
+                        __floats2half2_rn(acc[1].z * inv, acc[1].w * inv)};
+  *reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + chunk * 4) =
+      *reinterpret_cast<const uint4 *>(h);
+  if (chunk == 0 && a.lse) a.lse[orow] = dead ? -INFINITY : M + lg2(S) * kLn2;
 }
 
 // ---- host side ------------------------------------------------------------
@@ -79,9 +93,10 @@ struct Layout {
 };
 
 static bool layout(int32_t max_nodes, Layout *w) {
-  w->ctas = k16v8_sm_count();
-  if (w->ctas <= 0) return false;
+  const int sms = k16v8_sm_count();
+  if (sms <= 0) return false;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  w->ctas = sms;
   w->max_rows = max_nodes <= tcore::kNodes ? tcore::kRows : 2 * tcore::kRows;
   const size_t rows = 2 * static_cast<size_t>(w->ctas) * w->max_rows;
   w->lse_off = up(w->ctas * sizeof(int4));
@@ -161,9 +176,6 @@ extern "C" int32_t k16v8_paged_tree_attention(
   tree::Layout w;
   if (!tree::layout(max_nodes, &w)) return K16V8_ERR_CUDA;
   if (workspace_bytes < w.total) return K16V8_ERR_WORKSPACE_TOO_SMALL;
-  CUtensorMap mq, mk;
-  if (!map_rows(&mq, q, num_qo_heads, total_q) || !map_keys(&mk, k_cache, k_rows))
-    return K16V8_ERR_CUDA;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   const tree::Args a{static_cast<const __half *>(q),
                      qo_indptr,
@@ -189,9 +201,13 @@ extern "C" int32_t k16v8_paged_tree_attention(
                      lse,
                      dev_error};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CUtensorMap mq, mk;
+  if (!map_rows(&mq, q, num_qo_heads, total_q) || !map_keys(&mk, k_cache, k_rows))
+    return K16V8_ERR_CUDA;
   st = max_nodes > tree::tcore::kNodes ? tree::launch_tc<true>(mq, mk, a, w.ctas, s)
                                        : tree::launch_tc<false>(mq, mk, a, w.ctas, s);
   if (st != K16V8_OK) return st;
-  return k16v8_launch_pdl(tree::tree_merge_kernel, dim3(w.ctas, (max_nodes * kGroup + 31) / 32),
-                          dim3(128), 0, s, a);
+  return k16v8_launch_pdl(tree::tree_merge_kernel,
+                          dim3(w.ctas, (max_nodes * kGroup + 31) / 32, 4), dim3(128),
+                          static_cast<size_t>(w.ctas) * 32 * sizeof(float), s, a);
 }

@@ -18,7 +18,6 @@
 namespace k16v8 {
 namespace tree {
 
-constexpr unsigned kFull = 0xffffffffu;
 constexpr int kMaxBatch = 8192;  // the scan's prefix lives in shared memory
 
 struct Args {
@@ -67,10 +66,11 @@ struct Range {
   int b, cta;
 };
 
-// The CTA's range of units; every thread of the block calls it.  `prefix`:
-// scratch of batch + 1 entries, `aux`: of 33.
-__device__ __forceinline__ Range plan_range(const Args &a, const Shape &shape, int64_t *prefix,
-                                            int64_t *aux) {
+// The CTA's range of units, at least `least` (no less than the largest
+// weight, so that a CTA between two cuts has a tile); every thread of the block
+// calls it.  `prefix`: scratch of batch + 1 entries, `aux`: of 33.
+__device__ __forceinline__ Range plan_range(const Args &a, const Shape &shape, int least,
+                                            int64_t *prefix, int64_t *aux) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   int64_t carry = 0;
   for (int b0 = 0; b0 < a.batch; b0 += blockDim.x) {
@@ -86,7 +86,7 @@ __device__ __forceinline__ Range plan_range(const Args &a, const Shape &shape, i
     int64_t x = cost;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(kFull, x, o);
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) aux[warp] = x;
@@ -104,7 +104,6 @@ __device__ __forceinline__ Range plan_range(const Args &a, const Shape &shape, i
   if (threadIdx.x == 0) prefix[a.batch] = carry;
   __syncthreads();
   Range r;
-  const int least = a.max_nodes > shape.wide_nodes ? 2 : 1;  // a CTA between two cuts has a tile
   r.width = (carry + gridDim.x - 1) / gridDim.x;
   if (r.width < least) r.width = least;
   r.cta = blockIdx.x;
@@ -133,53 +132,66 @@ struct Piece {
   }
 };
 
-// Walks the pieces of a range in order; calls take(piece) for each and, at
-// the end, for one without tiles; take returns false to stop.  Of a cut
-// segment that begins in the CTA the merge is told.
-template <typename Take>
-__device__ __forceinline__ void walk_pieces(const Args &a, const Shape &shape, const Range &r,
-                                            bool teller, Take take) {
-  Piece p{};
-  int nt = 0, shift = 0;  // the segment's tiles and the weight's logarithm
-  auto load = [&]() {
+// Walks the pieces of a range in order.  Of a cut segment that begins in the
+// CTA it tells the merge.
+struct Walker {
+  Piece p;
+  int nt, shift;  // the segment's tiles and the weight's logarithm
+  int64_t start;  // of the segment, in units
+
+  __device__ __forceinline__ bool load(const Args &a, const Shape &shape) {
     bool bad;
     if (!sequence(a, p.b, p.q0, p.n, p.L, bad)) return false;
     nt = shape.tiles(p.L);
     shift = shape.weight(p.n) - 1;
     return true;
-  };
-  p.b = r.b;
-  load();  // it holds the range's first unit, so it has tiles
-  const int64_t seg = static_cast<int64_t>(nt) << shift;
-  p.g = static_cast<int>((r.lo - r.start) / seg);
-  int64_t start = r.start + p.g * seg;
-  p.t0 = static_cast<int>((r.lo - start + (1 << shift) - 1) >> shift);
-  while (true) {
-    if (p.t0 < nt) {
-      if (start + (static_cast<int64_t>(p.t0) << shift) >= r.hi) break;
-      p.t1 = static_cast<int>(
-          min(static_cast<int64_t>(nt), (r.hi - start + (1 << shift) - 1) >> shift));
-      p.tiles = p.t1 - p.t0;
-      p.whole = p.t0 == 0 && p.t1 == nt;
-      p.slot = 2 * r.cta + (start >= r.lo ? 1 : 0);
-      if (teller && start >= r.lo && p.t1 < nt)
-        a.cut[r.cta] = make_int4(
-            p.b, p.g,
-            static_cast<int>((start + (static_cast<int64_t>(nt - 1) << shift)) / r.width), 0);
-      if (!take(p)) return;
-    }  // else the range begins inside the segment's last tile
-    start += static_cast<int64_t>(nt) << shift;
-    p.t0 = 0;
-    if (++p.g == a.hkv) {
-      p.g = 0;
-      do {
-        ++p.b;
-      } while (p.b < a.batch && !load());
-      if (p.b >= a.batch) break;
-    }
   }
-  p.tiles = 0;
-  take(p);
+  __device__ __forceinline__ void init(const Args &a, const Shape &shape, const Range &r) {
+    p.b = r.b;
+    load(a, shape);  // it holds the range's first unit, so it has tiles
+    const int64_t seg = static_cast<int64_t>(nt) << shift;
+    p.g = static_cast<int>((r.lo - r.start) / seg);
+    start = r.start + p.g * seg;
+    p.t0 = static_cast<int>((r.lo - start + (1 << shift) - 1) >> shift);
+  }
+  // The next piece, false at the end of the range.
+  __device__ __forceinline__ bool next(const Args &a, const Shape &shape, const Range &r,
+                                       Piece &out) {
+    bool found = false;
+    while (!found && p.b < a.batch) {
+      if (p.t0 < nt) {  // else the range begins inside the segment's last tile
+        if (start + (static_cast<int64_t>(p.t0) << shift) >= r.hi) {
+          p.b = a.batch;
+          break;
+        }
+        p.t1 = static_cast<int>(
+            min(static_cast<int64_t>(nt), (r.hi - start + (1 << shift) - 1) >> shift));
+        p.tiles = p.t1 - p.t0;
+        p.whole = p.t0 == 0 && p.t1 == nt;
+        p.slot = 2 * r.cta + (start >= r.lo ? 1 : 0);
+        if (start >= r.lo && p.t1 < nt)
+          a.cut[r.cta] = make_int4(
+              p.b, p.g,
+              static_cast<int>((start + (static_cast<int64_t>(nt - 1) << shift)) / r.width), 0);
+        out = p;
+        found = true;
+      }
+      start += static_cast<int64_t>(nt) << shift;
+      p.t0 = 0;
+      if (++p.g == a.hkv) {
+        p.g = 0;
+        do {
+          ++p.b;
+        } while (p.b < a.batch && !load(a, shape));
+      }
+    }
+    return found;
+  }
+};
+
+// 0xff in every byte of w that is an E4M3 NaN (0x7f or 0xff).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
 }  // namespace tree

@@ -1,5 +1,5 @@
-// Tree attention on the tensor cores: the split kernel for trees of more than
-// a few nodes (see tree_attention.cu for the operator).
+// Tree attention on the tensor cores: the split kernel (see tree_attention.cu
+// for the operator).
 //
 // One CTA per SM, all 512 columns of tensor memory.  The work is the flat
 // list of (sequence, KV head, 128-position tile), cut into one equal range
@@ -47,6 +47,8 @@ namespace k16v8 {
 namespace tree {
 namespace tcore {
 
+constexpr unsigned kFull = 0xffffffffu;
+
 constexpr int kNodes = 32;                   // nodes per row tile
 constexpr int kRows = kNodes * kGroup;       // 128
 constexpr int kKv = 128;                     // positions per KV tile
@@ -58,11 +60,6 @@ constexpr int kDequantThreads = kDequantWarps * 32;
 constexpr int kPieceRing = 4;
 constexpr int kPieceReaders = 8 + kDequantWarps + 3;  // warps
 
-// 0xff in every byte of w that is an E4M3 NaN (0x7f or 0xff).
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
-  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-}
-
 // Rank of a dequant warp among them, or -1.
 __device__ __forceinline__ int dequant_rank(int warp) {
   return warp == 8 ? 0 : warp == 10 ? 1 : warp == 11 ? 2 : warp == 14 ? 3 : -1;
@@ -72,18 +69,20 @@ constexpr uint32_t kQBytes = kRows * 256;
 constexpr uint32_t kKBlk = kKv * 128;          // [128 pos][64 dims] fp16
 constexpr uint32_t kKStage = 2 * kKBlk;
 constexpr uint32_t kVstStage = kKv * 128;      // [128 pos][128] E4M3
-constexpr int kVstStages = 3;
 constexpr int kHalf = kKv / 2;                 // positions of a V half tile
 constexpr uint32_t kVBlk = kHalf * 128;        // [64 pos][64 dims] fp16
 constexpr uint32_t kVHalf = 2 * kVBlk;
-constexpr int kVHalves = 3;
 constexpr uint32_t kTmemCols = 512;  // S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512)
 
 // kWide: trees of more than 32 nodes may be among the batch.
 template <bool kWide>
 struct Smem {
   static constexpr int kQSlots = kWide ? 2 : 1;
+  // stages: with two row tiles a V tile is held until both have read it, so
+  // two whole ones are needed; else a half tile is free as soon as it is read
   static constexpr int kKStages = kWide ? 2 : 3;
+  static constexpr int kVstStages = kWide ? 2 : 3;
+  static constexpr int kVHalves = kWide ? 4 : 3;
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + kQSlots * kQBytes;
   static constexpr uint32_t kVst = kK + kKStages * kKStage;
@@ -108,16 +107,16 @@ enum {
   kBarVstFull = 10,   // +stage
   kBarVstEmpty = 13,  // +stage, kDequantThreads arrivals
   kBarVFull = 16,     // +half, kDequantThreads arrivals
-  kBarVEmpty = 19,    // +half
-  kBarSFull = 22,     // +slot
-  kBarPFull = 24,     // +slot, 128 arrivals
-  kBarODone = 26,     // +slot
-  kBarOEmpty = 28,    // 8 arrivals: both O tiles have been read
-  kBarJoin = 29,      // 256 arrivals: both slots' statistics are in shared memory
-  kBarPiece = 30,     // +ring entry: described
-  kBarTaken = 34,     // +ring entry: kPieceReaders arrivals
-  kBarDrain = 38,
-  kNumBars = 39
+  kBarVEmpty = 20,    // +half
+  kBarSFull = 24,     // +slot
+  kBarPFull = 26,     // +slot, 128 arrivals
+  kBarODone = 28,     // +slot
+  kBarOEmpty = 30,    // 8 arrivals: both O tiles have been read
+  kBarJoin = 31,      // 256 arrivals: both slots' statistics are in shared memory
+  kBarPiece = 32,     // +ring entry: described
+  kBarTaken = 36,     // +ring entry: kPieceReaders arrivals
+  kBarDrain = 40,
+  kNumBars = 41
 };
 static_assert(kNumBars * 8 + 16 <= 384, "barriers");
 
@@ -204,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
   }
   // ---- this CTA's range of the work (scratch: the operand stages) ----
   constexpr Shape kShape{kKv, kNodes};
-  const Range range = plan_range(a, kShape, reinterpret_cast<int64_t *>(smem_raw),
+  const Range range = plan_range(a, kShape, kWide ? 2 : 1, reinterpret_cast<int64_t *>(smem_raw),
                                  reinterpret_cast<int64_t *>(smem_raw + M::kBar));
   if (range.lo >= range.hi) return;  // uniform over the CTA
 
@@ -268,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       const bool row_valid = node < pc.n;
       const bool warp_live = (two ? w * kNodes : 0) + (warp & 3) * 8 < pc.n;
       const uint64_t mask = row_valid ? __ldg(a.tree_mask + pc.q0 + node) & pc.node_bits() : 0;
+      const float vs = __ldg(a.v_scale + pc.g);
       const int mine = two ? pc.tiles : (pc.tiles + 1 - w) / 2;
       const int theirs = two ? 0 : (pc.tiles + w) / 2;  // units of the other slot to join
       float m_used = -INFINITY, l = 0.f;
@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         l_all = f_own * l + f_other * l_o;
       }
       const bool dead = !(l_all > 0.f) && l_all == l_all;  // the row sees nothing
-      const float inv = dead ? 0.f : __ldg(a.v_scale + pc.g) / l_all;
+      const float inv = dead ? 0.f : __fdividef(vs, l_all);
       const float lse = dead ? -INFINITY : (m_all + lg2(l_all)) * kLn2;
       const float g_own = f_own * inv, g_other = f_other * inv;
       // with one row tile, slot w's warps write dims 64w .. 64w + 63 of every row
@@ -475,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     const int dt = dequant_rank(warp) * 32 + lane;
     Piece pc;
     Ring<kPieceRing> ring;
-    Ring<kVstStages> src;
-    Ring<kVHalves> dst;
+    Ring<M::kVstStages> src;
+    Ring<M::kVHalves> dst;
     bool ok = true;
     for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
       for (int t = pc.t0; ok && t < pc.t1; ++t) {
@@ -490,38 +490,52 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
           if (dst.wrapped) ok = wait(kBarVEmpty + dst.s, dst.phase ^ 1);
           if (!ok) break;
           uint8_t *vdst = sV + dst.s * kVHalf;
+          // chunk i of this thread: 16 E4M3 values, position hp of the half
+          constexpr int kChunks = kHalf * 8 / kDequantThreads;
+          auto put = [&](int hp, int c16, const uint4 &raw) {
+            const uint32_t wv[4] = {raw.x, raw.y, raw.z, raw.w};
+            uint32_t hv[8];
 #pragma unroll
-          for (int i = 0; i < kHalf * 8 / kDequantThreads; ++i) {  // chunks of 16 E4M3 values
-            const int id = i * kDequantThreads + dt;
-            const int hp = id >> 3, c16 = id & 7, pos = h * kHalf + hp;
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = make_uint4(0, 0, 0, 0);
-            if (pos < live && !(bad >> (pos >> 4) & 1)) {
-              uint4 raw = *reinterpret_cast<const uint4 *>(vst + pos * 128 + c16 * 16);
-              if (pos >= tree0) {  // a node: its NaN codes must not reach rows that do not see it
-                const uint32_t n0 = nan_bytes(raw.x), n1 = nan_bytes(raw.y), n2 = nan_bytes(raw.z),
-                               n3 = nan_bytes(raw.w);
-                if (n0 | n1 | n2 | n3) {
-                  raw = make_uint4(raw.x & ~n0, raw.y & ~n1, raw.z & ~n2, raw.w & ~n3);
-                  const int rel = pos - tree0;
-                  atomicOr(&nan_nodes[(p_idx & 3) * 2 + (rel >> 5)], 1u << (rel & 31));
-                }
-              }
-              const uint32_t wv[4] = {raw.x, raw.y, raw.z, raw.w};
-              uint32_t hv[8];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const __half2 u = e4m3x2_to_half2(static_cast<uint16_t>(wv[q] & 0xffffu));
-                const __half2 v = e4m3x2_to_half2(static_cast<uint16_t>(wv[q] >> 16));
-                hv[2 * q] = *reinterpret_cast<const uint32_t *>(&u);
-                hv[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&v);
-              }
-              lo = make_uint4(hv[0], hv[1], hv[2], hv[3]);
-              hi = make_uint4(hv[4], hv[5], hv[6], hv[7]);
+            for (int q = 0; q < 4; ++q) {
+              const __half2 u = e4m3x2_to_half2(static_cast<uint16_t>(wv[q] & 0xffffu));
+              const __half2 v = e4m3x2_to_half2(static_cast<uint16_t>(wv[q] >> 16));
+              hv[2 * q] = *reinterpret_cast<const uint32_t *>(&u);
+              hv[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&v);
             }
             const uint32_t off = hp * 128 + (c16 & 3) * 32;
             uint8_t *blk = vdst + (c16 >> 2) * kVBlk;
-            *reinterpret_cast<uint4 *>(blk + tc::sw128(off)) = lo;
-            *reinterpret_cast<uint4 *>(blk + tc::sw128(off + 16)) = hi;
+            *reinterpret_cast<uint4 *>(blk + tc::sw128(off)) = make_uint4(hv[0], hv[1], hv[2], hv[3]);
+            *reinterpret_cast<uint4 *>(blk + tc::sw128(off + 16)) =
+                make_uint4(hv[4], hv[5], hv[6], hv[7]);
+          };
+          const int hp0 = dt >> 3, c16 = dt & 7;
+          const uint8_t *from = vst + (h * kHalf + hp0) * 128 + c16 * 16;
+          if (tree0 >= kKv && !bad) {  // prefix positions only: no tests, loads in flight together
+            uint4 raw[kChunks];
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i)
+              raw[i] = *reinterpret_cast<const uint4 *>(from + i * (kDequantThreads / 8) * 128);
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) put(hp0 + i * (kDequantThreads / 8), c16, raw[i]);
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < kChunks; ++i) {
+              const int hp = hp0 + i * (kDequantThreads / 8), pos = h * kHalf + hp;
+              uint4 raw = make_uint4(0, 0, 0, 0);
+              if (pos < live && !(bad >> (pos >> 4) & 1)) {
+                raw = *reinterpret_cast<const uint4 *>(from + i * (kDequantThreads / 8) * 128);
+                if (pos >= tree0) {  // a node: NaN codes must not reach rows that do not see it
+                  const uint32_t n0 = nan_bytes(raw.x), n1 = nan_bytes(raw.y),
+                                 n2 = nan_bytes(raw.z), n3 = nan_bytes(raw.w);
+                  if (n0 | n1 | n2 | n3) {
+                    raw = make_uint4(raw.x & ~n0, raw.y & ~n1, raw.z & ~n2, raw.w & ~n3);
+                    const int rel = pos - tree0;
+                    atomicOr(&nan_nodes[(p_idx & 3) * 2 + (rel >> 5)], 1u << (rel & 31));
+                  }
+                }
+              }
+              put(hp, c16, raw);
+            }
           }
           fence_proxy_async();
           mbar_arrive(&bars[kBarVFull + dst.s]);
@@ -536,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     // ================= V loads =================
     Piece pc;
     Ring<kPieceRing> ring;
-    Ring<kVstStages> dst;
+    Ring<M::kVstStages> dst;
     uint32_t issued = 0;
     bool ok = true;
     while (ok && get_piece(pc, ring)) {
@@ -564,8 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     }
     // let the copies issued last land before shared memory is released
     if (lane == 0)
-      for (uint32_t i = issued < kVstStages ? 0 : issued - kVstStages; i < issued; ++i)
-        mbar_wait_bounded(&bars[kBarVstFull + i % kVstStages], (i / kVstStages) & 1);
+      for (uint32_t n = M::kVstStages, i = issued < n ? 0 : issued - n; i < issued; ++i)
+        mbar_wait_bounded(&bars[kBarVstFull + i % n], (i / n) & 1);
     __syncwarp();
   } else if (warp == kLoadKWarp) {
     // ================= Q and K loads =================
@@ -636,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     Piece pc;
     Ring<kPieceRing> ring;
     Ring<M::kKStages> kr;  // next K stage to use
-    Ring<kVHalves> vr;     // next V half to use
+    Ring<M::kVHalves> vr;     // next V half to use
     uint32_t uses[2] = {0, 0}, units[2] = {0, 0};
     bool ok = true;
     for (uint32_t p_idx = 0; ok && get_piece(pc, ring, true); ++p_idx) {
@@ -681,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         if (!ok) break;
         ++units[w];
         tc::fence_after_sync();
-        const Ring<kVHalves> v0 = vr;  // both row tiles read the same halves
+        const Ring<M::kVHalves> v0 = vr;  // both row tiles read the same halves
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!two || w == 0) {
@@ -713,13 +727,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     // ================= the CTA's pieces =================
     if (lane == 0) {
       Ring<kPieceRing> ring;
-      walk_pieces(a, kShape, range, true, [&](const Piece &p) {
-        if (ring.wrapped && !wait(kBarTaken + ring.s, ring.phase ^ 1)) return false;
+      Walker walker;
+      walker.init(a, kShape, range);
+      for (bool more = true; more;) {
+        if (ring.wrapped && !wait(kBarTaken + ring.s, ring.phase ^ 1)) break;
+        Piece p;
+        more = walker.next(a, kShape, range, p);
+        if (!more) p.tiles = 0;  // the end
         pieces[ring.s] = p;
         mbar_arrive(&bars[kBarPiece + ring.s]);
         ring.next();
-        return true;
-      });
+      }
     }
     __syncwarp();
   }
