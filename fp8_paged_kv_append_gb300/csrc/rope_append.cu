@@ -108,41 +108,34 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(
     float factor, const int64_t *__restrict__ slot_mapping, int32_t num_tokens,
     const float *__restrict__ v_scale, __half *q_out, __half *k_cache, uint8_t *v_cache,
     int32_t num_pages, int32_t hq, int32_t hkv, int32_t *dev_error) {
-  extern __shared__ __align__(16) float2 table[];  // [token of the run][rotary / 2]
+  // cos, sin of the run's tokens: pair 8c + 2i + e of a token at [i][c][e], so
+  // the eight lanes of a row read neighbouring 16 bytes
+  extern __shared__ __align__(16) float2 table[];
   pdl_wait();
   pdl_launch_dependents();
-  const int upt = (hq + 2 * hkv) * kUnitsPerRow;  // units per token
+  const uint32_t upt = static_cast<uint32_t>(hq + 2 * hkv) * kUnitsPerRow;  // units per token
   const int64_t total = static_cast<int64_t>(num_tokens) * upt;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * (kThreads * kUnits);
-  const int64_t t0 = first / upt;
-  const int rem = static_cast<int>(first - t0 * upt);
-  const int run = static_cast<int>(min(static_cast<int64_t>(kThreads * kUnits), total - first));
+  const int32_t t0 = static_cast<int32_t>(first / upt);
+  const uint32_t rem = static_cast<uint32_t>(first - static_cast<int64_t>(t0) * upt);
+  const uint32_t run =
+      static_cast<uint32_t>(min(static_cast<int64_t>(kThreads * kUnits), total - first));
   const int n_tok = (rem + run - 1) / upt + 1;
-  const int64_t n_slots = static_cast<int64_t>(num_pages) * kPage;
   const int half = rotary >> 1;
 
+  // The data first: nothing of it depends on slots or positions.
   Raw<T> raw[kUnits];
-  int64_t slot[kUnits];
   int row[kUnits], tok[kUnits], c[kUnits];
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
-    const int u = j * kThreads + threadIdx.x;
-    slot[j] = -1;
+    const uint32_t u = j * kThreads + threadIdx.x;
+    row[j] = -1;
     if (u >= run) continue;
     tok[j] = (rem + u) / upt;
     const int in_tok = rem + u - tok[j] * upt;
     row[j] = in_tok / kUnitsPerRow;
     c[j] = in_tok % kUnitsPerRow;
     const int64_t t = t0 + tok[j];
-    const int64_t s = __ldg(slot_mapping + t);
-    if (s < 0) continue;  // a padding token: nothing of it is read or written
-    const int32_t pos = __ldg(positions + t);
-    if (s >= n_slots || pos < 0 || pos >= kMaxPosition) {
-      if (in_tok == 0)
-        flag_error(dev_error, s >= n_slots ? K16V8_DEVERR_SLOT : K16V8_DEVERR_POSITION);
-      continue;
-    }
-    slot[j] = s;
     const T *src;
     if (row[j] < hq)
       src = q + t * q_ts + row[j] * kHeadDim;
@@ -151,24 +144,43 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(
     else
       src = v + t * v_ts + (row[j] - hq - hkv) * kHeadDim;
     const bool apart = !kInterleaved && row[j] < hq + hkv && 16 * c[j] < rotary;
-    load8(src + (apart ? 8 * c[j] : 16 * c[j]), raw[j].w);
+    load8(src + (apart ? 8 : 16) * c[j], raw[j].w);
     load8(src + (apart ? 8 * c[j] + half : 16 * c[j] + 8), raw[j].w + sizeof(T) / 2);
   }
+  int64_t slot[kUnits];
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j)
+    slot[j] = row[j] >= 0 ? __ldg(slot_mapping + t0 + tok[j]) : -1;
 
   for (int i = threadIdx.x; i < n_tok * half; i += kThreads) {
     const int t = i / half, f = i - t * half;
-    table[i] = turn(__ldg(positions + t0 + t), __ldg(inv_freq + f), factor);
+    table[t * half + ((f & 7) >> 1) * (half >> 2) + (f >> 3) * 2 + (f & 1)] =
+        turn(__ldg(positions + t0 + t), __ldg(inv_freq + f), factor);
+  }
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    if (slot[j] < 0) {  // a padding token: nothing is written for it
+      row[j] = -1;
+      continue;
+    }
+    const bool bad_slot = slot[j] >= static_cast<int64_t>(num_pages) * kPage;
+    if (bad_slot || static_cast<uint32_t>(__ldg(positions + t0 + tok[j])) >= kMaxPosition) {
+      if (row[j] == 0) flag_error(dev_error, bad_slot ? K16V8_DEVERR_SLOT : K16V8_DEVERR_POSITION);
+      row[j] = -1;
+    }
   }
   __syncthreads();
 
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
-    if (slot[j] < 0) continue;
+    if (row[j] < 0) continue;
     float x[8], y[8];
     widen8(raw[j].w, x, static_cast<const T *>(nullptr));
     widen8(raw[j].w + sizeof(T) / 2, y, static_cast<const T *>(nullptr));
-    const int64_t page = slot[j] / kPage;
-    const int off = static_cast<int>(slot[j] % kPage);
+    const uint32_t page = static_cast<uint32_t>(slot[j] >> 4), off = slot[j] & (kPage - 1);
+    static_assert(kPage == 16, "slot = page * 16 + offset");
+    // row of head 0 of the slot in the pool
+    const int64_t pool = static_cast<int64_t>(page) * hkv * kPage + off;
     if (row[j] >= hq + hkv) {  // value: IEEE divide by the head's scale, round to E4M3
       const int h = row[j] - hq - hkv;
       const float s = __ldg(v_scale + h);
@@ -180,16 +192,17 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(
                (static_cast<uint32_t>(e4m3x2_from_f32(__fdiv_rn(z[2], s), __fdiv_rn(z[3], s)))
                 << 16);
       }
-      const int64_t dst = ((page * hkv + h) * kPage + off) * kHeadDim + 16 * c[j];
-      *reinterpret_cast<uint4 *>(v_cache + dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(v_cache + (pool + h * kPage) * kHeadDim + 16 * c[j]) =
+          make_uint4(w[0], w[1], w[2], w[3]);
       continue;
     }
     const bool rotated = 16 * c[j] < rotary;
     if (rotated) {
-      const float4 *cs = reinterpret_cast<const float4 *>(table + tok[j] * half + 8 * c[j]);
+      const float4 *cs =
+          reinterpret_cast<const float4 *>(table + tok[j] * half) + c[j];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 t2 = cs[i];  // cos, sin of two frequencies
+        const float4 t2 = cs[i * (half >> 3)];  // cos, sin of two frequencies
         float &a0 = kInterleaved ? (i < 2 ? x[4 * i] : y[4 * i - 8]) : x[2 * i];
         float &b0 = kInterleaved ? (i < 2 ? x[4 * i + 1] : y[4 * i - 7]) : y[2 * i];
         float &a1 = kInterleaved ? (i < 2 ? x[4 * i + 2] : y[4 * i - 6]) : x[2 * i + 1];
@@ -202,11 +215,10 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(
         b1 = rb1;
       }
     }
-    __half *dst = row[j] < hq
-                      ? q_out + ((t0 + tok[j]) * hq + row[j]) * kHeadDim
-                      : k_cache + ((page * hkv + row[j] - hq) * kPage + off) * kHeadDim;
+    __half *dst = row[j] < hq ? q_out + (static_cast<int64_t>(t0 + tok[j]) * hq + row[j]) * kHeadDim
+                              : k_cache + (pool + (row[j] - hq) * kPage) * kHeadDim;
     const bool apart = !kInterleaved && rotated;
-    *reinterpret_cast<uint4 *>(dst + (apart ? 8 * c[j] : 16 * c[j])) = narrow8(x);
+    *reinterpret_cast<uint4 *>(dst + (apart ? 8 : 16) * c[j]) = narrow8(x);
     *reinterpret_cast<uint4 *>(dst + (apart ? 8 * c[j] + half : 16 * c[j] + 8)) = narrow8(y);
   }
 }
@@ -245,8 +257,20 @@ static int32_t launch(const Args &a, cudaStream_t stream) {
                           a.v_cache, a.num_pages, a.hq, a.hkv, a.dev_error);
 }
 
+// 64 bytes of a thread's input in flight: one fp32 unit or two 16-bit ones,
+// except where that leaves SMs without a CTA.  Two 16-bit units against one,
+// GB300: 45.0 against 49.0 us at 8,192 tokens of 40 + 10 heads, 3.5 against 4.1
+// at 256, 3.1 against 2.5 at 32 (30 CTAs); two fp32 units against one: 33.4
+// against 29.4 us at 4,096 tokens.
 template <typename T>
 static int32_t dispatch(const Args &a, bool interleaved, cudaStream_t stream) {
+  if constexpr (sizeof(T) == 2) {
+    const int64_t units = static_cast<int64_t>(a.num_tokens) * (a.hq + 2 * a.hkv) * kUnitsPerRow;
+    const int sms = k16v8_sm_count();
+    if (sms <= 0) return K16V8_ERR_CUDA;
+    if (units >= static_cast<int64_t>(sms) * 2 * kThreads)
+      return interleaved ? launch<T, true, 2>(a, stream) : launch<T, false, 2>(a, stream);
+  }
   return interleaved ? launch<T, true, 1>(a, stream) : launch<T, false, 1>(a, stream);
 }
 

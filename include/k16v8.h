@@ -542,8 +542,8 @@ int32_t k16v8_paged_prefill_attention_wait_test(
  *   k_cache[s/16][h][s%16][:] = fp16(rotated k[t][h])
  *   v_cache[s/16][h][s%16][:] = E4M3_rn_satfinite(fl32(v[t][h][:]) / v_scale[h])
  * (one rounding from fp32 each; a value beyond fp16's range becomes inf).  A
- * token with a negative slot is padding: nothing of it is read or written.  A
- * slot at or above num_pages*16 flags K16V8_DEVERR_SLOT, a position outside
+ * token with a negative slot is padding: nothing is written for it.  A slot
+ * at or above num_pages*16 flags K16V8_DEVERR_SLOT, a position outside
  * [0, 2^24) K16V8_DEVERR_POSITION, and the token is skipped.  Duplicate slots
  * in one call leave an unspecified one of the writers.
  *
