@@ -16,7 +16,9 @@
 // fraction.  For |p| < 2^24 the fraction is off by less than 2^-25 of a
 // revolution per unit frequency.
 //
-// HBM-bound.  A unit is 16 elements of one row: in the half layout dims
+// HBM-bound: 43.4 us for 8,192 bf16 tokens of 40 + 10 heads, 5.56 TB/s of the
+// bytes it cannot do without (0.82 of the copy rate), 28.6 us for 4,096 fp32
+// tokens (0.95).  A unit is 16 elements of one row: in the half layout dims
 // [8c, 8c+8) and their partners half a rotary width on, in the interleaved
 // layout 16 neighbouring dims -- either way frequencies 8c..8c+7, so one
 // table serves both.  A CTA takes a run of units; its threads load their
@@ -29,7 +31,7 @@
 namespace k16v8 {
 namespace rope {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kUnitsPerRow = kHeadDim / 16;
 constexpr int32_t kMaxPosition = 1 << 24;  // positions below are exact in fp32
 // 1 / 2pi as a sum of two fp32 numbers
@@ -259,9 +261,9 @@ static int32_t launch(const Args &a, cudaStream_t stream) {
 
 // 64 bytes of a thread's input in flight: one fp32 unit or two 16-bit ones,
 // except where that leaves SMs without a CTA.  Two 16-bit units against one,
-// GB300: 45.0 against 49.0 us at 8,192 tokens of 40 + 10 heads, 3.5 against 4.1
-// at 256, 3.1 against 2.5 at 32 (30 CTAs); two fp32 units against one: 33.4
-// against 29.4 us at 4,096 tokens.
+// GB300: 43.4 against 47.2 us at 8,192 tokens of 40 + 10 heads, 3.6 against 4.1
+// at 256, 3.1 against 2.5 at 32 (60 CTAs); two fp32 units against one: 29.2
+// against 28.6 us at 4,096 tokens.  (CTAs of 256 threads: 45.0 and 29.4 us.)
 template <typename T>
 static int32_t dispatch(const Args &a, bool interleaved, cudaStream_t stream) {
   if constexpr (sizeof(T) == 2) {
