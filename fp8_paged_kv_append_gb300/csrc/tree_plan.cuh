@@ -52,6 +52,13 @@ __device__ __forceinline__ bool sequence(const Args &a, int b, int &q0, int &n, 
   return !bad && n > 0;
 }
 
+// x / y of numbers >= 0, in 32 bits where they fit (64-bit division is a
+// hundred instructions).
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
 // The shape of a split kernel's tiles.
 struct Shape {
   int positions;   // per KV tile
@@ -92,7 +99,8 @@ __device__ __forceinline__ Range plan_range(const Args &a, const Shape &shape, i
     if (lane == 31) aux[warp] = x;
     __syncthreads();
     int64_t before = carry, all = 0;
-    for (int w = 0; w < warps; ++w) {
+    const int busy = min(warps, (a.batch - b0 + 31) >> 5);  // warps with sequences
+    for (int w = 0; w < busy; ++w) {
       const int64_t v = aux[w];
       if (w < warp) before += v;
       all += v;
@@ -104,7 +112,7 @@ __device__ __forceinline__ Range plan_range(const Args &a, const Shape &shape, i
   if (threadIdx.x == 0) prefix[a.batch] = carry;
   __syncthreads();
   Range r;
-  r.width = (carry + gridDim.x - 1) / gridDim.x;
+  r.width = divide(carry + gridDim.x - 1, gridDim.x);
   if (r.width < least) r.width = least;
   r.cta = blockIdx.x;
   r.lo = r.width * r.cta;
@@ -150,7 +158,7 @@ struct Walker {
     p.b = r.b;
     load(a, shape);  // it holds the range's first unit, so it has tiles
     const int64_t seg = static_cast<int64_t>(nt) << shift;
-    p.g = static_cast<int>((r.lo - r.start) / seg);
+    p.g = static_cast<int>(divide(r.lo - r.start, seg));
     start = r.start + p.g * seg;
     p.t0 = static_cast<int>((r.lo - start + (1 << shift) - 1) >> shift);
   }
@@ -172,7 +180,8 @@ struct Walker {
         if (start >= r.lo && p.t1 < nt)
           a.cut[r.cta] = make_int4(
               p.b, p.g,
-              static_cast<int>((start + (static_cast<int64_t>(nt - 1) << shift)) / r.width), 0);
+              static_cast<int>(divide(start + (static_cast<int64_t>(nt - 1) << shift), r.width)),
+              0);
         out = p;
         found = true;
       }

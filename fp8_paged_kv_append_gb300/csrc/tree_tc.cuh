@@ -95,9 +95,9 @@ struct Smem {
   static constexpr uint32_t kBytes = kStat + 2 * 2 * kRows * 4;
   static_assert(kBytes <= 227 * 1024, "one CTA's shared memory");
   static_assert(sizeof(int64_t) * (kMaxBatch + 1) <= kBar, "the scan's scratch");
+  static_assert(sizeof(int64_t) * 33 <= kBytes - kStat, "the scan's warp sums");
   static_assert(kInfo % 8 == 0 && kNan % 8 == 0 && kStat % 16 == 0, "alignment");
 };
-static_assert(sizeof(int64_t) * 33 <= 384, "the scan's warp sums, before the barriers live");
 
 enum {
   kBarQFull = 0,      // +slot
@@ -109,8 +109,8 @@ enum {
   kBarVFull = 16,     // +half, kDequantThreads arrivals
   kBarVEmpty = 20,    // +half
   kBarSFull = 24,     // +slot
-  kBarPFull = 26,     // +slot, 128 arrivals
-  kBarODone = 28,     // +slot
+  kBarPFull = 26,     // +slot, 4 arrivals (one per warp)
+  kBarODone = 28,     // +slot: the slot's last P V of a piece
   kBarOEmpty = 30,    // 8 arrivals: both O tiles have been read
   kBarJoin = 31,      // 256 arrivals: both slots' statistics are in shared memory
   kBarPiece = 32,     // +ring entry: described
@@ -195,18 +195,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int hq = a.hkv * kGroup;
-  pdl_wait();
-  if (tid == kPieceWarp * 32) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  if (smem_addr(smem_raw) & 1023u) {
-    if (tid == 0) flag_error(a.dev_error, K16V8_DEVERR_INTERNAL);
+  if (smem_addr(smem_raw) & 1023u) {  // operand tiles need 1024-byte alignment
+    pdl_wait();
+    if (tid == 0) {
+      a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      flag_error(a.dev_error, K16V8_DEVERR_INTERNAL);
+    }
     return;
   }
-  // ---- this CTA's range of the work (scratch: the operand stages) ----
-  constexpr Shape kShape{kKv, kNodes};
-  const Range range = plan_range(a, kShape, kWide ? 2 : 1, reinterpret_cast<int64_t *>(smem_raw),
-                                 reinterpret_cast<int64_t *>(smem_raw + M::kBar));
-  if (range.lo >= range.hi) return;  // uniform over the CTA
-
+  // ---- set-up that needs nothing of the preceding kernel ----
   if (warp == kLoadKWarp && lane == 0) {
     tc::prefetch_tensormap(&tmap_q);
     tc::prefetch_tensormap(&tmap_k);
@@ -215,11 +212,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
   }
-  if (tid == 0) {
+  if (tid == 32) {
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
       if (i >= kBarVstEmpty && i < kBarVEmpty) count = kDequantThreads;
-      if (i == kBarPFull || i == kBarPFull + 1) count = kRows;
+      if (i == kBarPFull || i == kBarPFull + 1) count = 4;
       if (i == kBarJoin) count = 2 * kRows;
       if (i == kBarOEmpty) count = 8;
       if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
@@ -229,7 +226,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     for (int i = 0; i < 8; ++i) nan_nodes[i] = 0;
     fence_barrier_init();
   }
+  pdl_wait();
+  if (tid == kPieceWarp * 32) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  // ---- this CTA's range of the work (scratch: the operand stages) ----
+  constexpr Shape kShape{kKv, kNodes};
+  const Range range = plan_range(a, kShape, kWide ? 2 : 1, reinterpret_cast<int64_t *>(smem_raw),
+                                 reinterpret_cast<int64_t *>(smem_raw + M::kStat));
+  const bool work = range.lo < range.hi;  // uniform over the CTA
   fence_proxy_async();  // the scan's scratch becomes operand stages
+  tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
@@ -247,7 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     return pc.tiles > 0;
   };
 
-  if (warp < 8) {
+  if (!work) {
+  } else if (warp < 8) {
     // ================= softmax of slot w =================
     const int w = warp >> 2;
     const int r = tid & 127;
@@ -258,7 +264,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     const uint32_t tOther = tmem + 256 + (w ^ 1) * 128;
     Piece pc;
     Ring<kPieceRing> ring;
-    uint32_t units = 0, other = 0;  // of this slot and of the other one, so far
+    uint32_t units = 0;             // of this slot so far
+    uint32_t last[2] = {0, 0};      // pieces in which a slot had units, so far
     uint32_t tiles = 0;             // of the CTA so far
     bool ok = true;
     for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
@@ -266,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       const int node = (two ? w * kNodes : 0) + (r >> 2);
       const bool row_valid = node < pc.n;
       const bool warp_live = (two ? w * kNodes : 0) + (warp & 3) * 8 < pc.n;
-      const uint64_t mask = row_valid ? __ldg(a.tree_mask + pc.q0 + node) & pc.node_bits() : 0;
+      const uint64_t mask_word = row_valid ? __ldg(a.tree_mask + pc.q0 + node) : 0;  // used late
       const float vs = __ldg(a.v_scale + pc.g);
       const int mine = two ? pc.tiles : (pc.tiles + 1 - w) / 2;
       const int theirs = two ? 0 : (pc.tiles + w) / 2;  // units of the other slot to join
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
           break;
         }
         if (!warp_live) {
-          mbar_arrive(&bars[kBarPFull + w]);
+          if (lane == 0) mbar_arrive(&bars[kBarPFull + w]);
           continue;
         }
         tc::fence_after_sync();
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         const bool need_mask = d < kKv || bad;
         // columns 32c .. 32c + 31 that this row sees
         auto seen = [&](int c) {
-          uint32_t v = visible(c, d, mask);
+          uint32_t v = visible(c, d, mask_word & pc.node_bits());
           if (bad >> (2 * c) & 1) v &= 0xffff0000u;
           if (bad >> (2 * c + 1) & 1) v &= 0x0000ffffu;
           return v;
@@ -323,12 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
           alpha = ex2(m_used - rmax);
           m_used = rmax;
         }
+        // O is stable: S(k) was issued after P V(k - 1), and MMAs complete in order
         if (k > 0 && __any_sync(kFull, alpha != 1.f)) {
-          if (!__all_sync(kFull, wait(kBarODone + w, (units - 1) & 1))) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t o[32];
@@ -369,15 +372,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         tc::tmem_wait_st();
         l = l * alpha + (ps2.x + ps2.y);
         tc::fence_before_sync();
-        mbar_arrive(&bars[kBarPFull + w]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarPFull + w]);
       }
       if (!ok) break;
       tiles += pc.tiles;
-      other += two ? pc.tiles : (pc.tiles + w) / 2;
       // ---- end of the piece: this slot's O, and with one row tile the other's ----
-      if (mine > 0) ok = __all_sync(kFull, wait(kBarODone + w, (units - 1) & 1));
-      if (ok && theirs > 0) ok = __all_sync(kFull, wait(kBarODone + (w ^ 1), (other - 1) & 1));
+      const bool second = two || pc.tiles > 1;  // slot 1 has units
+      if (mine > 0) ok = __all_sync(kFull, wait(kBarODone + w, last[w] & 1));
+      if (ok && theirs > 0) ok = __all_sync(kFull, wait(kBarODone + (w ^ 1), last[w ^ 1] & 1));
       if (!ok) break;
+      ++last[0];
+      last[1] += second;
       tc::fence_after_sync();
       const int pn = (p_idx & 3) * 2;
       const uint64_t nan_mask = nan_nodes[pn] | static_cast<uint64_t>(nan_nodes[pn + 1]) << 32;
@@ -428,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
             }
           }
           // NaN value codes of nodes this row sees
-          for (uint64_t nm = mask & nan_mask; nm; nm &= nm - 1) {
+          for (uint64_t nm = mask_word & nan_mask; nm; nm &= nm - 1) {
             const int pos = pc.base() + __ffsll(static_cast<long long>(nm)) - 1;
             const int page = __ldg(a.block_table + static_cast<int64_t>(pc.b) * a.maxp + pos / kPage);
             if (page < 0 || page >= a.num_pages) continue;
@@ -658,9 +664,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       const int n_units = two ? 2 * pc.tiles : pc.tiles;
       // S of unit u: slot u & 1, tile u (or u / 2); two units share a K stage
       // when there are two row tiles
-      auto issue_s = [&](int u) {
+      auto issue_s = [&](int u, bool k_there) {
         const int w = u & 1;
-        if ((!two || w == 0) && !wait(kBarKFull + kr.s, kr.phase, true)) return false;
+        if ((!two || w == 0) && !k_there && !wait(kBarKFull + kr.s, kr.phase, true)) return false;
         tc::fence_after_sync();
         const int qs = two ? w : (kWide ? p_idx & 1 : 0);
         const uint64_t a0 = dq + static_cast<uint64_t>(qs * (kQBytes / 16));
@@ -686,10 +692,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         ++uses[qs];
       }
       if (!ok) break;
-      ok = issue_s(0) && (n_units < 2 || issue_s(1));
+      ok = issue_s(0, false) && (n_units < 2 || issue_s(1, false));
       for (int u = 0; ok && u < n_units; ++u) {
         const int w = u & 1;
-        ok = wait(kBarPFull + w, units[w] & 1, true);
+        // P of this unit and, where they are new, both V halves, polled
+        // together (a wait that is satisfied costs ~100 cycles by itself); the
+        // key tile of unit u + 2 is looked at on the way but not waited for
+        Ring<M::kVHalves> v1 = vr;
+        v1.next();
+        const bool fresh = !two || w == 0;
+        bool p_there = false, v0_there = !fresh, v1_there = !fresh;
+        bool k_there = !fresh || u + 2 >= n_units;
+        ok = !*abort_flag;
+        for (uint32_t i = 0; ok && !(p_there && v0_there && v1_there); ++i) {
+          if (!k_there) k_there = mbar_test_wait(&bars[kBarKFull + kr.s], kr.phase);
+          if (!v0_there) v0_there = mbar_test_wait(&bars[kBarVFull + vr.s], vr.phase);
+          if (!v1_there) v1_there = mbar_test_wait(&bars[kBarVFull + v1.s], v1.phase);
+          if (!p_there) p_there = mbar_test_wait(&bars[kBarPFull + w], units[w] & 1);
+          if (i == kMaxSpins) {
+            *abort_flag = 1;
+            flag_error(a.dev_error, K16V8_DEVERR_TIMEOUT);
+            ok = false;
+          }
+        }
         if (ok && u == 0 && p_idx > 0)  // the last piece's O tiles have been read
           ok = wait(kBarOEmpty, (p_idx - 1) & 1, true);
         if (!ok) break;
@@ -698,11 +723,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         const Ring<M::kVHalves> v0 = vr;  // both row tiles read the same halves
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (!two || w == 0) {
-            ok = wait(kBarVFull + vr.s, vr.phase, true);
-            if (!ok) break;
-            tc::fence_after_sync();
-          }
           const uint64_t b0 = dv + static_cast<uint64_t>(vr.s * (kVHalf / 16));
 #pragma unroll
           for (int kk = 0; kk < kHalf / 16; ++kk)
@@ -714,9 +734,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
           vr.next();
         }
         if (two && w == 0) vr = v0;
-        if (!ok) break;
-        if (leader) tc::mma_commit(&bars[kBarODone + w]);
-        if (u + 2 < n_units) ok = issue_s(u + 2);
+        if (leader && u + 2 >= n_units) tc::mma_commit(&bars[kBarODone + w]);
+        if (u + 2 < n_units) ok = issue_s(u + 2, k_there);
       }
     }
     // every MMA issued has to land before tensor memory is released

@@ -152,9 +152,15 @@ def _ptr(t):
 
 
 def _stream(stream) -> int | None:
-    if stream is None:  # the handle alone: building the Stream object costs 3 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return _stream_on(None, torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _stream_on(stream, dev: int) -> int:
+    """The handle of a stream, None being the current one of device dev (the
+    handle alone: building the Stream object costs 3 us)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -524,7 +530,7 @@ def k16v8_rope_kv_append(q, k, v, positions, inv_freq, slot_mapping, v_scale, q_
     row, tokens = (T, hkv, d), (T,)
     cache = (k_cache.shape[0], hkv, PAGE_SIZE, d)
     half = inv_freq.numel()
-    st = load_library().k16v8_rope_kv_append(
+    st = (_lib or load_library()).k16v8_rope_kv_append(
         q_ptr, q_ts, k.data_ptr(), _rows(k, "k", dt, row, dev), v.data_ptr(),
         _rows(v, "v", dt, row, dev), _X_DTYPES[dt],
         _dense(positions, "positions", _I32, tokens, dev),
@@ -534,8 +540,9 @@ def k16v8_rope_kv_append(q, k, v, positions, inv_freq, slot_mapping, v_scale, q_
         out_ptr,
         _dense(k_cache, "k_cache", _F16, cache, dev),
         _dense(v_cache, "v_cache", _U8, cache, dev), cache[0], hq, hkv, d,
-        _error_word(dev_error, dev), _stream(stream))
-    _check("k16v8_rope_kv_append", st)
+        _error_word(dev_error, dev), _stream_on(stream, dev))
+    if st != K16V8_OK:
+        raise K16V8Error("k16v8_rope_kv_append", st)
 
 
 def k16v8_tree_workspace_size(total_q, batch, max_nodes, num_qo_heads, num_kv_heads, head_dim,
@@ -564,7 +571,7 @@ def k16v8_paged_tree_attention(q, qo_indptr, max_nodes, tree_mask, k_cache, v_ca
     if workspace is not None:
         ws_bytes = workspace.numel() * workspace.element_size()
         ws = _dense(workspace, "workspace", workspace.dtype, workspace.shape, dev)
-    st = load_library().k16v8_paged_tree_attention(
+    st = (_lib or load_library()).k16v8_paged_tree_attention(
         _dense(q, "q", _F16, (total_q, hq, d), dev),
         _dense(qo_indptr, "qo_indptr", _I32, (B + 1,), dev), total_q, max_nodes,
         _dense(tree_mask, "tree_mask", _I64, (total_q,), dev),
@@ -575,8 +582,9 @@ def k16v8_paged_tree_attention(q, qo_indptr, max_nodes, tree_mask, k_cache, v_ca
         _dense(seq_lens, "seq_lens", _I32, (B,), dev), max_seq_len, B, hq, hkv, d, P,
         sm_scale, ws, ws_bytes, _dense(out, "out", _F16, (total_q, hq, d), dev),
         None if lse is None else _dense(lse, "lse", _F32, (total_q, hq), dev),
-        _error_word(dev_error, dev), _stream(stream))
-    _check("k16v8_paged_tree_attention", st)
+        _error_word(dev_error, dev), _stream_on(stream, dev))
+    if st != K16V8_OK:
+        raise K16V8Error("k16v8_paged_tree_attention", st)
 
 
 def _prob_rows(t, name: str, shape, dev: int) -> int:
@@ -603,7 +611,7 @@ def k16v8_tree_verify(target_probs, draft_probs, tokens, parents, qo_indptr, max
     dev = _device(target_probs)
     B = path_len.shape[0]
     shape, rows, seqs = (total_q, V), (total_q,), (B,)
-    st = load_library().k16v8_tree_verify(
+    st = (_lib or load_library()).k16v8_tree_verify(
         target_probs.data_ptr(), _prob_rows(target_probs, "target_probs", shape, dev),
         None if draft_probs is None else draft_probs.data_ptr(),
         0 if draft_probs is None else _prob_rows(draft_probs, "draft_probs", shape, dev),
@@ -614,8 +622,9 @@ def k16v8_tree_verify(target_probs, draft_probs, tokens, parents, qo_indptr, max
         _dense(path, "path", _I32, (B, max_nodes), dev),
         _dense(path_len, "path_len", _I32, seqs, dev),
         _dense(next_token, "next_token", _I32, seqs, dev), _error_word(dev_error, dev),
-        _stream(stream))
-    _check("k16v8_tree_verify", st)
+        _stream_on(stream, dev))
+    if st != K16V8_OK:
+        raise K16V8Error("k16v8_tree_verify", st)
 
 
 def layer_pointers(caches) -> torch.Tensor:
@@ -636,7 +645,7 @@ def k16v8_kv_compact(k_ptrs, v_ptrs, num_pages, num_kv_heads, head_dim, block_ta
     layers = k_ptrs.shape[0]
     B, max_nodes = path.shape
     maxp = block_table.shape[1]
-    st = load_library().k16v8_kv_compact(
+    st = (_lib or load_library()).k16v8_kv_compact(
         _dense(k_ptrs, "k_ptrs", _I64, (layers,), dev),
         _dense(v_ptrs, "v_ptrs", _I64, (layers,), dev), layers,
         _dense(block_table, "block_table", _I32, (B, maxp), dev), maxp,
@@ -647,8 +656,9 @@ def k16v8_kv_compact(k_ptrs, v_ptrs, num_pages, num_kv_heads, head_dim, block_ta
         num_pages,
         None if new_seq_lens is None else _dense(new_seq_lens, "new_seq_lens", _I32, (B,),
                                                  dev),
-        _error_word(dev_error, dev), _stream(stream))
-    _check("k16v8_kv_compact", st)
+        _error_word(dev_error, dev), _stream_on(stream, dev))
+    if st != K16V8_OK:
+        raise K16V8Error("k16v8_kv_compact", st)
 
 
 def k16v8_read_device_error(dev_error, stream=None) -> int:
