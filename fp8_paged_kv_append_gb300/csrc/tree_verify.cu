@@ -24,14 +24,21 @@
 // same accepted path and the same token.  The conversion is two additions of
 // a magic number (whose mantissa then holds the digits) with the remainder
 // carried over: every step runs at full rate, while a conversion instruction
-// to 64 bits does not (the same pass with it: 95 us against 24 at 64 x 128,000).
+// to 64 bits does not (97 against 46 us at 64 sequences x 128,000).  For the
+// same reason no thread but one does arithmetic in fp64, and only for a
+// sibling that is tried after a rejection.
 //
-// Bound by the latency of one row of p and q.  A cluster of CTAs shares a
-// sequence: each sums its slice of the vocabulary, the slices' masses are
-// exchanged through distributed shared memory, and every CTA takes the same
-// decisions from the same integers.  The walk itself reads one p and one q
-// per node, fetched for all nodes at once.  The CTA that holds the drawn number
-// scans the run of its warp that holds it with all its threads.
+// Bound by one pass over the last row of p and q, and by the chain of memory
+// round trips and cluster barriers around it (about 5 us of the kernel).  A
+// cluster of CTAs shares a sequence: each sums its slice of the vocabulary,
+// the slices' masses are exchanged through distributed shared memory, and
+// every CTA takes the same decisions from the same integers.  The walk itself
+// reads one p and one q per node, fetched for all nodes at once.  The CTA that
+// holds the drawn number scans the run of its warp that holds it with all its
+// threads.  GB300: 6.8 us for one sequence of 32,000 tokens, 10.1 us for 32 of
+// 50,257 (no draft rows), 22.0 us for 64 chains of 8 nodes over 128,000 (65.5 MB:
+// 9.7 us at the copy rate), 32.3 us for trees with two children a node, some of
+// which pass over their row two or three times.
 #include <cooperative_groups.h>
 
 #include "k16v8_device.cuh"
@@ -199,6 +206,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
   const int b = blockIdx.x / csize;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   cluster_arrive();
+  // Slices in coordinates x = j + skew that start on the row's 16-byte
+  // boundary before token 0: CTA slices and warp runs are whole 128s.
+  const int per_cta = (vocab + 3 + csize * 128 - 1) / (csize * 128) * 128;
+  const int per_warp = (per_cta + kWarps * 128 - 1) / (kWarps * 128) * 128;
+
   if (tid < kNodes) sh.child[tid][0] = sh.child[tid][1] = 0;
   pdl_wait();
   pdl_launch_dependents();
@@ -252,11 +264,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
   __syncthreads();
   cluster_wait();  // every CTA runs: their shared memory can be written from now on
 
-  // Slices in coordinates x = j + skew that start on the row's 16-byte
-  // boundary before token 0: CTA slices and warp runs are whole 128s.
-  const int per_cta = (vocab + 3 + csize * 128 - 1) / (csize * 128) * 128;
-  const int per_warp = (per_cta + kWarps * 128 - 1) / (kWarps * 128) * 128;
-
   int passes = 0, skew = 0;
   // Mass of row `cur` with the weights max(p - C q, 0) (C = 0: p alone); the
   // warps' shares stay in sh.warp_mass, the CTAs' in sh.cta_mass[parity].
@@ -282,15 +289,16 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
     if (lane == 0) sh.warp_mass[warp] = sum;
     __syncthreads();
     const int par = passes & 1;
-    if (tid < csize) {
-      int64_t cta = 0;
-      for (int w = 0; w < kWarps; ++w) cta += sh.warp_mass[w];
-      cluster.map_shared_rank(&sh, tid)->cta_mass[par][rank] = cta;
+    if (warp == 0) {
+      static_assert(kWarps <= 32, "one lane per warp");
+      const int64_t cta = warp_sum(lane < kWarps ? sh.warp_mass[lane] : 0);
+      if (lane < csize) cluster.map_shared_rank(&sh, lane)->cta_mass[par][rank] = cta;
     }
     cluster.sync();
     ++passes;
     int64_t all = 0;
-    for (int r = 0; r < csize; ++r) all += sh.cta_mass[par][r];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) all += r < csize ? sh.cta_mass[par][r] : 0;
     return all;
   };
   auto mask64 = [](const uint32_t (&m)[2]) { return m[0] | static_cast<uint64_t>(m[1]) << 32; };
@@ -369,19 +377,19 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
   int64_t t = static_cast<int64_t>((__umul64hi(static_cast<uint64_t>(mass), u63) << 1) |
                                    ((static_cast<uint64_t>(mass) * u63) >> 63));
   t = min(t, mass - 1);
-  // weight of the removed tokens inside [a, z)
-  auto removed = [&](int a, int z) {
-    int64_t s = 0;
-    for (uint64_t m = out_of; m; m &= m - 1) {
-      const int i = __ffsll(static_cast<long long>(m)) - 1;
-      if (sh.token[i] >= a && sh.token[i] < z) s += units_of(sh.p[i]);
+  if (out_of) {  // the removed tokens' weights leave the shares that hold them
+    __syncthreads();  // the shares have been read
+    if (tid < kNodes && (out_of >> tid & 1)) {
+      const int x = sh.token[tid] + skew, r = x / per_cta, w = (x - r * per_cta) / per_warp;
+      const unsigned long long u = static_cast<unsigned long long>(-units_of(sh.p[tid]));
+      atomicAdd(reinterpret_cast<unsigned long long *>(&sh.cta_mass[last][r]), u);
+      if (r == rank) atomicAdd(reinterpret_cast<unsigned long long *>(&sh.warp_mass[w]), u);
     }
-    return s;
-  };
+    __syncthreads();
+  }
   int owner = 0;
   for (; owner < csize - 1; ++owner) {
-    const int a = owner * per_cta - skew;
-    const int64_t m = sh.cta_mass[last][owner] - removed(a, a + per_cta);
+    const int64_t m = sh.cta_mass[last][owner];
     if (t < m) break;
     t -= m;
   }
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
     const int c0 = rank * per_cta;
     a = c0 + w * per_warp - skew;
     z = min(vocab, min(c0 + per_cta, c0 + (w + 1) * per_warp) - skew);
-    const int64_t m = sh.warp_mass[w] - removed(a, z);
+    const int64_t m = sh.warp_mass[w];
     if (t < m || w == kWarps - 1) break;
     t -= m;
   }
@@ -482,8 +490,8 @@ extern "C" int32_t k16v8_tree_verify(const float *target_probs, int64_t target_r
       !k16v8_aligned(next_token, 4))
     return K16V8_ERR_INVALID_ARG;
   if (batch > 0x7fffffff / verify::kMaxCluster) return K16V8_ERR_INVALID_ARG;
-  // CTAs per sequence: as many as keep the whole batch on the SMs at once,
-  // two CTAs each
+  // CTAs per sequence: as many as keep the whole batch on the SMs at once, two
+  // CTAs each.  64 chains over 128,000: 4 CTAs each 22.0 us, 8 (two waves) 28.7.
   const int sms = k16v8_sm_count();
   if (sms <= 0) return K16V8_ERR_CUDA;
   int cluster = verify::kMaxCluster;
