@@ -15,19 +15,37 @@
 //    piece.  K and V are read once and every MMA row block works on another
 //    KV tile;
 //  * wider trees: two row tiles, both over every KV tile.
-// A unit is one (KV tile, slot): S = Q K^T, softmax, O += P V.
+// A unit is one (KV tile, slot): S = Q K^T, softmax, O += P V.  Where wide
+// trees may be among the batch a unit is worked on in two parts of 64
+// positions, each with half of the slot's S columns, so that one part's S and
+// P V run under the other's softmax.
 //
 // Warp roles (16 warps): 0-3 / 4-7 softmax of slot 0 / 1, one thread per row;
-// 8, 10, 11, 14 dequantise V (E4M3 pages -> fp16 MN-major half tiles); 9 issues
-// the MMAs; 13 loads Q and K pages (TMA); 12 loads the E4M3 pages (bulk
-// copies); 15 walks the CTA's pieces and hands them to the others.  Every
-// hand-off is an mbarrier, every wait is bounded.
+// 8, 10, 11, 14 dequantise V (E4M3 pages -> fp16 MN-major half tiles); 15
+// issues S = Q K^T and 9 O += P V; 13 loads Q and K pages (TMA); 12 loads the
+// E4M3 pages (bulk copies), walks the CTA's pieces and hands them to the
+// others.  Every hand-off is an mbarrier, every wait is bounded.
 //
 // What it is built around (cycles at 1.96 GHz, from time stamps of one CTA; a
 // KV tile at the full memory rate takes 2,150):
-//  * The softmax loops are kept rolled up: each warp runs its role's code once
+//  * An S MMA with both operands in shared memory takes the whole 128 bytes a
+//    cycle (64 cycles per 128 x 128 x 16), and everything else in shared memory
+//    waits: the test of a barrier takes 140-300 cycles.  So the warps that issue
+//    MMAs test all their barriers at once, one per lane, and keep what they
+//    learned (174 -> 168 us on 16 x 64 nodes at 8K); S and P V are issued by a
+//    warp each, because the issue of one unit takes ~1,000 cycles of one warp
+//    (173 -> 167 us).  Parts of 64 positions cost S a third of its rate (55
+//    cycles per 128 x 64 x 16) and still gain for two row tiles, where MMAs and
+//    softmax alternate otherwise (175 -> 168 us); for one row tile they gain
+//    nothing (95.1 and 95.2 us on 8 nodes at 128K) and are not used.
+//  * Nothing is in local memory: what L1 has left beside the operand stages is
+//    so little that a spilled register or an array indexed at run time costs a
+//    trip to L2 (~700 cycles) each time (46.8 -> 41.4 us on 32 x 8 nodes at 1.1K).
+//  * The maximum of a row comes with the load (tcgen05.ld.red), and 16 columns
+//    are on their way while 16 are exponentiated (103 -> 100 us on 32 nodes at
+//    128K).  The loops are kept rolled up: each warp runs its role's code once
 //    per tile, and unrolled over the 128 columns that code came from the far
-//    side of the instruction cache (4,000 cycles a tile, against 2,100).
+//    side of the instruction cache (4,000 cycles a tile, against 1,500).
 //  * The whole MMA warp walks the units and one elected lane issues: operands
 //    stay in uniform registers (3,030 -> 1,900 cycles a unit).
 //  * A bulk or tensor copy takes its lane ~90 cycles to issue, so K and V have
@@ -35,8 +53,12 @@
 //    hides (143 against 131 us on 8 nodes at 128K).
 //  * A copy lands ~2,000-3,000 cycles after it is issued: three stages each
 //    (two of K for wide trees, whose tiles take longer).
-//  * A piece's description takes several memory round trips to work out: one
-//    warp does that ahead of time.
+//  * A piece's description may take memory round trips to work out (the next
+//    sequence's lengths): that is done one piece ahead, behind the copies of
+//    the piece's first tile.
+// What a call takes now: 8 nodes at 128K 95 us (5.3 TB/s of K and V), 16 x 8
+// nodes at 8K 94 us, 16 x 64 nodes at 8K 158 us (1.1 PFLOP/s), 32 x 16 nodes at
+// 1.1K 44 us, one tree of 5 at 1K 12 us, the merge included.
 #pragma once
 
 #include "k16v8_device.cuh"
@@ -54,11 +76,11 @@ constexpr int kRows = kNodes * kGroup;       // 128
 constexpr int kKv = 128;                     // positions per KV tile
 constexpr int kPagesPerTile = kKv / kPage;   // 8
 constexpr int kThreads = 512;
-constexpr int kMmaWarp = 9, kLoadVWarp = 12, kLoadKWarp = 13, kPieceWarp = 15;
+constexpr int kOutWarp = 9, kLoadVWarp = 12, kLoadKWarp = 13, kScoreWarp = 15;
 constexpr int kDequantWarps = 4;
 constexpr int kDequantThreads = kDequantWarps * 32;
 constexpr int kPieceRing = 4;
-constexpr int kPieceReaders = 8 + kDequantWarps + 3;  // warps
+constexpr int kPieceReaders = 8 + kDequantWarps + 4;  // warps
 
 // Rank of a dequant warp among them, or -1.
 __device__ __forceinline__ int dequant_rank(int warp) {
@@ -74,9 +96,12 @@ constexpr uint32_t kVBlk = kHalf * 128;        // [64 pos][64 dims] fp16
 constexpr uint32_t kVHalf = 2 * kVBlk;
 constexpr uint32_t kTmemCols = 512;  // S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512)
 
+constexpr uint32_t kBarBytes = 448;
+
 // kWide: trees of more than 32 nodes may be among the batch.
 template <bool kWide>
 struct Smem {
+  static constexpr int kParts = kWide ? 2 : 1;  // of a unit
   static constexpr int kQSlots = kWide ? 2 : 1;
   // stages: with two row tiles a V tile is held until both have read it, so
   // two whole ones are needed; else a half tile is free as soon as it is read
@@ -88,7 +113,7 @@ struct Smem {
   static constexpr uint32_t kVst = kK + kKStages * kKStage;
   static constexpr uint32_t kV = kVst + kVstStages * kVstStage;
   static constexpr uint32_t kBar = kV + kVHalves * kVHalf;
-  static constexpr uint32_t kPieces = kBar + 384;
+  static constexpr uint32_t kPieces = kBar + kBarBytes;
   static constexpr uint32_t kInfo = kPieces + kPieceRing * sizeof(Piece);
   static constexpr uint32_t kNan = kInfo + 16 * 4;   // tree nodes with NaN value codes
   static constexpr uint32_t kStat = kNan + 4 * 8;    // [slot][max, sum][row]
@@ -108,17 +133,31 @@ enum {
   kBarVstEmpty = 13,  // +stage, kDequantThreads arrivals
   kBarVFull = 16,     // +half, kDequantThreads arrivals
   kBarVEmpty = 20,    // +half
-  kBarSFull = 24,     // +slot
-  kBarPFull = 26,     // +slot, 4 arrivals (one per warp)
-  kBarODone = 28,     // +slot: the slot's last P V of a piece
-  kBarOEmpty = 30,    // 8 arrivals: both O tiles have been read
-  kBarJoin = 31,      // 256 arrivals: both slots' statistics are in shared memory
-  kBarPiece = 32,     // +ring entry: described
-  kBarTaken = 36,     // +ring entry: kPieceReaders arrivals
-  kBarDrain = 40,
-  kNumBars = 41
+  kBarSFull = 24,     // +slot + 2 * part
+  kBarPFull = 28,     // +slot + 2 * part, 4 arrivals (one per warp)
+  kBarPV = 32,        // +slot + 2 * part: the part's P V is done
+  kBarODone = 36,     // +slot: the slot's last P V of a piece
+  kBarOEmpty = 38,    // 8 arrivals: both O tiles have been read
+  kBarJoin = 39,      // 256 arrivals: both slots' statistics are in shared memory
+  kBarPiece = 40,     // +ring entry: described
+  kBarTaken = 44,     // +ring entry: kPieceReaders arrivals
+  kBarDrain = 48,     // +0, 1: every S, every P V
+  kNumBars = 50
 };
-static_assert(kNumBars * 8 + 16 <= 384, "barriers");
+static_assert(kNumBars * 8 + 16 <= kBarBytes, "barriers");
+
+// A count for either slot.  (Arrays indexed at run time would live in local
+// memory, behind the little L1 that the operand stages leave.)
+struct Pair {
+  uint32_t c0 = 0, c1 = 0;
+  __device__ __forceinline__ uint32_t operator[](int w) const { return w ? c1 : c0; }
+  __device__ __forceinline__ void add(int w, uint32_t n = 1) {
+    if (w)
+      c1 += n;
+    else
+      c0 += n;
+  }
+};
 
 // Position in a ring of n stages: the stage, and the parity of its phase.
 template <int n>
@@ -153,14 +192,19 @@ __device__ __forceinline__ bool cta_wait(uint64_t *bar, uint32_t parity, volatil
   return false;
 }
 
-// Visible columns 32c .. 32c + 31 of a tile whose first position is base - d,
-// for a row with tree mask m (bits below n only): bits of the word.
-__device__ __forceinline__ uint32_t visible(int c, int d, uint64_t m) {
-  const int rel = 32 * c - d;  // position of the word's first column behind base
-  if (rel <= -32) return 0xffffffffu;
-  if (rel >= 64) return 0u;
-  if (rel < 0) return ((1u << -rel) - 1u) | static_cast<uint32_t>(m << -rel);
-  return static_cast<uint32_t>(m >> rel);
+// The 128 columns of a tile, or 64 of one part, that a row sees.
+struct Columns {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ uint32_t word(const Columns &s, int c) {
+  return static_cast<uint32_t>((c & 2 ? s.hi : s.lo) >> (c & 1) * 32);
+}
+// 64 columns from the one `rel` behind the first node, for a row with tree mask m.
+__device__ __forceinline__ uint64_t visible(int rel, uint64_t m) {
+  if (rel <= -64) return ~0ull;
+  if (rel >= 64) return 0ull;
+  if (rel < 0) return ((1ull << -rel) - 1) | m << -rel;
+  return m >> rel;
 }
 
 // Page id of page `lane` of a piece's tile t: -1 outside the pool, -2 behind
@@ -172,11 +216,41 @@ __device__ __forceinline__ int page_id(const Args &a, const Piece &p, int t, int
   return pid >= 0 && pid < a.num_pages ? pid : -1;
 }
 
+// An asynchronous load's registers stay its own until here.
+__device__ __forceinline__ void keep(const uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" ::"r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]),
+                 "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7]));
+}
+
+// p = 2^(s * scale - m) of 16 scores: fp16 to tensor memory, their sum in fp32.
+template <bool kMask>
+__device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[16], uint32_t seen,
+                                          float2 scale, float2 neg_m, float2 &sum) {
+  uint32_t pk[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float2 x = __ffma2_rn(
+        make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale, neg_m);
+    float2 p = make_float2(ex2(x.x), ex2(x.y));
+    if (kMask) {
+      if (!(seen >> (2 * e) & 1)) p.x = 0.f;
+      if (!(seen >> (2 * e + 1) & 1)) p.y = 0.f;
+    }
+    sum = __fadd2_rn(sum, p);
+    const __half2 h = __floats2half2_rn(p.x, p.y);
+    pk[e] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  tc::tmem_st8(t_p, pk);
+}
+
 template <bool kWide>
 __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
     const Args a) {
   using M = Smem<kWide>;
+  constexpr int kParts = M::kParts, kChunks = 4 / kParts;  // of a tile; of 32 columns
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sQ = smem_raw + M::kQ;
   uint8_t *sK = smem_raw + M::kK;
@@ -216,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
       if (i >= kBarVstEmpty && i < kBarVEmpty) count = kDequantThreads;
-      if (i == kBarPFull || i == kBarPFull + 1) count = 4;
+      if (i >= kBarPFull && i < kBarPV) count = 4;
       if (i == kBarJoin) count = 2 * kRows;
       if (i == kBarOEmpty) count = 8;
       if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
@@ -227,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     fence_barrier_init();
   }
   pdl_wait();
-  if (tid == kPieceWarp * 32) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (tid == kLoadVWarp * 32) a.cut[blockIdx.x] = make_int4(-1, 0, 0, 0);
   // ---- this CTA's range of the work (scratch: the operand stages) ----
   constexpr Shape kShape{kKv, kNodes};
   const Range range = plan_range(a, kShape, kWide ? 2 : 1, reinterpret_cast<int64_t *>(smem_raw),
@@ -262,128 +336,151 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     const uint32_t tS = tmem + w * 128;
     const uint32_t tO = tmem + 256 + w * 128;
     const uint32_t tOther = tmem + 256 + (w ^ 1) * 128;
-    Piece pc;
     Ring<kPieceRing> ring;
     uint32_t units = 0;             // of this slot so far
-    uint32_t last[2] = {0, 0};      // pieces in which a slot had units, so far
+    Pair last;                      // pieces in which a slot had units, so far
     uint32_t tiles = 0;             // of the CTA so far
     bool ok = true;
-    for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
+    for (uint32_t p_idx = 0; ok; ++p_idx) {
+      // the piece stays in shared memory: registers are short here
+      if (!__all_sync(kFull, wait(kBarPiece + ring.s, ring.phase))) break;
+      const Piece &pc = pieces[ring.s];
+      if (pc.tiles == 0) break;
       const bool two = kWide && pc.n > kNodes;  // two row tiles
       const int node = (two ? w * kNodes : 0) + (r >> 2);
       const bool row_valid = node < pc.n;
       const bool warp_live = (two ? w * kNodes : 0) + (warp & 3) * 8 < pc.n;
-      const uint64_t mask_word = row_valid ? __ldg(a.tree_mask + pc.q0 + node) : 0;  // used late
+      const uint64_t mask_word =
+          row_valid ? __ldg(a.tree_mask + pc.q0 + node) & pc.node_bits() : 0;  // used late
       const float vs = __ldg(a.v_scale + pc.g);
       const int mine = two ? pc.tiles : (pc.tiles + 1 - w) / 2;
+      const int n_tiles = pc.tiles, d0 = pc.base() - pc.t0 * kKv;
       const int theirs = two ? 0 : (pc.tiles + w) / 2;  // units of the other slot to join
       float m_used = -INFINITY, l = 0.f;
-      for (int k = 0; k < mine; ++k, ++units) {
-        if (!__all_sync(kFull, wait(kBarSFull + w, units & 1))) {
-          ok = false;
-          break;
-        }
-        if (!warp_live) {
-          if (lane == 0) mbar_arrive(&bars[kBarPFull + w]);
-          continue;
-        }
-        tc::fence_after_sync();
-        const int tile = two ? k : 2 * k + w;
-        const int d = pc.base() - (pc.t0 + tile) * kKv;  // prefix columns of this tile
-        const uint32_t bad = info[(tiles + tile) & 7];
-        const bool need_mask = d < kKv || bad;
-        // columns 32c .. 32c + 31 that this row sees
-        auto seen = [&](int c) {
-          uint32_t v = visible(c, d, mask_word & pc.node_bits());
-          if (bad >> (2 * c) & 1) v &= 0xffff0000u;
-          if (bad >> (2 * c + 1) & 1) v &= 0x0000ffffu;
-          return v;
-        };
-        // pass 1: row max
-        float rmax = -INFINITY;
+      for (int k = 0; ok && k < mine; ++k, ++units) {
 #pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          uint32_t sr[2][32];
-          tc::tmem_ld32(tS + lane_base + h * 64, sr[0]);
-          tc::tmem_ld32(tS + lane_base + h * 64 + 32, sr[1]);
-          tc::tmem_wait_ld();
+        for (int part = 0; part < kParts; ++part) {
+          if (!__all_sync(kFull, wait(kBarSFull + w + 2 * part, units & 1))) {
+            ok = false;
+            break;
+          }
+          if (!warp_live) {
+            if (lane == 0) mbar_arrive(&bars[kBarPFull + w + 2 * part]);
+            continue;
+          }
+          tc::fence_after_sync();
+          const int tile = two ? k : 2 * k + w;
+          const int d = d0 - tile * kKv;  // prefix columns of this tile
+          const uint32_t bad = info[(tiles + tile) & 7];
+          const bool need_mask = d < kKv || bad;
+          Columns seen{0, 0};
           if (need_mask) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const uint32_t v = seen(2 * h + c);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (v >> e & 1) rmax = fmaxf(rmax, __uint_as_float(sr[c][e]));
+            seen.lo = visible(part * 64 - d, mask_word);
+            if (kParts == 1) seen.hi = visible(64 - d, mask_word);
+            for (uint32_t pages = bad >> 4 * part; pages; pages &= pages - 1) {
+              const int page = __ffs(static_cast<int>(pages)) - 1;
+              const uint64_t out = 0xffffull << (page & 3) * 16;
+              if (page < 4)
+                seen.lo &= ~out;
+              else if (kParts == 1)
+                seen.hi &= ~out;
+            }
+          }
+          const uint32_t tSp = tS + lane_base + part * kChunks * 32;
+          // pass 1: row max
+          float rmax = -INFINITY;
+          if (!need_mask) {
+#pragma unroll 1
+            for (int c = kChunks - 2; c >= 0; c -= 2) {
+              uint32_t s0[32], s1[32];
+              float m0, m1;
+              tc::tmem_ld32_max(tSp + c * 32 + 32, s1, m1);
+              tc::tmem_ld32_max(tSp + c * 32, s0, m0);
+              tc::tmem_wait_ld();
+              keep(s1);
+              keep(s0);
+              rmax = fmaxf(rmax, fmaxf(m0, m1));
             }
           } else {
-            float m4[4] = {rmax, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; ++e) m4[e & 3] = fmaxf(m4[e & 3], __uint_as_float(sr[c][e]));
-            rmax = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          }
-        }
-        rmax *= qk_scale;
-        float alpha = 1.f;
-        if (rmax > m_used + 8.f) {
-          alpha = ex2(m_used - rmax);
-          m_used = rmax;
-        }
-        // O is stable: S(k) was issued after P V(k - 1), and MMAs complete in order
-        if (k > 0 && __any_sync(kFull, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tc::tmem_ld32(tO + lane_base + c * 32, o);
-            tc::tmem_wait_ld();
+            for (int c = 0; c < kChunks; ++c) {
+              uint32_t s0[32];
+              tc::tmem_ld32(tSp + c * 32, s0);
+              tc::tmem_wait_ld();
+              const uint32_t v = word(seen, c);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st32(tO + lane_base + c * 32, o);
-          }
-        }
-        // pass 2: p = 2^(s * scale - m), fp32 row sum, P (fp16) over the S columns read
-        const float neg = m_used == -INFINITY ? 0.f : -m_used;
-        const float2 sc2 = make_float2(qk_scale, qk_scale);
-        const float2 nm2 = make_float2(neg, neg);
-        float2 ps2 = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t sr[32];
-          tc::tmem_ld32(tS + lane_base + c * 32, sr);
-          tc::tmem_wait_ld();
-          uint32_t pk[16];
-          const uint32_t v = need_mask ? seen(c) : kFull;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 x = __ffma2_rn(
-                make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sc2, nm2);
-            float2 pp = make_float2(ex2(x.x), ex2(x.y));
-            if (need_mask) {
-              if (!(v >> (2 * e) & 1)) pp.x = 0.f;
-              if (!(v >> (2 * e + 1) & 1)) pp.y = 0.f;
+              for (int e = 0; e < 32; ++e)
+                if (v >> e & 1) rmax = fmaxf(rmax, __uint_as_float(s0[e]));
             }
-            ps2 = __fadd2_rn(ps2, pp);
-            const __half2 hh = __floats2half2_rn(pp.x, pp.y);
-            pk[e] = *reinterpret_cast<const uint32_t *>(&hh);
           }
-          tc::tmem_st16(tS + lane_base + c * 16, pk);
+          rmax *= qk_scale;
+          float alpha = 1.f;
+          if (rmax > m_used + 8.f) {
+            alpha = ex2(m_used - rmax);
+            m_used = rmax;
+          }
+          if (k + part > 0 && __any_sync(kFull, alpha != 1.f)) {
+            // S of this part was issued after the P V of the part kParts before it;
+            // any in between have to be done as well
+            if (kParts > 1) {
+              if (!__all_sync(kFull, wait(kBarPV + w + 2 * (part ^ 1), (units + part + 1) & 1))) {
+                ok = false;
+                break;
+              }
+              tc::fence_after_sync();
+            }
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tc::tmem_ld32(tO + lane_base + c * 32, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc::tmem_st32(tO + lane_base + c * 32, o);
+            }
+          }
+          // pass 2: p = 2^(s * scale - m), fp32 row sum, P (fp16) over the S columns read
+          const float neg = m_used == -INFINITY ? 0.f : -m_used;
+          const float2 sc2 = make_float2(qk_scale, qk_scale);
+          const float2 nm2 = make_float2(neg, neg);
+          float2 ps2 = make_float2(0.f, 0.f);
+          uint32_t s0[16], s1[16];
+          if (!need_mask) {  // 16 columns are on their way while 16 are worked on
+            tc::tmem_ld16(tSp, s0);
+            tc::tmem_wait_ld();
+#pragma unroll 1
+            for (int c = 0; c < kChunks; ++c) {
+              tc::tmem_ld16(tSp + c * 32 + 16, s1);
+              exp_chunk<false>(tSp + c * 16, s0, 0, sc2, nm2, ps2);
+              tc::tmem_wait_ld();
+              tc::tmem_ld16(tSp + ((c + 1) & (kChunks - 1)) * 32, s0);  // (the last is unused)
+              exp_chunk<false>(tSp + c * 16 + 8, s1, 0, sc2, nm2, ps2);
+              tc::tmem_wait_ld();
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 2 * kChunks; ++c) {
+              tc::tmem_ld16(tSp + c * 16, s0);
+              tc::tmem_wait_ld();
+              exp_chunk<true>(tSp + c * 8, s0, word(seen, c >> 1) >> ((c & 1) * 16), sc2, nm2, ps2);
+            }
+          }
+          tc::tmem_wait_st();
+          l = l * alpha + (ps2.x + ps2.y);
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarPFull + w + 2 * part]);
         }
-        tc::tmem_wait_st();
-        l = l * alpha + (ps2.x + ps2.y);
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarPFull + w]);
       }
       if (!ok) break;
-      tiles += pc.tiles;
+      tiles += n_tiles;
       // ---- end of the piece: this slot's O, and with one row tile the other's ----
       const bool second = two || pc.tiles > 1;  // slot 1 has units
       if (mine > 0) ok = __all_sync(kFull, wait(kBarODone + w, last[w] & 1));
       if (ok && theirs > 0) ok = __all_sync(kFull, wait(kBarODone + (w ^ 1), last[w ^ 1] & 1));
       if (!ok) break;
-      ++last[0];
-      last[1] += second;
+      last.add(0);
+      last.add(1, second);
       tc::fence_after_sync();
       const int pn = (p_idx & 3) * 2;
       const uint64_t nan_mask = nan_nodes[pn] | static_cast<uint64_t>(nan_nodes[pn + 1]) << 32;
@@ -411,26 +508,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       const float lse = dead ? -INFINITY : (m_all + lg2(l_all)) * kLn2;
       const float g_own = f_own * inv, g_other = f_other * inv;
       // with one row tile, slot w's warps write dims 64w .. 64w + 63 of every row
-      const int c_lo = two ? 0 : 2 * w, c_hi = two ? 4 : 2 * w + 2;
+      const int c_lo = two ? 0 : 4 * w, c_hi = two ? 8 : 4 * w + 4;  // 16 dims each
       const int row = (two ? w * kRows : 0) + r;  // of the segment
       const int64_t orow = static_cast<int64_t>(pc.q0 + node) * hq + pc.g * kGroup + (r & 3);
       if (warp_live) {
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {
-          float o[32];
+          float o[16];
           {
-            uint32_t x[32];
+            uint32_t x[16];
             if (mine > 0) {
-              tc::tmem_ld32(tO + lane_base + c * 32, x);
+              tc::tmem_ld16(tO + lane_base + c * 16, x);
               tc::tmem_wait_ld();
             }
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = mine > 0 ? __uint_as_float(x[e]) * g_own : 0.f;
+            for (int e = 0; e < 16; ++e) o[e] = mine > 0 ? __uint_as_float(x[e]) * g_own : 0.f;
             if (theirs > 0) {
-              tc::tmem_ld32(tOther + lane_base + c * 32, x);
+              tc::tmem_ld16(tOther + lane_base + c * 16, x);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(x[e]), g_other, o[e]);
+              for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(x[e]), g_other, o[e]);
             }
           }
           // NaN value codes of nodes this row sees
@@ -439,15 +536,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
             const int page = __ldg(a.block_table + static_cast<int64_t>(pc.b) * a.maxp + pos / kPage);
             if (page < 0 || page >= a.num_pages) continue;
             const uint8_t *vr = a.v_cache + ((static_cast<int64_t>(page) * a.hkv + pc.g) * kPage +
-                                             pos % kPage) * kHeadDim + c * 32;
+                                             pos % kPage) * kHeadDim + c * 16;
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
+            for (int e = 0; e < 16; ++e)
               if ((__ldg(vr + e) & 0x7f) == 0x7f) o[e] = NAN;
           }
           if (row_valid && pc.whole) {
-            uint4 *po = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + c * 32);
+            uint4 *po = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + c * 16);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               uint32_t pk[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -457,9 +554,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
               po[q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           } else if (row_valid) {
-            float4 *po = a.part_o + (static_cast<int64_t>(pc.slot) * 32 + c * 8) * a.max_rows + row;
+            float4 *po = a.part_o + (static_cast<int64_t>(pc.slot) * 32 + c * 4) * a.max_rows + row;
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
+            for (int q = 0; q < 4; ++q)
               po[static_cast<int64_t>(q) * a.max_rows] =
                   make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
@@ -473,7 +570,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       }
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarOEmpty]);  // O is read: the next piece may write it
+      if (lane == 0) {
+        mbar_arrive(&bars[kBarOEmpty]);  // O is read: the next piece may write it
+        mbar_arrive(&bars[kBarTaken + ring.s]);
+      }
+      ring.next();
     }
     pdl_launch_dependents();
   } else if (dequant_rank(warp) >= 0) {
@@ -553,12 +654,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       }
     }
   } else if (warp == kLoadVWarp) {
-    // ================= V loads =================
+    // ================= V loads, and the CTA's pieces =================
+    // Lane 0 also walks the pieces: the first at the start, the next one behind
+    // the copies of a piece's first tile.
+    Walker walker;
+    Ring<kPieceRing> out;
+    bool more = true;
+    if (lane == 0) walker.init(a, kShape, range);
+    auto describe = [&]() {
+      bool done = true;
+      if (lane == 0 && more) {
+        done = !out.wrapped || wait(kBarTaken + out.s, out.phase ^ 1);
+        if (done) {
+          Piece p;
+          more = walker.next(a, kShape, range, p);
+          if (!more) p.tiles = 0;  // the end
+          pieces[out.s] = p;
+          mbar_arrive(&bars[kBarPiece + out.s]);
+          out.next();
+        }
+      }
+      return __all_sync(kFull, done) != 0;
+    };
     Piece pc;
     Ring<kPieceRing> ring;
     Ring<M::kVstStages> dst;
     uint32_t issued = 0;
-    bool ok = true;
+    bool ok = describe();
     while (ok && get_piece(pc, ring)) {
       int pid = page_id(a, pc, pc.t0, lane);
       for (int t = pc.t0; t < pc.t1; ++t) {
@@ -580,6 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         __syncwarp();
         dst.next();
         ++issued;
+        if (t == pc.t0) ok = ok && describe();
+        if (!ok) break;
       }
     }
     // let the copies issued last land before shared memory is released
@@ -592,7 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     Piece pc;
     Ring<kPieceRing> ring;
     Ring<M::kKStages> dst;
-    uint32_t issued = 0, uses[2] = {0, 0};
+    uint32_t issued = 0;
+    Pair uses;
     bool ok = true;
     for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
       int pid = page_id(a, pc, pc.t0, lane);
@@ -622,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
             const int qs = two ? i : (kWide ? p_idx & 1 : 0);
             if (uses[qs] > 0) ok = __all_sync(kFull, wait(kBarQEmpty + qs, (uses[qs] - 1) & 1));
             if (!ok) break;
-            ++uses[qs];
+            uses.add(qs);
             if (lane == 0) {
               mbar_arrive_expect_tx(&bars[kBarQFull + qs], kQBytes);
               for (int h = 0; h < 2; ++h)
@@ -643,121 +768,156 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         if (uses[s] > 0) mbar_wait_bounded(&bars[kBarQFull + s], (uses[s] - 1) & 1);
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    // ================= MMA issue =================
-    // The whole warp walks the units, so every operand stays uniform; one lane
-    // issues.
+  } else if (warp == kScoreWarp || warp == kOutWarp) {
+    // ================= MMA issue: S = Q K^T by one warp, O += P V by the other =================
+    // Each whole warp walks the units, so every operand stays uniform; one lane
+    // issues.  Every lane tests one barrier, for the phase that its next use
+    // needs, and a unit waits for those in a mask: a test takes ~140 cycles, and
+    // what a unit's issue takes bounds the tile.
     const bool leader = tc::elect_one();
-    constexpr uint32_t kIdescQK = tc::idesc_f16_f32(kRows, kKv, false, false);
-    constexpr uint32_t kIdescPV = tc::idesc_f16_f32(kRows, kHeadDim, false, true);
-    const uint64_t dq = tc::smem_desc_sw128(smem_addr(sQ), 16, 1024);
-    const uint64_t dk = tc::smem_desc_sw128(smem_addr(sK), 16, 1024);
-    const uint64_t dv = tc::smem_desc_sw128(smem_addr(sV), kVBlk, 1024);
+    uint64_t *bar = bars;  // this lane's
+    uint32_t parity = 0;
+    uint32_t ready = 0;  // lanes whose barrier is known to be there
+    auto poll = [&](uint32_t need) {
+      for (uint32_t i = 0; (ready & need) != need; ++i) {
+        ready = __ballot_sync(kFull, mbar_test_wait(bar, parity));
+        if ((i & 255u) == 255u && (i >= kMaxSpins || *abort_flag)) {
+          if (!*abort_flag) flag_error(a.dev_error, K16V8_DEVERR_TIMEOUT);
+          *abort_flag = 1;
+          return false;
+        }
+      }
+      tc::fence_after_sync();
+      return true;
+    };
+    auto used = [&](uint32_t lanes) {
+      parity ^= lanes >> lane & 1u;
+      ready &= ~lanes;
+    };
     Piece pc;
     Ring<kPieceRing> ring;
-    Ring<M::kKStages> kr;  // next K stage to use
-    Ring<M::kVHalves> vr;     // next V half to use
-    uint32_t uses[2] = {0, 0}, units[2] = {0, 0};
     bool ok = true;
-    for (uint32_t p_idx = 0; ok && get_piece(pc, ring, true); ++p_idx) {
-      const bool two = kWide && pc.n > kNodes;
-      const int n_units = two ? 2 * pc.tiles : pc.tiles;
-      // S of unit u: slot u & 1, tile u (or u / 2); two units share a K stage
-      // when there are two row tiles
-      auto issue_s = [&](int u, bool k_there) {
-        const int w = u & 1;
-        if ((!two || w == 0) && !k_there && !wait(kBarKFull + kr.s, kr.phase, true)) return false;
-        tc::fence_after_sync();
-        const int qs = two ? w : (kWide ? p_idx & 1 : 0);
-        const uint64_t a0 = dq + static_cast<uint64_t>(qs * (kQBytes / 16));
-        const uint64_t b0 = dk + static_cast<uint64_t>(kr.s * (kKStage / 16));
+    if (warp == kScoreWarp) {
+      constexpr uint32_t kIdesc = tc::idesc_f16_f32(kRows, kKv / kParts, false, false);
+      const uint64_t dk = tc::smem_desc_sw128(smem_addr(sK), 16, 1024);
+      const uint32_t dk_lo = static_cast<uint32_t>(dk), d_hi = static_cast<uint32_t>(dk >> 32);
+      const uint32_t dq_lo = dk_lo + (M::kQ >> 4) - (M::kK >> 4);
+      // lane 0: the K stage; 1 + slot + 2 * part: P V of the S tile's last use
+      // (the first passes); 5, 6: the query
+      constexpr uint32_t kK = 1u, kPV = 2u, kQ = 32u;
+      Ring<M::kKStages> kr;
+      bar += lane == 0 ? kBarKFull : lane <= 4 ? kBarPV + lane - 1 : kBarQFull + (lane == 6);
+      parity = lane >= 1 && lane <= 4;
+      for (uint32_t p_idx = 0; ok && get_piece(pc, ring, true); ++p_idx) {
+        const bool two = kWide && pc.n > kNodes;
+        const int slots = two ? 2 : 1;
+        const int q0 = kWide && !two ? p_idx & 1 : 0;  // the first slot's query
+        const int tiles = pc.tiles;
+        for (int t = 0; ok && t < tiles; ++t) {
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+#pragma unroll 1
+            for (int i = 0; i < slots; ++i) {
+              const int w = two ? i : t & 1;
+              const int tile = w + 2 * part;
+              uint32_t need = kPV << tile;
+              if (part == 0 && i == 0) need |= kK;
+              if (t == 0 && part == 0) need |= kQ << (q0 + i);
+              ok = poll(need);
+              if (!ok) break;
+              used(kPV << tile);
+              const uint32_t a0 = dq_lo + (q0 + i) * (kQBytes / 16);
+              const uint32_t b0 = dk_lo + kr.s * (kKStage / 16) + part * (kKBlk / kParts / 16);
+              const uint32_t d = tmem + w * 128 + part * (kKv / kParts);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint64_t ao = static_cast<uint64_t>((kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2);
-          const uint64_t bo = static_cast<uint64_t>((kk >> 2) * (kKBlk / 16) + (kk & 3) * 2);
-          if (leader) tc::mma_f16_ss(tmem + w * 128, a0 + ao, b0 + bo, kIdescQK, kk > 0);
-        }
-        if (leader) tc::mma_commit(&bars[kBarSFull + w]);
-        if (!two || w == 1) {
+              for (int kk = 0; kk < 8; ++kk)
+                if (leader)
+                  tc::mma_f16_ss(d, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, d_hi,
+                                 b0 + (kk >> 2) * (kKBlk / 16) + (kk & 3) * 2, d_hi, kIdesc, kk > 0);
+              if (leader) tc::mma_commit(&bars[kBarSFull + tile]);
+            }
+            if (!ok) break;
+          }
           if (leader) tc::mma_commit(&bars[kBarKEmpty + kr.s]);
           kr.next();
-        }
-        // the last S that reads this query
-        if (leader && u + (two ? 2 : 1) >= n_units) tc::mma_commit(&bars[kBarQEmpty + qs]);
-        return true;
-      };
-      for (int i = 0; ok && i < (two ? 2 : 1); ++i) {
-        const int qs = two ? i : (kWide ? p_idx & 1 : 0);
-        ok = wait(kBarQFull + qs, uses[qs] & 1, true);
-        ++uses[qs];
-      }
-      if (!ok) break;
-      ok = issue_s(0, false) && (n_units < 2 || issue_s(1, false));
-      for (int u = 0; ok && u < n_units; ++u) {
-        const int w = u & 1;
-        // P of this unit and, where they are new, both V halves, polled
-        // together (a wait that is satisfied costs ~100 cycles by itself); the
-        // key tile of unit u + 2 is looked at on the way but not waited for
-        Ring<M::kVHalves> v1 = vr;
-        v1.next();
-        const bool fresh = !two || w == 0;
-        bool p_there = false, v0_there = !fresh, v1_there = !fresh;
-        bool k_there = !fresh || u + 2 >= n_units;
-        ok = !*abort_flag;
-        for (uint32_t i = 0; ok && !(p_there && v0_there && v1_there); ++i) {
-          if (!k_there) k_there = mbar_test_wait(&bars[kBarKFull + kr.s], kr.phase);
-          if (!v0_there) v0_there = mbar_test_wait(&bars[kBarVFull + vr.s], vr.phase);
-          if (!v1_there) v1_there = mbar_test_wait(&bars[kBarVFull + v1.s], v1.phase);
-          if (!p_there) p_there = mbar_test_wait(&bars[kBarPFull + w], units[w] & 1);
-          if (i == kMaxSpins) {
-            *abort_flag = 1;
-            flag_error(a.dev_error, K16V8_DEVERR_TIMEOUT);
-            ok = false;
+          ready &= ~kK;
+          if (lane == 0) {
+            bar = &bars[kBarKFull + kr.s];
+            parity = kr.phase;
           }
         }
-        if (ok && u == 0 && p_idx > 0)  // the last piece's O tiles have been read
-          ok = wait(kBarOEmpty, (p_idx - 1) & 1, true);
-        if (!ok) break;
-        ++units[w];
-        tc::fence_after_sync();
-        const Ring<M::kVHalves> v0 = vr;  // both row tiles read the same halves
+        if (leader) tc::mma_commit(&bars[kBarQEmpty + q0]);
+        if (leader && two) tc::mma_commit(&bars[kBarQEmpty + 1]);
+        used(two ? 3 * kQ : kQ << q0);
+      }
+    } else {
+      constexpr uint32_t kIdesc = tc::idesc_f16_f32(kRows, kHeadDim, false, true);
+      constexpr int kHalves = 2 / kParts;  // of V, per part
+      const uint64_t dv = tc::smem_desc_sw128(smem_addr(sV), kVBlk, 1024);
+      const uint32_t dv_lo = static_cast<uint32_t>(dv), d_hi = static_cast<uint32_t>(dv >> 32);
+      // lanes 0, 1: the V halves; 2 + slot + 2 * part: P; 6: the last piece's O
+      // tiles have been read (the first passes)
+      constexpr uint32_t kV = 1u, kP = 4u, kO = 64u;
+      Ring<M::kVHalves> vr;
+      bar += lane < 2 ? kBarVFull + lane : lane < 6 ? kBarPFull + lane - 2 : kBarOEmpty;
+      parity = lane == 6;
+      while (ok && get_piece(pc, ring, true)) {
+        const bool two = kWide && pc.n > kNodes;
+        const int slots = two ? 2 : 1;
+        const int tiles = pc.tiles;
+        for (int t = 0; ok && t < tiles; ++t) {
+#pragma unroll 1
+          for (int part = 0; part < kParts; ++part) {
+            Ring<M::kVHalves> v1 = vr;
+            if (kHalves == 2) v1.next();
+#pragma unroll 1
+            for (int i = 0; i < slots; ++i) {
+              const int w = two ? i : t & 1;
+              const int tile = w + 2 * part;
+              uint32_t need = kP << tile;
+              if (i == 0) need |= kHalves == 2 ? 3 * kV : kV;
+              if (t == 0 && part == 0) need |= kO;
+              ok = poll(need);
+              if (!ok) break;
+              used(kP << tile);
+              const bool more_o = (two ? t : t >> 1) + part > 0;  // O is added to
+              const uint32_t p0 = tmem + w * 128 + part * (kKv / kParts);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint64_t b0 = dv + static_cast<uint64_t>(vr.s * (kVHalf / 16));
+              for (int h = 0; h < kHalves; ++h) {
+                const uint32_t b0 = dv_lo + (h ? v1.s : vr.s) * (kVHalf / 16);
 #pragma unroll
-          for (int kk = 0; kk < kHalf / 16; ++kk)
-            if (leader)
-              tc::mma_f16_ts(tmem + 256 + w * 128, tmem + w * 128 + (h * (kHalf / 16) + kk) * 8,
-                             b0 + static_cast<uint64_t>(kk * 128), kIdescPV,
-                             u >= 2 || h > 0 || kk > 0);
-          if (leader && (!two || w == 1)) tc::mma_commit(&bars[kBarVEmpty + vr.s]);
-          vr.next();
+                for (int kk = 0; kk < kHalf / 16; ++kk)
+                  if (leader)
+                    tc::mma_f16_ts(tmem + 256 + w * 128, p0 + (h * (kHalf / 16) + kk) * 8,
+                                   b0 + kk * 128, d_hi, kIdesc, more_o || h + kk > 0);
+                if (leader && i + 1 == slots) tc::mma_commit(&bars[kBarVEmpty + (h ? v1.s : vr.s)]);
+              }
+              if (leader) tc::mma_commit(&bars[kBarPV + tile]);
+              // the slot's last of the piece
+              if (leader && part == kParts - 1 && t + (two ? 1 : 2) >= tiles)
+                tc::mma_commit(&bars[kBarODone + w]);
+            }
+            if (!ok) break;
+            vr = v1;
+            vr.next();
+            if (kHalves == 2) {
+              v1 = vr;
+              v1.next();
+            }
+            ready &= ~(3 * kV);
+            if (lane < 2) {
+              bar = &bars[kBarVFull + (lane ? v1.s : vr.s)];
+              parity = lane ? v1.phase : vr.phase;
+            }
+          }
         }
-        if (two && w == 0) vr = v0;
-        if (leader && u + 2 >= n_units) tc::mma_commit(&bars[kBarODone + w]);
-        if (u + 2 < n_units) ok = issue_s(u + 2, k_there);
+        used(kO);
       }
     }
     // every MMA issued has to land before tensor memory is released
-    if (leader) tc::mma_commit(&bars[kBarDrain]);
-    mbar_wait_bounded(&bars[kBarDrain], 0);
-    __syncwarp();
-  } else if (warp == kPieceWarp) {
-    // ================= the CTA's pieces =================
-    if (lane == 0) {
-      Ring<kPieceRing> ring;
-      Walker walker;
-      walker.init(a, kShape, range);
-      for (bool more = true; more;) {
-        if (ring.wrapped && !wait(kBarTaken + ring.s, ring.phase ^ 1)) break;
-        Piece p;
-        more = walker.next(a, kShape, range, p);
-        if (!more) p.tiles = 0;  // the end
-        pieces[ring.s] = p;
-        mbar_arrive(&bars[kBarPiece + ring.s]);
-        ring.next();
-      }
-    }
+    const int drain = kBarDrain + (warp == kOutWarp);
+    if (leader) tc::mma_commit(&bars[drain]);
+    mbar_wait_bounded(&bars[drain], 0);
     __syncwarp();
   }
 
