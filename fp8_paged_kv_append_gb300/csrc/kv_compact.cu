@@ -91,6 +91,11 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) kv_compact_kernel(
   if (first >= m) return;
   uint8_t *kc = reinterpret_cast<uint8_t *>(__ldg(k_ptrs + layer));
   uint8_t *vc = reinterpret_cast<uint8_t *>(__ldg(v_ptrs + layer));
+  const uint64_t low = reinterpret_cast<uint64_t>(kc) | reinterpret_cast<uint64_t>(vc);
+  if (!kc || !vc || (low & 15)) {
+    if (lane == 0) flag_error(dev_error, K16V8_DEVERR_PAGE);
+    return;
+  }
   const int32_t *bt = block_table + static_cast<int64_t>(b) * maxp;
   for (int j0 = first; j0 < m; j0 += kGroupRows) {
     // lane 2r + d: the offset of row j0 + r's source (d = 0) or destination

@@ -139,6 +139,43 @@ def test_another_stream_and_a_graph(K):
     torch.cuda.synchronize()
     with torch.cuda.stream(s):
         same(run(K, c, stream=s), moved(c))
+    # captured once, replayed over other paths in the same buffers
+    start = [to_dev(x.view(np.int16)).view(torch.float16) for x in c["ks"]], [to_dev(x) for x in c["vs"]]
+    ks, vs = [[x.clone() for x in xs] for xs in start]
+    ptrs = K.layer_pointers(ks), K.layer_pointers(vs)
+    bt, lens, indptr, path, plen = (to_dev(c[x]) for x in ("bt", "lens", "indptr", "path", "plen"))
+    new = torch.zeros(2, dtype=torch.int32, device=dev())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        K.k16v8_kv_compact(*ptrs, c["P"], 2, 128, bt, lens, indptr, path, plen, new)
+    for paths in ([[0, 2, 7], [0, 3, 5]], [[0, 1], [0, 8]], [[4], [0, 1, 2, 3, 6, 7, 8]]):
+        for dst, src in zip(ks + vs, start[0] + start[1]):
+            dst.copy_(src)
+        d = make(9, [50, 40], [9, 9], paths, 4, 2)
+        path.copy_(to_dev(d["path"]))
+        plen.copy_(to_dev(d["plen"]))
+        g.replay()
+        torch.cuda.synchronize()
+        same(([x.view(torch.int16).cpu().numpy().view(np.uint16) for x in ks],
+              [x.cpu().numpy() for x in vs], new.cpu().numpy()), moved(d))
+
+
+def test_bad_layer_addresses_are_flagged_and_not_followed(K):
+    c = make(11, [50, 40], [9, 9], [[0, 2, 7], [0, 3, 5]], 3, 2)
+    ks = [to_dev(x.view(np.int16)).view(torch.float16) for x in c["ks"]]
+    vs = [to_dev(x) for x in c["vs"]]
+    kp, vp = K.layer_pointers(ks), K.layer_pointers(vs)
+    kp[0] = 0
+    vp[2] += 8
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    K.k16v8_kv_compact(kp, vp, c["P"], 2, 128, to_dev(c["bt"]), to_dev(c["lens"]), to_dev(c["indptr"]),
+                       to_dev(c["path"]), to_dev(c["plen"]), None, err)
+    assert K.k16v8_read_device_error(err) == K.DEVERR_PAGE
+    want = moved(c)
+    for li in range(3):
+        k, v = (want[0][li], want[1][li]) if li == 1 else (c["ks"][li], c["vs"][li])
+        assert np.array_equal(ks[li].view(torch.int16).cpu().numpy().view(np.uint16), k)
+        assert np.array_equal(vs[li].cpu().numpy(), v)
 
 
 def test_binding_refuses_wrong_tensors(K):
