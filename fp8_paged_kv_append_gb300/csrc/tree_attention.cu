@@ -134,7 +134,8 @@ static int32_t check_tree_shape(int32_t total_q, int32_t batch, int32_t max_node
     return K16V8_ERR_INVALID_ARG;
   if (head_dim != kHeadDim || hq != kGroup * hkv || max_nodes > K16V8_MAX_TREE_NODES)
     return K16V8_ERR_UNSUPPORTED_SHAPE;
-  if (batch > tree::kMaxBatch || hkv > 4095) return K16V8_ERR_INVALID_ARG;
+  if (batch > tree::kMaxBatch || hkv > 4095 || max_len > tree::kMaxLen)
+    return K16V8_ERR_INVALID_ARG;
   return K16V8_OK;
 }
 
@@ -160,6 +161,8 @@ extern "C" int32_t k16v8_paged_tree_attention(
                                 max_seq_len);
   if (st != K16V8_OK) return st;
   if (num_pages <= 0 || max_pages_per_seq < 0) return K16V8_ERR_INVALID_ARG;
+  // a row's largest score times the scale has to be its largest scaled score
+  if (!(sm_scale >= 0.f && sm_scale - sm_scale == 0.f)) return K16V8_ERR_INVALID_ARG;
   if (static_cast<int64_t>(max_pages_per_seq) * kPage < max_seq_len) return K16V8_ERR_INVALID_ARG;
   if (batch == 0 || total_q == 0 || max_nodes == 0 || max_seq_len == 0) return K16V8_OK;
   if (!q || !qo_indptr || !tree_mask || !k_cache || !v_cache || !v_scale || !block_table ||

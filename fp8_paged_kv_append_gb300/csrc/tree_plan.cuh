@@ -19,6 +19,7 @@ namespace k16v8 {
 namespace tree {
 
 constexpr int kMaxBatch = 8192;  // the scan's prefix lives in shared memory
+constexpr int kMaxLen = 1 << 30;  // positions round up to tiles in 32 bits
 
 struct Args {
   const __half *q;

@@ -177,15 +177,11 @@ struct Ring {
 // As in prefill: a wait that runs out raises the CTA-wide abort flag, which
 // the suspending waits poll; every role leaves its loops on a failed wait.
 __device__ __forceinline__ bool cta_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                         int32_t *dev_error, bool spin = false) {
+                                         int32_t *dev_error) {
   if (*abort_flag) return false;
-  if (spin) {
-    if (mbar_spin_bounded(bar, parity)) return true;
-  } else {
-    for (uint32_t i = 0; i < kMaxPolls; ++i) {
-      if (mbar_try_wait(bar, parity)) return true;
-      if ((i & 1023u) == 1023u && *abort_flag) return false;
-    }
+  for (uint32_t i = 0; i < kMaxPolls; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 1023u && *abort_flag) return false;
   }
   *abort_flag = 1;
   flag_error(dev_error, K16V8_DEVERR_TIMEOUT);
@@ -313,12 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
-  auto wait = [&](int bar, uint32_t parity, bool spin = false) {
-    return cta_wait(&bars[bar], parity, abort_flag, a.dev_error, spin);
+  auto wait = [&](int bar, uint32_t parity) {
+    return cta_wait(&bars[bar], parity, abort_flag, a.dev_error);
   };
   // The next piece, for a whole warp; false at the end (or after an abort).
-  auto get_piece = [&](Piece &pc, Ring<kPieceRing> &r, bool spin = false) {
-    if (!__all_sync(kFull, wait(kBarPiece + r.s, r.phase, spin))) return false;
+  auto get_piece = [&](Piece &pc, Ring<kPieceRing> &r) {
+    if (!__all_sync(kFull, wait(kBarPiece + r.s, r.phase))) return false;
     pc = pieces[r.s];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[kBarTaken + r.s]);
@@ -808,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       Ring<M::kKStages> kr;
       bar += lane == 0 ? kBarKFull : lane <= 4 ? kBarPV + lane - 1 : kBarQFull + (lane == 6);
       parity = lane >= 1 && lane <= 4;
-      for (uint32_t p_idx = 0; ok && get_piece(pc, ring, true); ++p_idx) {
+      for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
         const bool two = kWide && pc.n > kNodes;
         const int slots = two ? 2 : 1;
         const int q0 = kWide && !two ? p_idx & 1 : 0;  // the first slot's query
@@ -861,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       Ring<M::kVHalves> vr;
       bar += lane < 2 ? kBarVFull + lane : lane < 6 ? kBarPFull + lane - 2 : kBarOEmpty;
       parity = lane == 6;
-      while (ok && get_piece(pc, ring, true)) {
+      while (ok && get_piece(pc, ring)) {
         const bool two = kWide && pc.n > kNodes;
         const int slots = two ? 2 : 1;
         const int tiles = pc.tiles;

@@ -548,7 +548,7 @@ def k16v8_rope_kv_append(q, k, v, positions, inv_freq, slot_mapping, v_scale, q_
 def k16v8_tree_workspace_size(total_q, batch, max_nodes, num_qo_heads, num_kv_heads, head_dim,
                               max_seq_len) -> int:
     """Bytes of workspace k16v8_paged_tree_attention needs for these sizes on
-    the current device (0: none)."""
+    the current device (0 where they are refused)."""
     return int(load_library().k16v8_tree_workspace_size(
         total_q, batch, max_nodes, num_qo_heads, num_kv_heads, head_dim, max_seq_len))
 
@@ -560,7 +560,7 @@ def k16v8_paged_tree_attention(q, qo_indptr, max_nodes, tree_mask, k_cache, v_ca
     int32 [B+1], the nodes being the last positions of the cache; tree_mask
     int64 [total_q], bit j of a node's word set where it sees node j of its
     tree (tree_step.tree_masks builds it from the parents).  workspace uint8
-    of k16v8_tree_workspace_size bytes, or None where that is 0."""
+    of k16v8_tree_workspace_size bytes, not shared by calls that overlap."""
     total_q, hq, d = q.shape
     dev = _device(q)
     P, hkv = k_cache.shape[0], k_cache.shape[1]

@@ -47,7 +47,9 @@ class MultiLayerTreeDecode:
     block_table int32 [B, max_pages] on the host (numpy) covering every
     position up to max_seq_len; inv_freq / attn_factor from
     rope.rope_inv_freq.  Row buffers hold batch * max_nodes rows; rows behind
-    the last tree are padding (slot -1) and stay as they are."""
+    the last tree are padding (slot -1) and stay as they are.  The workspace and
+    the tree buffers serve one step at a time: steps and replays that overlap
+    need an object each."""
 
     def __init__(self, k_caches, v_caches, v_scales, block_table, batch, max_nodes, max_seq_len,
                  num_qo_heads, inv_freq, attn_factor=1.0, interleaved=False, sm_scale=None,
@@ -81,7 +83,11 @@ class MultiLayerTreeDecode:
         self.k_ptrs, self.v_ptrs = K.layer_pointers(k_caches), K.layer_pointers(v_caches)
         n = K.k16v8_tree_workspace_size(self.rows, self.batch, self.max_nodes, self.hq, self.hkv,
                                         self.d, self.max_seq_len)
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+        if n == 0:
+            raise ValueError(f"no tree attention for {self.batch} sequences of up to "
+                             f"{self.max_nodes} nodes and {self.max_seq_len} positions, "
+                             f"{self.hq} over {self.hkv} heads of {self.d}")
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=dev)
         self.graph = None
 
     def set_trees(self, parents, prefix_lens) -> None:

@@ -584,10 +584,13 @@ int32_t k16v8_rope_kv_append(const void *q, int64_t q_token_stride, const void *
  *   max_nodes    host hint: the largest tree, <= K16V8_MAX_TREE_NODES
  *   tree_mask    device uint64 [total_q]
  *   seq_lens     device int32 [batch], the nodes included, <= max_seq_len
+ *   max_seq_len  at most 2^30; batch at most 8192, num_kv_heads at most 4095,
+ *                num_pages * num_kv_heads * 16 below 2^31
+ *   sm_scale     finite, >= 0
  *   workspace    device, 256-B aligned, k16v8_tree_workspace_size(...) bytes
- *                for the same arguments on the same device (0: NULL allowed);
- *                needs no initialisation.  Calls that overlap on the GPU must
- *                not share one.
+ *                for the same arguments on the same device (0 only where they
+ *                are refused); needs no initialisation.  Calls that overlap on
+ *                the GPU, replays of captured ones too, must not share one.
  *   out, lse     as for k16v8_paged_prefill_attention (lse may be NULL)
  * A sequence with rows outside [0, total_q), n > max_nodes, n > seq_len or
  * seq_len > max_seq_len flags K16V8_DEVERR_SEQLEN and is skipped; a page id
@@ -658,7 +661,8 @@ int32_t k16v8_tree_verify(const float *target_probs, int64_t target_row_stride,
  *
  *   k_caches, v_caches  device arrays of num_layers device addresses, the
  *                 layers' caches (distinct buffers of num_pages pages that
- *                 share the block table)
+ *                 share the block table; NULL or not 16-byte aligned: flags
+ *                 K16V8_DEVERR_PAGE, and nothing of the layer moves)
  *   seq_lens      device int32 [batch], the nodes included
  *   qo_indptr     device int32 [batch+1]: n = qo_indptr[b+1] - qo_indptr[b]
  *   path          device int32 [batch][max_nodes], strictly increasing

@@ -135,6 +135,61 @@ def test_ragged_batch_with_idle_sequences_and_spare_rows(K):
     assert np.all(out[end:] == 9.0) and np.all(lse[end:] == 9.0)
 
 
+@pytest.mark.parametrize("hint", [32, 64])
+def test_many_short_sequences(K, hint):
+    """Several sequences per SM, most within one KV tile."""
+    rng = np.random.default_rng(60 + hint)
+    nodes = rng.integers(0, 6, 150)
+    nodes[::40] = (hint, 9, 0, hint - 3)
+    lens = nodes + rng.integers(0, 160, 150)
+    compare(K, Case(61, lens, nodes, hkv=10, max_nodes=hint))
+
+
+@pytest.mark.parametrize("n", [1, 5, 16, 32])
+def test_wide_hint_over_narrow_trees(K, n):
+    compare(K, Case(62 + n, [n, 40 + n, 500, 1300], [n] * 4, branch=3, max_nodes=64))
+
+
+def test_wide_and_narrow_trees_in_turn(K):
+    compare(K, Case(67, [700, 90, 260, 1500, 129, 64], [40, 3, 64, 32, 0, 33], hkv=3, max_nodes=64))
+
+
+@pytest.mark.parametrize("n", [20, 60])
+def test_replayed_graphs_that_share_a_workspace(K, n):
+    """Two captured calls of different batches, replayed in turn over new queries."""
+    cases = [Case(70, [900, 30, 400], [n, 4, n], hkv=3), Case(71, [60, 2100], [n, 9], hkv=3)]
+    size = max(K.k16v8_tree_workspace_size(c.rows, c.B, c.max_nodes, c.hq, c.hkv, 128,
+                                           int(c.lens.max())) for c in cases)
+    ws = torch.full((size,), 0xA5, dtype=torch.uint8, device=dev())
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    held = []
+    for c in cases:
+        t = [to_dev(x) for x in (c.q, c.indptr, c.mask, c.kc, c.vc, c.vs, c.bt, c.lens)]
+        out = torch.zeros((c.rows, c.hq, 128), dtype=torch.float16, device=dev())
+        lse = torch.zeros((c.rows, c.hq), dtype=torch.float32, device=dev())
+
+        def call(c=c, t=t, out=out, lse=lse):
+            K.k16v8_paged_tree_attention(t[0], t[1], c.max_nodes, *t[2:8], int(c.lens.max()), c.scale,
+                                         ws, out, lse, err)
+
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        held.append((c, t, out, lse, g))
+    for turn in range(2):
+        for c, t, out, lse, g in held:
+            c.q = np.random.default_rng(72 + turn).standard_normal(c.q.shape).astype(np.float16)
+            t[0].copy_(to_dev(c.q))
+            out.fill_(9.0)
+        for h in held:
+            h[4].replay()
+        assert K.k16v8_read_device_error(err) == 0
+        for c, t, out, lse, g in held:
+            c.check(out.cpu().numpy().astype(np.float64), lse.cpu().numpy())
+
+
 @pytest.mark.parametrize("hkv", [1, 3, 10])
 def test_heads(K, hkv):
     compare(K, Case(4, [100, 777], [11, 5], hkv=hkv))

@@ -156,3 +156,6 @@ def test_host_checks(K):
         s.set_trees([[-1, 0]] + [[]] * (B - 1), [MAX_LEN - 1] + [0] * (B - 1))
     with pytest.raises(RuntimeError):
         s.replay()
+    from fp8_paged_kv_append_gb300.tree_step import MultiLayerTreeDecode
+    with pytest.raises(ValueError):
+        MultiLayerTreeDecode(m.kc, m.vc, m.vs, m.bt, B, 65, MAX_LEN, 4 * HKV, m.freq)

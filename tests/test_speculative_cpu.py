@@ -57,7 +57,9 @@ def test_rope_refusals(lib, change, status):
     (dict(total_q=-1), 1), (dict(batch=-1), 1), (dict(max_nodes=-1), 1), (dict(hkv=0), 1),
     (dict(max_len=-1), 1), (dict(d=64), 2), (dict(hq=10), 2), (dict(max_nodes=65), 2),
     (dict(batch=8193), 1), (dict(hq=4 * 4096, hkv=4096), 1), (dict(pages=0), 1),
-    (dict(maxp=-1), 1), (dict(maxp=7), 1),
+    (dict(maxp=-1), 1), (dict(maxp=7), 1), (dict(maxp=1 << 27, max_len=(1 << 30) + 1), 1),
+    (dict(scale=-0.1), 1), (dict(scale=math.inf), 1), (dict(scale=math.nan), 1),
+    (dict(pages=1 << 26, ws_bytes=1 << 40), 1),
     (dict(q=None), 1), (dict(indptr=None), 1), (dict(mask=None), 1), (dict(kc=None), 1),
     (dict(vc=None), 1), (dict(v_scale=None), 1), (dict(table=None), 1), (dict(lens=None), 1),
     (dict(out=None), 1), (dict(q=A + 8), 1), (dict(kc=A + 8), 1), (dict(vc=A + 8), 1),
