@@ -220,7 +220,9 @@ __device__ __forceinline__ void keep(const uint32_t (&r)[32]) {
                  "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7]));
 }
 
-// p = 2^(s * scale - m) of 16 scores: fp16 to tensor memory, their sum in fp32.
+// p = 2^(s * scale - m) of 16 scores to tensor memory, their sum in fp32.  P is
+// rounded to fp16 (2^-11 of a weight), the type of V's tile: an MMA takes both
+// operands in one type, and bf16 would round P eight times as coarsely.
 template <bool kMask>
 __device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[16], uint32_t seen,
                                           float2 scale, float2 neg_m, float2 &sum) {
