@@ -509,7 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       const int c_lo = two ? 0 : 4 * w, c_hi = two ? 8 : 4 * w + 4;  // 16 dims each
       const int row = (two ? w * kRows : 0) + r;  // of the segment
       const int64_t orow = static_cast<int64_t>(pc.q0 + node) * hq + pc.g * kGroup + (r & 3);
+      const bool whole = pc.whole;
       if (warp_live) {
+        // (what the piece says is read once: shared memory is slow under the MMAs)
+        __half *po = a.out + orow * kHeadDim;
+        float4 *pp = a.part_o + static_cast<int64_t>(pc.slot) * 32 * a.max_rows + row;
 #pragma unroll 1
         for (int c = c_lo; c < c_hi; ++c) {
           float o[16];
@@ -539,8 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
             for (int e = 0; e < 16; ++e)
               if ((__ldg(vr + e) & 0x7f) == 0x7f) o[e] = NAN;
           }
-          if (row_valid && pc.whole) {
-            uint4 *po = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + c * 16);
+          if (row_valid && whole) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
               uint32_t pk[4];
@@ -549,18 +552,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
                 const __half2 hh = __floats2half2_rn(o[q * 8 + 2 * e], o[q * 8 + 2 * e + 1]);
                 pk[e] = *reinterpret_cast<const uint32_t *>(&hh);
               }
-              po[q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              reinterpret_cast<uint4 *>(po)[2 * c + q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             }
           } else if (row_valid) {
-            float4 *po = a.part_o + (static_cast<int64_t>(pc.slot) * 32 + c * 4) * a.max_rows + row;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              po[static_cast<int64_t>(q) * a.max_rows] =
+              pp[static_cast<int64_t>(4 * c + q) * a.max_rows] =
                   make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
         }
         if (row_valid && (two || w == 0)) {
-          if (!pc.whole)
+          if (!whole)
             a.part_lse[static_cast<int64_t>(pc.slot) * a.max_rows + row] = lse;
           else if (a.lse)
             a.lse[orow] = lse;
