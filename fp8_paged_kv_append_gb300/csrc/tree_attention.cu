@@ -19,55 +19,53 @@ namespace k16v8 {
 namespace tree {
 
 // Joins the pieces of the segment that begins in CTA blockIdx.x and is cut:
-// o = sum_p e^(lse_p - lse) o_p, lse = log sum_p e^lse_p.  A block takes 32
-// rows x 32 dims: a lane per row, a warp per 8 dims, so a warp's loads are
-// 512-byte runs.  Bound by latency: the first pieces' rows are asked for
-// before the LSEs are in hand, and eight pieces are in flight at a time.
-constexpr int kMergeFlight = 8;
-__global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
-  extern __shared__ float lse_of[];  // [piece][32 rows]
-  pdl_wait();
-  pdl_launch_dependents();
-  const int4 cut = __ldg(a.cut + blockIdx.x);
-  if (cut.x < 0) return;
-  const int first = blockIdx.x, pieces = cut.z - first + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = blockIdx.y * 32 + lane, chunk = (blockIdx.z * 4 + warp) * 2;
-  auto slot = [&](int p) { return 2 * static_cast<int64_t>(first + p) + (p == 0 ? 1 : 0); };
-  float4 x[kMergeFlight][2];
-  auto load = [&](int p0) {
+// o = sum_p e^(lse_p - lse) o_p, lse = log sum_p e^lse_p, with a running
+// maximum.  A warp takes 32 rows, a lane each (so its loads are 512-byte runs),
+// by kChunks chunks of 4 dims, and has kFlight pieces in flight.
+template <int kChunks, int kFlight>
+__device__ __forceinline__ void merge_rows(const Args &a, const int4 &cut, int first, int row,
+                                           int chunk) {
+  const int pieces = cut.z - first + 1;
+  float M = -INFINITY, S = 0.f;
+  float4 acc[kChunks];
 #pragma unroll
-    for (int u = 0; u < kMergeFlight; ++u) {
-      if (p0 + u >= pieces) continue;
-      const float4 *po = a.part_o + (slot(p0 + u) * 32 + chunk) * a.max_rows + row;
-      x[u][0] = __ldg(po);
-      x[u][1] = __ldg(po + a.max_rows);
-    }
-  };
-  load(0);
-  for (int p = warp; p < pieces; p += 4)
-    lse_of[p * 32 + lane] = __ldg(a.part_lse + slot(p) * a.max_rows + row);
+  for (int c = 0; c < kChunks; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   const int q0 = __ldg(a.qo_indptr + cut.x), n = __ldg(a.qo_indptr + cut.x + 1) - q0;
-  __syncthreads();
-  float M = -INFINITY;
-  for (int p = 0; p < pieces; ++p) M = fmaxf(M, lse_of[p * 32 + lane]);
-  float S = 0.f;
-  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int p0 = 0; p0 < pieces; p0 += kMergeFlight) {
-    if (p0 > 0) load(p0);
+  for (int p0 = 0; p0 < pieces; p0 += kFlight) {
+    float4 x[kFlight][kChunks];
+    float l[kFlight];
 #pragma unroll
-    for (int u = 0; u < kMergeFlight; ++u) {
-      if (p0 + u >= pieces) continue;
-      const float l = lse_of[(p0 + u) * 32 + lane];
-      if (l == -INFINITY) continue;
-      const float w = ex2((l - M) * kLog2e);
+    for (int u = 0; u < kFlight; ++u) {
+      const int p = min(p0 + u, pieces - 1);  // (the last one again: no branch)
+      const int64_t slot = 2 * static_cast<int64_t>(first + p) + (p == 0 ? 1 : 0);
+      const float4 *po = a.part_o + (slot * 32 + chunk) * a.max_rows + row;
+      l[u] = __ldg(a.part_lse + slot * a.max_rows + row);
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c) x[u][c] = __ldg(po + static_cast<int64_t>(c) * a.max_rows);
+    }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      if (p0 + u >= pieces) l[u] = -INFINITY;
+      top = fmaxf(top, l[u]);
+    }
+    const float fade = M == -INFINITY ? 0.f : ex2((M - top) * kLog2e);
+    M = top;
+    S *= fade;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c)
+      acc[c] = make_float4(acc[c].x * fade, acc[c].y * fade, acc[c].z * fade, acc[c].w * fade);
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      if (l[u] == -INFINITY) continue;
+      const float w = ex2((l[u] - M) * kLog2e);
       S += w;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        acc[i].x = fmaf(w, x[u][i].x, acc[i].x);
-        acc[i].y = fmaf(w, x[u][i].y, acc[i].y);
-        acc[i].z = fmaf(w, x[u][i].z, acc[i].z);
-        acc[i].w = fmaf(w, x[u][i].w, acc[i].w);
+      for (int c = 0; c < kChunks; ++c) {
+        acc[c].x = fmaf(w, x[u][c].x, acc[c].x);
+        acc[c].y = fmaf(w, x[u][c].y, acc[c].y);
+        acc[c].z = fmaf(w, x[u][c].z, acc[c].z);
+        acc[c].w = fmaf(w, x[u][c].w, acc[c].w);
       }
     }
   }
@@ -76,13 +74,42 @@ __global__ void __launch_bounds__(128) tree_merge_kernel(const Args a) {
   const float inv = dead ? 0.f : 1.f / S;
   const int64_t orow =
       static_cast<int64_t>(q0 + row / kGroup) * a.hkv * kGroup + cut.y * kGroup + row % kGroup;
-  const __half2 h[4] = {__floats2half2_rn(acc[0].x * inv, acc[0].y * inv),
-                        __floats2half2_rn(acc[0].z * inv, acc[0].w * inv),
-                        __floats2half2_rn(acc[1].x * inv, acc[1].y * inv),
-                        __floats2half2_rn(acc[1].z * inv, acc[1].w * inv)};
-  *reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + chunk * 4) =
-      *reinterpret_cast<const uint4 *>(h);
+  uint4 *po = reinterpret_cast<uint4 *>(a.out + orow * kHeadDim + chunk * 4);
+#pragma unroll
+  for (int c = 0; c < kChunks; c += 2) {
+    const __half2 h[4] = {__floats2half2_rn(acc[c].x * inv, acc[c].y * inv),
+                          __floats2half2_rn(acc[c].z * inv, acc[c].w * inv),
+                          __floats2half2_rn(acc[c + 1].x * inv, acc[c + 1].y * inv),
+                          __floats2half2_rn(acc[c + 1].z * inv, acc[c + 1].w * inv)};
+    po[c / 2] = *reinterpret_cast<const uint4 *>(h);
+  }
   if (chunk == 0 && a.lse) a.lse[orow] = dead ? -INFINITY : M + lg2(S) * kLn2;
+}
+
+// One CTA: 32 rows by 16 kChunks dims.  Latency-bound: three round trips (the
+// cut, lengths and rows, stores) for up to 2 pieces or 16 / kChunks, no
+// shared memory; about 3 us of a call, and 8 where all 152 CTAs' segments are
+// cut and have 256 rows (40 MB).  LSEs through shared memory ahead of the
+// rows: 95.9 against 91.8 us on 5 nodes at 128K.
+constexpr int kMergeWarps = 4;
+template <int kChunks>
+__global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const Args a) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int4 cut = __ldg(a.cut + blockIdx.x);
+  if (cut.x < 0) return;
+  const int row = blockIdx.y * 32 + (threadIdx.x & 31);
+  const int chunk = (blockIdx.z * kMergeWarps + (threadIdx.x >> 5)) * kChunks;
+  if (cut.z - static_cast<int>(blockIdx.x) + 1 <= 2)
+    merge_rows<kChunks, 2>(a, cut, blockIdx.x, row, chunk);
+  else
+    merge_rows<kChunks, 16 / kChunks>(a, cut, blockIdx.x, row, chunk);
+}
+
+template <int kChunks>
+static int32_t launch_merge(const Args &a, int ctas, cudaStream_t s) {
+  const dim3 grid(ctas, (a.max_nodes * kGroup + 31) / 32, kHeadDim / 4 / (kMergeWarps * kChunks));
+  return k16v8_launch_pdl(tree_merge_kernel<kChunks>, grid, dim3(kMergeWarps * 32), 0, s, a);
 }
 
 // ---- host side ------------------------------------------------------------
@@ -210,7 +237,12 @@ extern "C" int32_t k16v8_paged_tree_attention(
   st = max_nodes > tree::tcore::kNodes ? tree::launch_tc<true>(mq, mk, a, w.ctas, s)
                                        : tree::launch_tc<false>(mq, mk, a, w.ctas, s);
   if (st != K16V8_OK) return st;
-  return k16v8_launch_pdl(tree::tree_merge_kernel,
-                          dim3(w.ctas, (max_nodes * kGroup + 31) / 32, 4), dim3(128),
-                          static_cast<size_t>(w.ctas) * 32 * sizeof(float), s, a);
+  // Wide trees have row groups enough, and every CTA costs its launch whether its
+  // segment is cut or not.  2 and 4 chunks per warp, both calls together, us: 5
+  // nodes at 1K 11.5 / 12.0, at 128K 91.8 / 94.8; 16 nodes 12.1 / 12.4, 93.3 /
+  // 94.3 and 32 x 1.1K 41.4 / 40.8; 32 nodes at 128K 95.4 / 95.9, 32 x 1.1K 45.7 /
+  // 44.9, one short sequence 12.2 / 11.0; 64 nodes, 16 x 8K 160.3 / 154.8 (8: 154.6),
+  // 1 x 128K 149 / 146.7 (8: 149.1).
+  return max_nodes > 16 ? tree::launch_merge<4>(a, w.ctas, s)
+                        : tree::launch_merge<2>(a, w.ctas, s);
 }
