@@ -36,8 +36,9 @@
 //    warp each, because the issue of one unit takes ~1,000 cycles of one warp
 //    (173 -> 167 us).  Parts of 64 positions cost S a third of its rate (55
 //    cycles per 128 x 64 x 16) and still gain for two row tiles, where MMAs and
-//    softmax alternate otherwise (175 -> 168 us); for one row tile they gain
-//    nothing (95.1 and 95.2 us on 8 nodes at 128K) and are not used.
+//    softmax alternate otherwise (173 / 155 us in one part and in two, 16 x 64
+//    nodes at 8K); for one row tile they do not (44.7 / 45.3 us on 32 x 32 nodes at
+//    1.1K, 100.6 / 101.1 at 8K) and are not used.
 //  * Nothing is in local memory: what L1 has left beside the operand stages is
 //    so little that a spilled register or an array indexed at run time costs a
 //    trip to L2 (~700 cycles) each time (46.8 -> 41.4 us on 32 x 8 nodes at 1.1K).
