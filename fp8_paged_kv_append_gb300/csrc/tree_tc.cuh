@@ -179,10 +179,9 @@ struct Ring {
 // the suspending waits poll; every role leaves its loops on a failed wait.
 __device__ __forceinline__ bool cta_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                          int32_t *dev_error) {
-  if (*abort_flag) return false;
   for (uint32_t i = 0; i < kMaxPolls; ++i) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023u) == 1023u && *abort_flag) return false;
+    if ((i & 1023u) == 0 && *abort_flag) return false;
   }
   *abort_flag = 1;
   flag_error(dev_error, K16V8_DEVERR_TIMEOUT);
