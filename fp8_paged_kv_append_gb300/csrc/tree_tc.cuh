@@ -370,23 +370,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
           const int tile = two ? k : 2 * k + w;
           const int d = d0 - tile * kKv;  // prefix columns of this tile
           const uint32_t bad = info[(tiles + tile) & 7];
-          const bool need_mask = d < kKv || bad;
-          Columns seen{0, 0};
-          if (need_mask) {
-            seen.lo = visible(part * 64 - d, mask_word);
-            if (kParts == 1) seen.hi = visible(64 - d, mask_word);
-            for (uint32_t pages = bad >> 4 * part; pages; pages &= pages - 1) {
-              const int page = __ffs(static_cast<int>(pages)) - 1;
-              const uint64_t out = 0xffffull << (page & 3) * 16;
-              if (page < 4)
-                seen.lo &= ~out;
-              else if (kParts == 1)
-                seen.hi &= ~out;
-            }
-          }
           const uint32_t tSp = tS + lane_base + part * kChunks * 32;
           // pass 1: row max
           float rmax = -INFINITY;
+          bool need_mask = d < kKv;
           if (!need_mask) {
 #pragma unroll 1
             for (int c = kChunks - 2; c >= 0; c -= 2) {
@@ -399,7 +386,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
               keep(s0);
               rmax = fmaxf(rmax, fmaxf(m0, m1));
             }
-          } else {
+            need_mask = bad != 0;  // (seldom; its load took place meanwhile)
+          }
+          Columns seen{0, 0};
+          if (need_mask) {
+            seen.lo = visible(part * 64 - d, mask_word);
+            if (kParts == 1) seen.hi = visible(64 - d, mask_word);
+            for (uint32_t pages = bad >> 4 * part; pages; pages &= pages - 1) {
+              const int page = __ffs(static_cast<int>(pages)) - 1;
+              const uint64_t out = 0xffffull << (page & 3) * 16;
+              if (page < 4)
+                seen.lo &= ~out;
+              else if (kParts == 1)
+                seen.hi &= ~out;
+            }
+            rmax = -INFINITY;
 #pragma unroll 1
             for (int c = 0; c < kChunks; ++c) {
               uint32_t s0[32];
