@@ -289,13 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       uint32_t count = 1;
       if (i >= kBarVstEmpty && i < kBarVEmpty) count = kDequantThreads;
       if (i >= kBarPFull && i < kBarPV) count = 4;
-      if (i == kBarJoin) count = 2 * kRows;
+      if (i == kBarJoin) count = 8;
       if (i == kBarOEmpty) count = 8;
       if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
       mbar_init(&bars[i], count);
     }
     *abort_flag = 0;
-    for (int i = 0; i < 8; ++i) nan_nodes[i] = 0;
     fence_barrier_init();
   }
   pdl_wait();
@@ -338,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     uint32_t units = 0;             // of this slot so far
     Pair last;                      // pieces in which a slot had units, so far
     uint32_t tiles = 0;             // of the CTA so far
+    uint32_t joins = 0;             // pieces with one row tile, so far
     bool ok = true;
     for (uint32_t p_idx = 0; ok; ++p_idx) {
       // the piece stays in shared memory: registers are short here
@@ -486,14 +486,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       float f_own = 1.f, f_other = 0.f;
       float m_all = m_used, l_all = l;
       if (!two) {
+        // (the last piece's have been read: this one's O was written after that)
         stat[(w * 2 + 0) * kRows + r] = m_used;
         stat[(w * 2 + 1) * kRows + r] = l;
-      }
-      mbar_arrive(&bars[kBarJoin]);
-      ok = __all_sync(kFull, wait(kBarJoin, p_idx & 1));
-      if (!ok) break;
-      if (tid < 2) nan_nodes[pn + tid] = 0;
-      if (!two) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarJoin]);
+        ok = __all_sync(kFull, wait(kBarJoin, joins++ & 1));
+        if (!ok) break;
         const float m_o = stat[((w ^ 1) * 2 + 0) * kRows + r];
         const float l_o = stat[((w ^ 1) * 2 + 1) * kRows + r];
         m_all = fmaxf(m_used, m_o);
@@ -671,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
           more = walker.next(a, kShape, range, p);
           if (!more) p.tiles = 0;  // the end
           pieces[out.s] = p;
+          nan_nodes[2 * out.s] = nan_nodes[2 * out.s + 1] = 0;  // (a ring like the pieces')
           mbar_arrive(&bars[kBarPiece + out.s]);
           out.next();
         }
