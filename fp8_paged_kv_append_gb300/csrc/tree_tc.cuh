@@ -57,9 +57,11 @@
 //  * A piece's description may take memory round trips to work out (the next
 //    sequence's lengths): that is done one piece ahead, behind the copies of
 //    the piece's first tile.
-// What a call takes now: 8 nodes at 128K 92 us (5.5 TB/s of K and V), 16 x 8
-// nodes at 8K 94 us, 16 x 64 nodes at 8K 155 us (1.1 PFLOP/s), 32 x 16 nodes at
-// 1.1K 41 us, one tree of 5 at 1K 11.5 us, the merge included.
+//  * Slots do not wait for one another where they need not: two row tiles end
+//    their pieces apart (163 -> 148 us on 256 x 64 nodes at 250 positions).
+// What a call takes now: 8 nodes at 128K 90 us (5.6 TB/s of K and V), 16 x 8
+// nodes at 8K 93 us, 16 x 64 nodes at 8K 152 us (1.1 PFLOP/s), 32 x 16 nodes at
+// 1.1K 40 us, one tree of 5 at 1K 11.3 us, the merge included.
 #pragma once
 
 #include "k16v8_device.cuh"
