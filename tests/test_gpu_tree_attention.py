@@ -190,6 +190,33 @@ def test_replayed_graphs_that_share_a_workspace(K, n):
             c.check(out.cpu().numpy().astype(np.float64), lse.cpu().numpy())
 
 
+def test_calls_on_two_streams_at_once(K):
+    """Narrow and wide calls in flight together, a workspace each; every round the same bits.
+    (The wide one's first sequence is shorter than its tree: flagged and skipped.)"""
+    cases = [Case(80, [900, 30, 2400], [20, 4, 7], hkv=3), Case(81, [60, 2100, 333], [64, 9, 40], hkv=3)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    held = []
+    for c in cases:
+        t = [to_dev(x) for x in (c.q, c.indptr, c.mask, c.kc, c.vc, c.vs, c.bt, c.lens)]
+        size = K.k16v8_tree_workspace_size(c.rows, c.B, c.max_nodes, c.hq, c.hkv, 128, int(c.lens.max()))
+        ws = torch.full((size,), 0xA5, dtype=torch.uint8, device=dev())
+        outs = [torch.zeros((c.rows, c.hq, 128), dtype=torch.float16, device=dev()) for _ in range(20)]
+        lse = torch.zeros((c.rows, c.hq), dtype=torch.float32, device=dev())
+        err = torch.zeros(1, dtype=torch.int32, device=dev())
+        held.append((c, t, ws, outs, lse, err))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for s, (c, t, ws, outs, lse, err) in zip(streams, held):
+            K.k16v8_paged_tree_attention(t[0], t[1], c.max_nodes, *t[2:8], int(c.lens.max()), c.scale, ws,
+                                         outs[i], lse, err, s)
+    torch.cuda.synchronize()
+    for (c, t, ws, outs, lse, err), flags, skip in zip(held, (0, K.DEVERR_SEQLEN), ((), (0,))):
+        assert K.k16v8_read_device_error(err) == flags
+        c.check(outs[0].cpu().numpy().astype(np.float64), lse.cpu().numpy(), skip=skip)
+        for o in outs[1:]:
+            assert torch.equal(o.view(torch.int16), outs[0].view(torch.int16))
+
+
 @pytest.mark.parametrize("hkv", [1, 3, 10])
 def test_heads(K, hkv):
     compare(K, Case(4, [100, 777], [11, 5], hkv=hkv))
