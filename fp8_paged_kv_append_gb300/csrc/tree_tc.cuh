@@ -222,9 +222,19 @@ __device__ __forceinline__ void keep(const uint32_t (&r)[32]) {
                  "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7]));
 }
 
-// p = 2^(s * scale - m) of 16 scores to tensor memory, their sum in fp32.  P is
-// rounded to fp16 (2^-11 of a weight), the type of V's tile: an MMA takes both
-// operands in one type, and bf16 would round P eight times as coarsely.
+// A row's weights are held 2^7 times as large as against its maximum, which
+// moves when it grows by more than 2^8, so they stay below 2^15.
+constexpr float kLift = 7.f, kSlack = 8.f;
+
+// p = 2^(s * scale - m) of 16 scores to tensor memory, their sum in fp32; m is
+// kLift below a maximum of the row.  P is rounded to fp16, the type of V's
+// tile: an MMA takes both operands in one type, and bf16 would round P eight
+// times as coarsely.  That is 2^-11 of a weight down to 2^-21 of the row's
+// largest; a smaller one is subnormal and off by up to 2^-32 of the largest,
+// which the row's sum, in fp32, does not share: L positions put O off by at
+// most L 2^-32 max|v|.  (Without the lift, L 2^-25: a score 17 above a flat tail
+// of 131,072 positions loses 0.24% of the output; the lift takes no instruction
+// per weight.)
 template <bool kMask>
 __device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[16], uint32_t seen,
                                           float2 scale, float2 neg_m, float2 &sum) {
@@ -416,9 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
           }
           rmax *= qk_scale;
           float alpha = 1.f;
-          if (rmax > m_used + 8.f) {
-            alpha = ex2(m_used - rmax);
-            m_used = rmax;
+          if (rmax > m_used + (kLift + kSlack)) {
+            alpha = ex2(m_used - (rmax - kLift));
+            m_used = rmax - kLift;
           }
           if (k + part > 0 && __any_sync(kFull, alpha != 1.f)) {
             // S of this part was issued after the P V of the part kParts before it;
@@ -505,7 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
       }
       const bool dead = !(l_all > 0.f) && l_all == l_all;  // the row sees nothing
       const float inv = dead ? 0.f : __fdividef(vs, l_all);
-      const float lse = dead ? -INFINITY : (m_all + lg2(l_all)) * kLn2;
+      // (the lift is taken off the sum, whose logarithm is most accurate near 1)
+      const float lse =
+          dead ? -INFINITY : ((m_all + kLift) + lg2(l_all * 0x1p-7f)) * kLn2;
+      static_assert(kLift == 7.f, "the factor of l_all");
       const float g_own = f_own * inv, g_other = f_other * inv;
       // with one row tile, slot w's warps write dims 64w .. 64w + 63 of every row
       const int c_lo = two ? 0 : 4 * w, c_hi = two ? 8 : 4 * w + 4;  // 16 dims each

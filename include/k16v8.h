@@ -577,7 +577,9 @@ int32_t k16v8_rope_kv_append(const void *q, int64_t q_token_stride, const void *
  * what it sees, with s_j = sm_scale * q.k_j and v_j = v_scale[h/4] * e4m3(v8_j):
  *   lse = ln sum exp(s_j),  out = sum exp(s_j - lse) v_j
  * A row that sees nothing gives out = 0, lse = -inf.  What is stored at a
- * position that a row does not see (NaN, inf) does not reach that row.
+ * position that a row does not see (NaN, inf) does not reach that row.  The
+ * weights are rounded to fp16 before they meet the values: 2^-11 relative, or
+ * 2^-32 of the row's largest weight where that is more.
  *
  *   q            device fp16 [total_q][num_qo_heads][head_dim], 16-B aligned
  *   qo_indptr    device int32 [batch+1]
