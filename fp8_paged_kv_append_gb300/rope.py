@@ -20,7 +20,11 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
     "yarn":   interpolation by parts: a pair that makes more than beta_fast
               turns over original_max_position positions is kept, one with
               fewer than beta_slow is divided by factor, those between are
-              blended linearly over the pair's index; attn_factor is
+              blended linearly over the pair's index (the ends of the blend
+              rounded outwards to whole pairs and kept within 0 and
+              rotary_dim - 1, as in Peng et al., "YaRN: Efficient Context
+              Window Extension of Large Language Models", 2023: the upper
+              end may lie beyond the last pair); attn_factor is
               0.1 ln(factor) + 1
     attn_factor is 1 for the others."""
     if rotary_dim < 16 or rotary_dim > 128 or rotary_dim % 16:
@@ -49,7 +53,7 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
             return half * math.log(original_max_position / (turns * 2 * math.pi)) / math.log(base)
 
         low = max(math.floor(pair_with_turns(beta_fast)), 0)
-        high = min(math.ceil(pair_with_turns(beta_slow)), half - 1)
+        high = min(math.ceil(pair_with_turns(beta_slow)), rotary_dim - 1)
         slow = ((i - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
         freq = freq / factor * slow + freq * (1.0 - slow)
         attn_factor = 0.1 * math.log(factor) + 1.0
