@@ -77,7 +77,12 @@ __device__ __forceinline__ int64_t units(uint32_t hi, uint32_t lo, uint32_t n) {
   return static_cast<int64_t>(h) * (1 << 22) + l;
 }
 
-// C (in units, below 64) as a sum of two fp32 numbers.
+// C (in units, below 64) as a sum of two fp32 numbers.  Rows that sum to 1 keep
+// it there: 63 children leave masses of at most 1 each.  A larger one's high part
+// would not be exact (and from 2^14 on not fit), so the walk ends with an error.
+constexpr int64_t kMaxC = 64 * kOne;
+// A mass that ends the walk so; also what 2^19 weights of 1 add up to.
+constexpr int64_t kTooLarge = INT64_MIN;
 __device__ __forceinline__ float c_high(int64_t C) {
   return static_cast<float>(static_cast<uint32_t>(C >> 26)) * 0x1p-18f;
 }
@@ -104,9 +109,10 @@ __device__ __forceinline__ int64_t units_of(float p) {
 }
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
+  uint64_t s = static_cast<uint64_t>(v);  // (2^63 units come out as kTooLarge)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return static_cast<int64_t>(s);
 }
 
 // The two halves of a cluster barrier: the first says that this CTA runs.
@@ -218,16 +224,18 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
 
   const int q0 = __ldg(qo_indptr + b);
   const int n = __ldg(qo_indptr + b + 1) - q0;
-  if (q0 < 0 || n <= 0 || n > max_nodes || q0 > total_q - n) {  // the whole cluster leaves
-    if (rank == 0) {
-      if (tid == 0) {
-        if (q0 < 0 || n != 0) flag_error(dev_error, K16V8_DEVERR_SEQLEN);
-        path_len[b] = 0;
-        next_token[b] = -1;
-      }
-      for (int i = tid; i < max_nodes; i += kThreads)
-        path_out[static_cast<int64_t>(b) * max_nodes + i] = -1;
+  auto no_result = [&](int32_t error) {
+    if (rank != 0) return;
+    if (tid == 0) {
+      if (error) flag_error(dev_error, error);
+      path_len[b] = 0;
+      next_token[b] = -1;
     }
+    for (int i = tid; i < max_nodes; i += kThreads)
+      path_out[static_cast<int64_t>(b) * max_nodes + i] = -1;
+  };
+  if (q0 < 0 || n <= 0 || n > max_nodes || q0 > total_q - n) {  // the whole cluster leaves
+    no_result(q0 < 0 || n != 0 ? K16V8_DEVERR_SEQLEN : 0);
     cluster_wait();
     return;
   }
@@ -296,10 +304,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
     }
     cluster.sync();
     ++passes;
-    int64_t all = 0;
+    uint64_t all = 0;
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) all += r < csize ? sh.cta_mass[par][r] : 0;
-    return all;
+    return static_cast<int64_t>(all);
   };
   auto mask64 = [](const uint32_t (&m)[2]) { return m[0] | static_cast<uint64_t>(m[1]) << 32; };
 
@@ -342,9 +350,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
       }
       if (draft) {
         C += tried ? mass : kOne;
+        if (C >= kMaxC || C < 0) {
+          mass = kTooLarge;
+          break;
+        }
         mass = mass_of(cur, C);
       } else {
         if (mass < 0) mass = mass_of(cur, 0);
+        if (mass < 0) break;
         if (!gone) {
           mass -= units_of(sh.p[i]);
           out_of |= 1ull << i;
@@ -353,13 +366,17 @@ __global__ void __launch_bounds__(kThreads, 2) tree_verify_kernel(
       tried = true;
     }
   }
-  if (mass < 0) mass = mass_of(cur, 0);
-  if (mass <= 0) {  // nothing left but rounding: the target's row itself
+  if (mass == -1) mass = mass_of(cur, 0);
+  if (mass <= 0 && mass != kTooLarge) {  // nothing left but rounding: the target's row itself
     if (C != 0) mass = mass_of(cur, 0);
     for (uint64_t m = out_of; m; m &= m - 1)
       mass += units_of(sh.p[__ffsll(static_cast<long long>(m)) - 1]);
     C = 0;
     out_of = 0;
+  }
+  if (mass == kTooLarge) {  // the whole cluster leaves
+    no_result(K16V8_DEVERR_PROBS);
+    return;
   }
   if (rank == 0) {
     if (tid == 0) path_len[b] = len;

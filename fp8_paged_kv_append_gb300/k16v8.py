@@ -29,7 +29,7 @@ K16V8_F32 = 1
 K16V8_BF16 = 2
 DECODE_METADATA_READY = 1
 DEVERR_SLOT, DEVERR_PAGE, DEVERR_SEQLEN, DEVERR_TIMEOUT, DEVERR_INTERNAL = 1, 2, 4, 8, 16
-DEVERR_POSITION, DEVERR_TREE = 32, 64
+DEVERR_POSITION, DEVERR_TREE, DEVERR_PROBS = 32, 64, 128
 PAGE_SIZE = 16
 HEAD_DIM = 128
 MAX_SPLIT_CHUNK = 8192  # K16V8_MAX_SPLIT_CHUNK

@@ -73,6 +73,7 @@ typedef enum { K16V8_F16 = 0, K16V8_F32 = 1, K16V8_BF16 = 2 } k16v8_dtype;
 #define K16V8_DEVERR_INTERNAL 0x10 /* a kernel's own layout check failed; nothing was written */
 #define K16V8_DEVERR_POSITION 0x20 /* rope_kv_append: position < 0 or >= 2^24 */
 #define K16V8_DEVERR_TREE 0x40   /* a parent, token or path entry that is none of its tree */
+#define K16V8_DEVERR_PROBS 0x80  /* tree_verify: sums far above 1 */
 
 /*
  * kv_append -- "the candidate also gathers values and writes the compressed
@@ -633,7 +634,8 @@ int32_t k16v8_paged_tree_attention(const void *q, const int32_t *qo_indptr, int3
  *
  *   target_probs, draft_probs  device fp32 [total_q][vocab_size], row strides
  *                 in elements (0 = vocab_size); values in [0, 1] (others are
- *                 clamped, NaN counts as 0), rows that sum to about 1
+ *                 clamped, NaN counts as 0), rows that sum to about 1 (the
+ *                 formulas hold for others, up to the sums below)
  *   tokens        device int32 [total_q] (node 0's is not read)
  *   parents       device int32 [total_q], indices within the tree (node 0's is
  *                 not read)
@@ -645,7 +647,10 @@ int32_t k16v8_paged_tree_attention(const void *q, const int32_t *qo_indptr, int3
  * A node whose parent is not an earlier node of its tree, or whose token is
  * outside [0, vocab_size), flags K16V8_DEVERR_TREE and is never reached; rows
  * outside [0, total_q) or n > max_nodes flag K16V8_DEVERR_SEQLEN and give
- * path_len 0.
+ * path_len 0, a path of -1 and next_token -1.  So does, with
+ * K16V8_DEVERR_PROBS, a tree at one of whose nodes the Z of the rejected
+ * children add up to 64 or a row sums to 2^19 (rows that sum to at most 1.01
+ * never do).
  */
 int32_t k16v8_tree_verify(const float *target_probs, int64_t target_row_stride,
                           const float *draft_probs, int64_t draft_row_stride,
