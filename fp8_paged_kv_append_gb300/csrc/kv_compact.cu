@@ -160,8 +160,13 @@ extern "C" int32_t k16v8_kv_compact(const uint64_t *k_caches, const uint64_t *v_
       !k16v8_aligned(qo_indptr, 4) || !k16v8_aligned(path, 4) || !k16v8_aligned(path_len, 4) ||
       (new_seq_lens && !k16v8_aligned(new_seq_lens, 4)))
     return K16V8_ERR_INVALID_ARG;
-  // other warps still read seq_lens when the new lengths are written
-  if (new_seq_lens && new_seq_lens < seq_lens + batch && seq_lens < new_seq_lens + batch)
+  // other warps still read the inputs when the new lengths are written
+  auto over = [&](const int32_t *in, int64_t n) {
+    return new_seq_lens && n > 0 && new_seq_lens < in + n && in < new_seq_lens + batch;
+  };
+  if (over(seq_lens, batch) || over(path_len, batch) || over(qo_indptr, batch + 1ll) ||
+      over(path, static_cast<int64_t>(batch) * max_nodes) ||
+      over(block_table, static_cast<int64_t>(batch) * max_pages_per_seq))
     return K16V8_ERR_INVALID_ARG;
   if (static_cast<int64_t>(batch) * num_kv_heads > 0x7fffffffLL) return K16V8_ERR_INVALID_ARG;
   const int64_t items = static_cast<int64_t>(num_layers) * batch * num_kv_heads;

@@ -640,7 +640,7 @@ def k16v8_kv_compact(k_ptrs, v_ptrs, num_pages, num_kv_heads, head_dim, block_ta
     """Move the accepted rows of every tree to the front of its positions in
     all layers (k_ptrs, v_ptrs: layer_pointers of the caches, each of
     num_pages pages); path int32 [B,max_nodes], path_len int32 [B] from
-    k16v8_tree_verify; new_seq_lens int32 [B] (not seq_lens itself)."""
+    k16v8_tree_verify; new_seq_lens int32 [B] (none of the inputs)."""
     dev = _device(k_ptrs)
     layers = k_ptrs.shape[0]
     B, max_nodes = path.shape

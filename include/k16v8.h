@@ -673,7 +673,8 @@ int32_t k16v8_tree_verify(const float *target_probs, int64_t target_row_stride,
  *   seq_lens      device int32 [batch], the nodes included
  *   qo_indptr     device int32 [batch+1]: n = qo_indptr[b+1] - qo_indptr[b]
  *   path          device int32 [batch][max_nodes], strictly increasing
- *   new_seq_lens  device int32 [batch] or NULL; not seq_lens itself
+ *   new_seq_lens  device int32 [batch] or NULL; overlaps no input (refused
+ *                 for the int32 arrays)
  * A path that does not increase strictly within its tree flags
  * K16V8_DEVERR_TREE, a sequence with n > seq_len, n > max_nodes or
  * seq_len > 16*max_pages_per_seq K16V8_DEVERR_SEQLEN: nothing of it moves and
