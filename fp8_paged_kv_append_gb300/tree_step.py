@@ -18,26 +18,33 @@ from . import k16v8 as K
 from .decode_step import validate_scales
 
 
-def tree_masks(parents) -> np.ndarray:
-    """int64 [n]: bit j of word i is set where node j is node i or one of its
-    ancestors.  parents[0] is not read; parents[i] < i."""
-    n = len(parents)
-    if n > K.MAX_TREE_NODES:
-        raise ValueError(f"a tree has at most {K.MAX_TREE_NODES} nodes, got {n}")
-    words: list[int] = []
+def _checked_parents(parents):
+    """(node, its parent) for every node; a parent but the first node's has to
+    be an earlier node."""
+    if len(parents) > K.MAX_TREE_NODES:
+        raise ValueError(f"a tree has at most {K.MAX_TREE_NODES} nodes, got {len(parents)}")
     for i, p in enumerate(parents):
         if i and not 0 <= p < i:
             raise ValueError(f"parent of node {i} must be an earlier node, got {p}")
+        yield i, p
+
+
+def tree_masks(parents) -> np.ndarray:
+    """int64 [n]: bit j of word i is set where node j is node i or one of its
+    ancestors.  parents[0] is not read; parents[i] < i."""
+    words: list[int] = []
+    for i, p in _checked_parents(parents):
         words.append((words[p] if i else 0) | 1 << i)
     return np.array(words, np.uint64).view(np.int64)
 
 
 def tree_depths(parents) -> np.ndarray:
-    """int32 [n]: edges between node 0 and each node."""
-    depth = np.zeros(len(parents), np.int32)
-    for i in range(1, len(parents)):
-        depth[i] = depth[parents[i]] + 1
-    return depth
+    """int32 [n]: edges between node 0 and each node.  parents as for
+    tree_masks."""
+    depth: list[int] = []
+    for i, p in _checked_parents(parents):
+        depth.append(depth[p] + 1 if i else 0)
+    return np.array(depth, np.int32)
 
 
 class MultiLayerTreeDecode:
