@@ -86,8 +86,9 @@ __device__ __forceinline__ void merge_rows(const Args &a, const int4 &cut, int f
   if (chunk == 0 && a.lse) a.lse[orow] = dead ? -INFINITY : M + lg2(S) * kLn2;
 }
 
-// One CTA: 32 rows by 16 kChunks dims.  Latency-bound: three round trips (the
-// cut, lengths and rows, stores) for up to 2 pieces or 16 / kChunks, no
+// One CTA: 32 rows by 16 kChunks dims (32 dims for trees of up to 16 nodes, 64
+// beyond: launch_merge).  Latency-bound: three round trips (the cut, lengths
+// and rows, stores) for up to 2 pieces or 16 / kChunks (8 and 4), no
 // shared memory; about 3 us of a call, and 8 where all 152 CTAs' segments are
 // cut and have 256 rows (40 MB).  LSEs through shared memory ahead of the
 // rows: 95.9 against 91.8 us on 5 nodes at 128K.
@@ -207,12 +208,10 @@ extern "C" int32_t k16v8_paged_tree_attention(
   if (!tree::layout(max_nodes, &w)) return K16V8_ERR_CUDA;
   if (workspace_bytes < w.total) return K16V8_ERR_WORKSPACE_TOO_SMALL;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  const tree::Args a{static_cast<const __half *>(q),
-                     qo_indptr,
+  const tree::Args a{qo_indptr,
                      total_q,
                      max_nodes,
                      tree_mask,
-                     static_cast<const __half *>(k_cache),
                      v_cache,
                      v_scale,
                      block_table,

@@ -21,12 +21,10 @@ namespace tree {
 constexpr int kMaxBatch = 8192;  // the scan's prefix lives in shared memory
 constexpr int kMaxLen = 1 << 30;  // positions round up to tiles in 32 bits
 
-struct Args {
-  const __half *q;
+struct Args {  // (queries and keys come through their tensor maps)
   const int32_t *qo_indptr;
   int32_t total_q, max_nodes;
   const uint64_t *tree_mask;
-  const __half *k_cache;
   const uint8_t *v_cache;
   const float *v_scale;
   const int32_t *block_table;

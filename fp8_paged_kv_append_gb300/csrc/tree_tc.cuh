@@ -83,7 +83,7 @@ constexpr int kOutWarp = 9, kLoadVWarp = 12, kLoadKWarp = 13, kScoreWarp = 15;
 constexpr int kDequantWarps = 4;
 constexpr int kDequantThreads = kDequantWarps * 32;
 constexpr int kPieceRing = 4;
-constexpr int kPieceReaders = 8 + kDequantWarps + 4;  // warps
+constexpr int kPieceReaders = 8 + kDequantWarps + 4;  // every warp
 
 // Rank of a dequant warp among them, or -1.
 __device__ __forceinline__ int dequant_rank(int warp) {
@@ -141,7 +141,7 @@ enum {
   kBarPV = 32,        // +slot + 2 * part: the part's P V is done
   kBarODone = 36,     // +slot: the slot's last P V of a piece
   kBarOEmpty = 38,    // 8 arrivals: both O tiles have been read
-  kBarJoin = 39,      // 256 arrivals: both slots' statistics are in shared memory
+  kBarJoin = 39,      // 8 arrivals (one per warp): both slots' statistics are in shared memory
   kBarPiece = 40,     // +ring entry: described
   kBarTaken = 44,     // +ring entry: kPieceReaders arrivals
   kBarDrain = 48,     // +0, 1: every S, every P V
