@@ -35,7 +35,8 @@ def reference(q, k, v, scale):
     ds = 2.0 ** -17 * scale * (q.abs() @ k.abs().t()).amax(-1) + 2.0 ** -22 * s.abs().amax(-1)
     L = len(k)
     rel = 2 * ds + 2.0 ** -18 + 2.0 ** -11 + L * (2.0 ** -31 + 2.0 ** -27)
-    bound = (rel[:, None] * A + L * 2.0 ** -32 * v.abs().max() + 2.0 ** -11 * out.abs() + 2.0 ** -25)
+    vmax = v.abs().nan_to_num(0.0).max()
+    bound = rel[:, None] * A + L * 2.0 ** -32 * vmax + 2.0 ** -11 * out.abs() + 2.0 ** -25
     return out, lse, bound, ds + 2.0 ** -20 * lse.abs() + 2.0 ** -18 + L * 2.0 ** -31
 
 
@@ -80,3 +81,40 @@ def test_dominant_scores_over_a_flat_tail(K, n, far):
     e = (out.double().view(B, 4 * n, 128) - ref).abs()
     assert torch.all(e <= bound), (float((e / ref.abs()).max()), float((e / bound).max()))
     assert torch.all((lse.double().view(B, 4 * n) - ref_l).abs() <= bound_l)
+
+
+@pytest.mark.parametrize("n", [7, 50])
+def test_one_long_context_in_pieces(K, n):
+    """100,003 positions over all SMs, joined.  (A few of the random values lie beyond 464 and are
+    NaN codes: every row sees them, and those dims are NaN in all.)"""
+    hkv, L = 2, 100003
+    pages = -(-L // 16)
+    gen = torch.Generator(device=dev()).manual_seed(n)
+    randn = lambda *s: torch.randn(s, generator=gen, device=dev())
+    q, k = randn(n, 4 * hkv, 128).half(), randn(pages + 3, hkv, 16, 128).half()
+    codes = (90 * randn(pages + 3, hkv, 16, 128)).to(torch.float8_e4m3fn)
+    vs = torch.tensor([3.0 / 448, 4.0 / 448], device=dev())
+    table = torch.randperm(pages + 3, generator=gen, device=dev())[:pages].to(torch.int32)[None]
+    scale = float(np.float32(1 / np.sqrt(128)))
+    mask = torch.tensor([(1 << i + 1) - 1 for i in range(n)], dtype=torch.int64, device=dev())
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev())
+    ws = torch.empty(K.k16v8_tree_workspace_size(n, 1, n, 4 * hkv, hkv, 128, L), dtype=torch.uint8,
+                     device=dev())
+    out = torch.zeros((n, 4 * hkv, 128), dtype=torch.float16, device=dev())
+    lse = torch.zeros((n, 4 * hkv), device=dev())
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    K.k16v8_paged_tree_attention(q, i32(0, n), n, mask, k, codes.view(torch.uint8), vs, table, i32(L),
+                                 L, scale, ws, out, lse, err)
+    assert K.k16v8_read_device_error(err) == 0
+    rows = table[0].long()
+    for g in range(hkv):
+        kg = k[rows, g].reshape(-1, 128)[:L].double()
+        vg = codes.float()[rows, g].reshape(-1, 128)[:L].double() * vs[g].double()
+        for i in range(n):  # a chain: node i sees all before it
+            end = L - n + i + 1
+            ref, ref_l, bound, bound_l = reference(q[i, 4 * g:4 * g + 4].double(), kg[:end], vg[:end],
+                                                   scale)
+            got = out[i, 4 * g:4 * g + 4].double()
+            assert torch.equal(got.isnan(), ref.isnan()) and not got.isnan().all()
+            assert torch.all(((got - ref).abs() <= bound) | ref.isnan())
+            assert torch.all((lse[i, 4 * g:4 * g + 4].double() - ref_l).abs() <= bound_l)
