@@ -133,7 +133,7 @@ static bool layout(int32_t max_nodes, Layout *w) {
   return true;
 }
 
-template <bool kWide>
+template <bool kWide, bool kTest>
 static int32_t launch_tc(const CUtensorMap &mq, const CUtensorMap &mk, const Args &a, int ctas,
                          cudaStream_t s) {
   static bool configured[64] = {false};
@@ -141,14 +141,14 @@ static int32_t launch_tc(const CUtensorMap &mq, const CUtensorMap &mk, const Arg
   if (cudaGetDevice(&dev) != cudaSuccess) return K16V8_ERR_CUDA;
   constexpr uint32_t smem = tcore::Smem<kWide>::kBytes;
   if (dev >= 64 || !configured[dev]) {
-    if (cudaFuncSetAttribute(tcore::tree_tc_kernel<kWide>,
+    if (cudaFuncSetAttribute(tcore::tree_tc_kernel<kWide, kTest>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
       return K16V8_ERR_CUDA;
     if (dev < 64) configured[dev] = true;
   }
-  return k16v8_launch_pdl(tcore::tree_tc_kernel<kWide>, dim3(ctas), dim3(tcore::kThreads), smem, s,
-                          mq, mk, a);
+  return k16v8_launch_pdl(tcore::tree_tc_kernel<kWide, kTest>, dim3(ctas), dim3(tcore::kThreads),
+                          smem, s, mq, mk, a);
 }
 
 }  // namespace tree
@@ -178,7 +178,8 @@ extern "C" size_t k16v8_tree_workspace_size(int32_t total_q, int32_t batch, int3
   return w.total;
 }
 
-extern "C" int32_t k16v8_paged_tree_attention(
+template <bool kTest>
+static int32_t tree_attention(
     const void *q, const int32_t *qo_indptr, int32_t total_q, int32_t max_nodes,
     const uint64_t *tree_mask, const void *k_cache, const uint8_t *v_cache, const float *v_scale,
     const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
@@ -233,8 +234,8 @@ extern "C" int32_t k16v8_paged_tree_attention(
   CUtensorMap mq, mk;
   if (!map_rows(&mq, q, num_qo_heads, total_q) || !map_keys(&mk, k_cache, k_rows))
     return K16V8_ERR_CUDA;
-  st = max_nodes > tree::tcore::kNodes ? tree::launch_tc<true>(mq, mk, a, w.ctas, s)
-                                       : tree::launch_tc<false>(mq, mk, a, w.ctas, s);
+  st = max_nodes > tree::tcore::kNodes ? tree::launch_tc<true, kTest>(mq, mk, a, w.ctas, s)
+                                       : tree::launch_tc<false, kTest>(mq, mk, a, w.ctas, s);
   if (st != K16V8_OK) return st;
   // Wide trees have row groups enough, and every CTA costs its launch whether its
   // segment is cut or not.  2 and 4 chunks per warp, both calls together, us: 5
@@ -244,4 +245,30 @@ extern "C" int32_t k16v8_paged_tree_attention(
   // 1 x 128K 149 / 146.7 (8: 149.1).
   return max_nodes > 16 ? tree::launch_merge<4>(a, w.ctas, s)
                         : tree::launch_merge<2>(a, w.ctas, s);
+}
+
+extern "C" int32_t k16v8_paged_tree_attention(
+    const void *q, const int32_t *qo_indptr, int32_t total_q, int32_t max_nodes,
+    const uint64_t *tree_mask, const void *k_cache, const uint8_t *v_cache, const float *v_scale,
+    const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+    int32_t max_seq_len, int32_t batch, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t num_pages, float sm_scale, void *workspace, size_t workspace_bytes,
+    void *out, float *lse, int32_t *dev_error, void *stream) {
+  return tree_attention<false>(q, qo_indptr, total_q, max_nodes, tree_mask, k_cache, v_cache, v_scale,
+                               block_table, max_pages_per_seq, seq_lens, max_seq_len, batch,
+                               num_qo_heads, num_kv_heads, head_dim, num_pages, sm_scale, workspace,
+                               workspace_bytes, out, lse, dev_error, stream);
+}
+
+extern "C" int32_t k16v8_paged_tree_attention_wait_test(
+    const void *q, const int32_t *qo_indptr, int32_t total_q, int32_t max_nodes,
+    const uint64_t *tree_mask, const void *k_cache, const uint8_t *v_cache, const float *v_scale,
+    const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+    int32_t max_seq_len, int32_t batch, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t num_pages, float sm_scale, void *workspace, size_t workspace_bytes,
+    void *out, float *lse, int32_t *dev_error, void *stream) {
+  return tree_attention<true>(q, qo_indptr, total_q, max_nodes, tree_mask, k_cache, v_cache, v_scale,
+                               block_table, max_pages_per_seq, seq_lens, max_seq_len, batch,
+                               num_qo_heads, num_kv_heads, head_dim, num_pages, sm_scale, workspace,
+                               workspace_bytes, out, lse, dev_error, stream);
 }

@@ -255,7 +255,10 @@ __device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[16],
   tc::tmem_st8(t_p, pk);
 }
 
-template <bool kWide>
+// kTest: the form of the bounded-wait test hook.  CTA 0 withholds K of its first
+// tile (no arrival, nothing in flight), so the score warp's wait for it runs out
+// after kTestSpins polls and every role takes the abort path.
+template <bool kWide, bool kTest>
 __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
     const Args a) {
@@ -316,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
   const Range range = plan_range(a, kShape, kWide ? 2 : 1, reinterpret_cast<int64_t *>(smem_raw),
                                  reinterpret_cast<int64_t *>(smem_raw + M::kStat));
   const bool work = range.lo < range.hi;  // uniform over the CTA
+  const bool withholds = kTest && blockIdx.x == 0;
   fence_proxy_async();  // the scan's scratch becomes operand stages
   tc::fence_before_sync();
   __syncthreads();
@@ -742,12 +746,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
         if (!ok) break;
         const uint32_t bad = __ballot_sync(kFull, pid == -1);
         const uint32_t bytes = __popc(__ballot_sync(kFull, pid >= 0)) * 4096u;
+        const bool withheld = withholds && issued == 0;
         if (lane == 0) {
           info[issued & 7] = bad;
-          mbar_arrive_expect_tx(&bars[kBarKFull + dst.s], bytes);
+          if (!withheld) mbar_arrive_expect_tx(&bars[kBarKFull + dst.s], bytes);
         }
         __syncwarp();
-        if (pid >= 0) {
+        if (pid >= 0 && !withheld) {
           uint8_t *k_dst = sK + dst.s * kKStage + lane * 2048;
           const int row = (pid * a.hkv + pc.g) * kPage;
           tc::tma_load_2d(k_dst, &tmap_k, 0, row, &bars[kBarKFull + dst.s]);
@@ -779,7 +784,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     if (lane == 0) {
       constexpr uint32_t n = M::kKStages;
       for (uint32_t i = issued < n ? 0 : issued - n; i < issued; ++i)
-        mbar_wait_bounded(&bars[kBarKFull + i % n], (i / n) & 1);
+        if (!(withholds && i == 0))
+          mbar_wait_bounded(&bars[kBarKFull + i % n], (i / n) & 1);
       for (int s = 0; s < 2; ++s)
         if (uses[s] > 0) mbar_wait_bounded(&bars[kBarQFull + s], (uses[s] - 1) & 1);
     }
@@ -797,7 +803,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
     auto poll = [&](uint32_t need) {
       for (uint32_t i = 0; (ready & need) != need; ++i) {
         ready = __ballot_sync(kFull, mbar_test_wait(bar, parity));
-        if ((i & 255u) == 255u && (i >= kMaxSpins || *abort_flag)) {
+        const uint32_t limit = withholds && warp == kScoreWarp ? kTestSpins : kMaxSpins;
+        if ((i & 255u) == 255u && (i >= limit || *abort_flag)) {
           if (!*abort_flag) flag_error(a.dev_error, K16V8_DEVERR_TIMEOUT);
           *abort_flag = 1;
           return false;
@@ -854,6 +861,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
             }
             if (!ok) break;
           }
+          // (a stage whose copy did not land is not to be filled again: its barrier's
+          // phase is still open)
+          if (!ok) break;
           if (leader) tc::mma_commit(&bars[kBarKEmpty + kr.s]);
           kr.next();
           ready &= ~kK;
@@ -862,6 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_tc_kernel(
             parity = kr.phase;
           }
         }
+        if (!ok) break;
         if (leader) tc::mma_commit(&bars[kBarQEmpty + q0]);
         if (leader && two) tc::mma_commit(&bars[kBarQEmpty + 1]);
         used(two ? 3 * kQ : kQ << q0);

@@ -101,6 +101,9 @@ SIGNATURES = {
     "k16v8_paged_tree_attention": (_i32, [_P, _P, _i32, _i32, _P, _P, _P, _P, _P, _i32, _P, _i32,
                                           _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz, _P, _P, _P,
                                           _P]),
+    "k16v8_paged_tree_attention_wait_test": (_i32, [_P, _P, _i32, _i32, _P, _P, _P, _P, _P, _i32, _P,
+                                                    _i32, _i32, _i32, _i32, _i32, _i32, _f32, _P,
+                                                    _sz, _P, _P, _P, _P]),
     "k16v8_tree_verify": (_i32, [_P, _i64, _P, _i64, _P, _P, _P, _i32, _i32, _P, _i32, _i32, _P,
                                  _P, _P, _P, _P]),
     "k16v8_kv_compact": (_i32, [_P, _P, _i32, _P, _i32, _P, _P, _P, _i32, _P, _i32, _i32, _i32,
@@ -585,6 +588,22 @@ def k16v8_paged_tree_attention(q, qo_indptr, max_nodes, tree_mask, k_cache, v_ca
         _error_word(dev_error, dev), _stream_on(stream, dev))
     if st != K16V8_OK:
         raise K16V8Error("k16v8_paged_tree_attention", st)
+
+
+def k16v8_paged_tree_attention_wait_test(q, qo_indptr, max_nodes, tree_mask, k_cache, v_cache,
+                                         v_scale, block_table, seq_lens, max_seq_len, sm_scale,
+                                         workspace, out, lse=None, dev_error=None, stream=None):
+    """Test hook: k16v8_paged_tree_attention with the keys of the first CTA's
+    first tile withheld, so that CTA's bounded wait expires
+    (K16V8_DEVERR_TIMEOUT)."""
+    total_q, hq, d = q.shape
+    st = load_library().k16v8_paged_tree_attention_wait_test(
+        _ptr(q), _ptr(qo_indptr), total_q, int(max_nodes), _ptr(tree_mask), _ptr(k_cache),
+        _ptr(v_cache), _ptr(v_scale), _ptr(block_table), block_table.shape[1], _ptr(seq_lens),
+        int(max_seq_len), seq_lens.shape[0], hq, k_cache.shape[1], d, k_cache.shape[0],
+        float(sm_scale), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
+        _ptr(lse), _ptr(dev_error), _stream(stream))
+    _check("k16v8_paged_tree_attention_wait_test", st)
 
 
 def _prob_rows(t, name: str, shape, dev: int) -> int:

@@ -615,6 +615,19 @@ int32_t k16v8_paged_tree_attention(const void *q, const int32_t *qo_indptr, int3
                                    void *out, float *lse, int32_t *dev_error, void *stream);
 
 /*
+ * Test hook of its bounded waits, as the two above: CTA 0 (the first tiles of
+ * the first sequence's KV head 0) withholds the keys of its first tile, so its
+ * rows, and those joined with them, are not valid.
+ */
+int32_t k16v8_paged_tree_attention_wait_test(
+    const void *q, const int32_t *qo_indptr, int32_t total_q, int32_t max_nodes,
+    const uint64_t *tree_mask, const void *k_cache, const uint8_t *v_cache, const float *v_scale,
+    const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+    int32_t max_seq_len, int32_t batch, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t num_pages, float sm_scale, void *workspace, size_t workspace_bytes,
+    void *out, float *lse, int32_t *dev_error, void *stream);
+
+/*
  * tree_verify -- which nodes the target accepts (rejection sampling that
  * leaves the target's distribution unchanged) and the token after them.
  *
