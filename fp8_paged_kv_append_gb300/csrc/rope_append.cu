@@ -24,90 +24,21 @@
 // table serves both.  A CTA takes a run of units; its threads load their
 // units first, compute the run's cosines and sines into shared memory (each
 // once) while those loads are in flight, and then turn and store.
-#include <cuda_bf16.h>
-
-#include "k16v8_device.cuh"
+#include "rope_device.cuh"
 
 namespace k16v8 {
 namespace rope {
 
 constexpr int kThreads = 128;
-constexpr int kUnitsPerRow = kHeadDim / 16;
-constexpr int32_t kMaxPosition = 1 << 24;  // positions below are exact in fp32
-// 1 / 2pi as a sum of two fp32 numbers
-constexpr float kInv2PiHi = 0x1.45f306p-3f;
-constexpr float kInv2PiLo = 0x1.b9391p-28f;
-
-template <typename T>
-struct Raw {  // 16 elements
-  uint4 w[sizeof(T)];
-};
-
-// Elements [e, e + 8) of a row.
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, uint4 *w) {
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
-    w[i] = reinterpret_cast<const uint4 *>(p)[i];
-}
-
-__device__ __forceinline__ void widen8(const uint4 *w, float (&x)[8], const __half *) {
-  const __half2 *h = reinterpret_cast<const __half2 *>(w);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(h[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
-__device__ __forceinline__ void widen8(const uint4 *w, float (&x)[8], const __nv_bfloat16 *) {
-  const uint32_t u[4] = {w->x, w->y, w->z, w->w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ void widen8(const uint4 *w, float (&x)[8], const float *) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    x[4 * i] = __uint_as_float(w[i].x);
-    x[4 * i + 1] = __uint_as_float(w[i].y);
-    x[4 * i + 2] = __uint_as_float(w[i].z);
-    x[4 * i + 3] = __uint_as_float(w[i].w);
-  }
-}
-
-__device__ __forceinline__ uint4 narrow8(const float (&x)[8]) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t *>(&h);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
-}
-
-// cos and sin of position * freq, times factor.
-__device__ __forceinline__ float2 turn(int32_t position, float freq, float factor) {
-  const float p = static_cast<float>(position);
-  const float rh = __fmul_rn(freq, kInv2PiHi);  // products that are not to be contracted
-  const float rl = fmaf(freq, kInv2PiLo, fmaf(freq, kInv2PiHi, -rh));
-  const float th = __fmul_rn(p, rh);
-  const float tl = fmaf(p, rl, fmaf(p, rh, -th));
-  const float frac = (th - rintf(th)) + tl;
-  float s, c;
-  sincospif(2.f * frac, &s, &c);
-  return make_float2(c * factor, s * factor);
-}
 
 // kUnits units per thread.  Rows of a token: hq query heads, hkv key heads,
-// hkv value heads.
-template <typename T, bool kInterleaved, int kUnits>
+// hkv value heads.  kAxes: positions [axes.count][num_tokens], pair f turned by row axes[f].
+template <typename T, bool kInterleaved, int kUnits, bool kAxes>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(
     const T *q, int64_t q_ts, const T *k, int64_t k_ts, const T *v, int64_t v_ts,
-    const int32_t *__restrict__ positions, const float *__restrict__ inv_freq, int32_t rotary,
-    float factor, const int64_t *__restrict__ slot_mapping, int32_t num_tokens,
+    const int32_t *__restrict__ positions, const PairAxes axes,
+    const float *__restrict__ inv_freq, int32_t rotary, float factor,
+    const int64_t *__restrict__ slot_mapping, int32_t num_tokens,
     const float *__restrict__ v_scale, __half *q_out, __half *k_cache, uint8_t *v_cache,
     int32_t num_pages, int32_t hq, int32_t hkv, int32_t *dev_error) {
   // cos, sin of the run's tokens: pair 8c + 2i + e of a token at [i][c][e], so
@@ -157,7 +88,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(
   for (int i = threadIdx.x; i < n_tok * half; i += kThreads) {
     const int t = i / half, f = i - t * half;
     table[t * half + ((f & 7) >> 1) * (half >> 2) + (f >> 3) * 2 + (f & 1)] =
-        turn(__ldg(positions + t0 + t), __ldg(inv_freq + f), factor);
+        turn(__ldg(positions + (kAxes ? static_cast<int64_t>(axes[f]) * num_tokens : 0) + t0 + t),
+             __ldg(inv_freq + f), factor);
   }
 #pragma unroll
   for (int j = 0; j < kUnits; ++j) {
@@ -166,7 +98,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(
       continue;
     }
     const bool bad_slot = slot[j] >= static_cast<int64_t>(num_pages) * kPage;
-    if (bad_slot || static_cast<uint32_t>(__ldg(positions + t0 + tok[j])) >= kMaxPosition) {
+    if (bad_slot ||
+        !positions_ok(positions, num_tokens, kAxes ? axes.count : 1, t0 + tok[j])) {
       if (row[j] == 0) flag_error(dev_error, bad_slot ? K16V8_DEVERR_SLOT : K16V8_DEVERR_POSITION);
       row[j] = -1;
     }
@@ -229,6 +162,7 @@ struct Args {
   const void *q, *k, *v;
   int64_t q_ts, k_ts, v_ts;
   const int32_t *positions;
+  PairAxes axes;
   const float *inv_freq;
   int32_t rotary;
   float factor;
@@ -241,7 +175,7 @@ struct Args {
   int32_t *dev_error;
 };
 
-template <typename T, bool kInterleaved, int kUnits>
+template <typename T, bool kInterleaved, int kUnits, bool kAxes>
 static int32_t launch(const Args &a, cudaStream_t stream) {
   const int upt = (a.hq + 2 * a.hkv) * kUnitsPerRow;
   const int64_t total = static_cast<int64_t>(a.num_tokens) * upt;
@@ -250,11 +184,11 @@ static int32_t launch(const Args &a, cudaStream_t stream) {
   // a run of units touches at most this many tokens
   const int toks = (kThreads * kUnits - 2) / upt + 2;
   const size_t smem = static_cast<size_t>(toks) * (a.rotary / 2) * sizeof(float2);
-  return k16v8_launch_pdl(rope_append_kernel<T, kInterleaved, kUnits>,
+  return k16v8_launch_pdl(rope_append_kernel<T, kInterleaved, kUnits, kAxes>,
                           dim3(static_cast<unsigned>(blocks)), dim3(kThreads), smem, stream,
                           static_cast<const T *>(a.q), a.q_ts, static_cast<const T *>(a.k), a.k_ts,
-                          static_cast<const T *>(a.v), a.v_ts, a.positions, a.inv_freq, a.rotary,
-                          a.factor, a.slots, a.num_tokens, a.v_scale,
+                          static_cast<const T *>(a.v), a.v_ts, a.positions, a.axes, a.inv_freq,
+                          a.rotary, a.factor, a.slots, a.num_tokens, a.v_scale,
                           static_cast<__half *>(a.q_out), static_cast<__half *>(a.k_cache),
                           a.v_cache, a.num_pages, a.hq, a.hkv, a.dev_error);
 }
@@ -264,16 +198,16 @@ static int32_t launch(const Args &a, cudaStream_t stream) {
 // GB300: 43.4 against 47.2 us at 8,192 tokens of 40 + 10 heads, 3.6 against 4.1
 // at 256, 3.1 against 2.5 at 32 (60 CTAs); two fp32 units against one: 29.2
 // against 28.6 us at 4,096 tokens.  (CTAs of 256 threads: 45.0 and 29.4 us.)
-template <typename T>
+template <typename T, bool kAxes>
 static int32_t dispatch(const Args &a, bool interleaved, cudaStream_t stream) {
   if constexpr (sizeof(T) == 2) {
     const int64_t units = static_cast<int64_t>(a.num_tokens) * (a.hq + 2 * a.hkv) * kUnitsPerRow;
     const int sms = k16v8_sm_count();
     if (sms <= 0) return K16V8_ERR_CUDA;
     if (units >= static_cast<int64_t>(sms) * 2 * kThreads)
-      return interleaved ? launch<T, true, 2>(a, stream) : launch<T, false, 2>(a, stream);
+      return interleaved ? launch<T, true, 2, kAxes>(a, stream) : launch<T, false, 2, kAxes>(a, stream);
   }
-  return interleaved ? launch<T, true, 1>(a, stream) : launch<T, false, 1>(a, stream);
+  return interleaved ? launch<T, true, 1, kAxes>(a, stream) : launch<T, false, 1, kAxes>(a, stream);
 }
 
 }  // namespace rope
@@ -281,9 +215,11 @@ static int32_t dispatch(const Args &a, bool interleaved, cudaStream_t stream) {
 
 using namespace k16v8;
 
-extern "C" int32_t k16v8_rope_kv_append(
+template <bool kAxes>
+static int32_t rope_kv_append(
     const void *q, int64_t q_token_stride, const void *k, int64_t k_token_stride, const void *v,
-    int64_t v_token_stride, int32_t x_dtype, const int32_t *positions, const float *inv_freq,
+    int64_t v_token_stride, int32_t x_dtype, const int32_t *positions,
+    int32_t num_axes, const int8_t *pair_axis, const float *inv_freq,
     int32_t rotary_dim, int32_t interleaved, float attn_factor, const int64_t *slot_mapping,
     int32_t num_tokens, const float *v_scale, void *q_out, void *k_cache, uint8_t *v_cache,
     int32_t num_pages, int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -298,6 +234,10 @@ extern "C" int32_t k16v8_rope_kv_append(
     return K16V8_ERR_INVALID_ARG;
   if (interleaved != 0 && interleaved != 1) return K16V8_ERR_INVALID_ARG;
   if (!(attn_factor - attn_factor == 0.f)) return K16V8_ERR_INVALID_ARG;  // finite
+  rope::PairAxes axes{0, 0, 1};
+  if (kAxes && (num_axes < 1 || num_axes > K16V8_MAX_ROPE_AXES || !pair_axis ||
+                !rope::pack_axes(pair_axis, rotary_dim / 2, num_axes, &axes)))
+    return K16V8_ERR_INVALID_ARG;
   if (num_tokens == 0) return K16V8_OK;
   if ((num_qo_heads > 0 && (!q || !q_out)) || !k || !v || !positions || !inv_freq ||
       !slot_mapping || !v_scale || !k_cache || !v_cache)
@@ -318,11 +258,39 @@ extern "C" int32_t k16v8_rope_kv_append(
       !k16v8_aligned(positions, 4) || !k16v8_aligned(inv_freq, 4) || !k16v8_aligned(v_scale, 4))
     return K16V8_ERR_INVALID_ARG;
   const rope::Args a{q,           k,         v,       q_token_stride, k_token_stride,
-                     v_token_stride, positions, inv_freq, rotary_dim,   attn_factor,
+                     v_token_stride, positions, axes, inv_freq, rotary_dim, attn_factor,
                      slot_mapping, num_tokens, v_scale, q_out,          k_cache,
                      v_cache,     num_pages, num_qo_heads, num_kv_heads, dev_error};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (x_dtype == K16V8_F32) return rope::dispatch<float>(a, interleaved != 0, s);
-  if (x_dtype == K16V8_BF16) return rope::dispatch<__nv_bfloat16>(a, interleaved != 0, s);
-  return rope::dispatch<__half>(a, interleaved != 0, s);
+  if (x_dtype == K16V8_F32) return rope::dispatch<float, kAxes>(a, interleaved != 0, s);
+  if (x_dtype == K16V8_BF16) return rope::dispatch<__nv_bfloat16, kAxes>(a, interleaved != 0, s);
+  return rope::dispatch<__half, kAxes>(a, interleaved != 0, s);
+}
+
+extern "C" int32_t k16v8_rope_kv_append(
+    const void *q, int64_t q_token_stride, const void *k, int64_t k_token_stride, const void *v,
+    int64_t v_token_stride, int32_t x_dtype, const int32_t *positions, const float *inv_freq,
+    int32_t rotary_dim, int32_t interleaved, float attn_factor, const int64_t *slot_mapping,
+    int32_t num_tokens, const float *v_scale, void *q_out, void *k_cache, uint8_t *v_cache,
+    int32_t num_pages, int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim,
+    int32_t *dev_error, void *stream) {
+  return rope_kv_append<false>(q, q_token_stride, k, k_token_stride, v, v_token_stride, x_dtype,
+                               positions, 1, nullptr, inv_freq, rotary_dim, interleaved,
+                               attn_factor, slot_mapping, num_tokens, v_scale, q_out, k_cache,
+                               v_cache, num_pages, num_qo_heads, num_kv_heads, head_dim, dev_error,
+                               stream);
+}
+
+extern "C" int32_t k16v8_rope_axes_kv_append(
+    const void *q, int64_t q_token_stride, const void *k, int64_t k_token_stride, const void *v,
+    int64_t v_token_stride, int32_t x_dtype, const int32_t *positions, int32_t num_axes,
+    const int8_t *pair_axis, const float *inv_freq, int32_t rotary_dim, int32_t interleaved,
+    float attn_factor, const int64_t *slot_mapping, int32_t num_tokens, const float *v_scale,
+    void *q_out, void *k_cache, uint8_t *v_cache, int32_t num_pages, int32_t num_qo_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t *dev_error, void *stream) {
+  return rope_kv_append<true>(q, q_token_stride, k, k_token_stride, v, v_token_stride, x_dtype,
+                              positions, num_axes, pair_axis, inv_freq, rotary_dim, interleaved,
+                              attn_factor, slot_mapping, num_tokens, v_scale, q_out, k_cache,
+                              v_cache, num_pages, num_qo_heads, num_kv_heads, head_dim, dev_error,
+                              stream);
 }

@@ -34,6 +34,7 @@ PAGE_SIZE = 16
 HEAD_DIM = 128
 MAX_SPLIT_CHUNK = 8192  # K16V8_MAX_SPLIT_CHUNK
 MAX_TREE_NODES = 64  # K16V8_MAX_TREE_NODES
+MAX_ROPE_AXES = 4  # K16V8_MAX_ROPE_AXES
 
 # Every symbol include/k16v8.h declares, with its ctypes signature.
 _P = ctypes.c_void_p
@@ -97,6 +98,15 @@ SIGNATURES = {
                                                        _f32, _P, _P, _P, _P]),
     "k16v8_rope_kv_append": (_i32, [_P, _i64, _P, _i64, _P, _i64, _i32, _P, _P, _i32, _i32, _f32,
                                     _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32, _i32, _P, _P]),
+    "k16v8_rope_axes_kv_append": (_i32, [_P, _i64, _P, _i64, _P, _i64, _i32, _P, _i32, _P, _P, _i32,
+                                         _i32, _f32, _P, _i32, _P, _P, _P, _P, _i32, _i32, _i32,
+                                         _i32, _P, _P]),
+    "k16v8_rope_kv_append_k8v8": (_i32, [_P, _i64, _P, _i64, _P, _i64, _i32, _P, _i32, _P, _i32, _P,
+                                         _P, _i32, _i32, _f32, _P, _i32, _P, _i32, _P, _P, _P, _P,
+                                         _i32, _i32, _i32, _i32, _P, _P]),
+    "k16v8_decode_workspace_size_k8v8": (_sz, [_i32, _i32, _i32]),
+    "k16v8_paged_decode_attention_k8v8": (_i32, [_P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _i32,
+                                                 _i32, _f32, _P, _sz, _P, _P, _P, _P]),
     "k16v8_tree_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "k16v8_paged_tree_attention": (_i32, [_P, _P, _i32, _i32, _P, _P, _P, _P, _P, _i32, _P, _i32,
                                           _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz, _P, _P, _P,
@@ -678,6 +688,134 @@ def k16v8_kv_compact(k_ptrs, v_ptrs, num_pages, num_kv_heads, head_dim, block_ta
         _error_word(dev_error, dev), _stream_on(stream, dev))
     if st != K16V8_OK:
         raise K16V8Error("k16v8_kv_compact", st)
+
+
+# ---- positions with several axes; the K8/V8 cache ------------------------------------
+
+def _axes(pair_axis, half: int) -> bytes:
+    """The axis of each pair as the host array of the C ABI (bytes are taken as
+    they are)."""
+    if type(pair_axis) is not bytes:
+        pair_axis = bytes(pair_axis)
+    if len(pair_axis) != half:
+        raise ValueError(f"pair_axis must have an entry for each of {half} pairs, got "
+                         f"{len(pair_axis)}")
+    return pair_axis
+
+
+def k16v8_rope_axes_kv_append(q, k, v, positions, pair_axis, inv_freq, slot_mapping, v_scale, q_out,
+                              k_cache, v_cache, interleaved=False, attn_factor=1.0, dev_error=None,
+                              stream=None) -> None:
+    """k16v8_rope_kv_append with positions int32 [axes,T]: pair i is turned by
+    row pair_axis[i] of them (host integers, e.g. rope.rope_pair_axes)."""
+    T, hkv, d = k.shape
+    dt, dev = k.dtype, _device(k)
+    if dt not in _X_DTYPES:
+        raise ValueError(f"k must be fp16, fp32 or bf16, got {dt}")
+    hq = 0 if q is None else q.shape[1]
+    if q is None:
+        q_ptr, q_ts, out_ptr = None, 0, None
+    else:
+        q_ptr, q_ts = q.data_ptr(), _rows(q, "q", dt, (T, hq, d), dev)
+        out_ptr = _dense(q_out, "q_out", _F16, (T, hq, d), dev)
+    row = (T, hkv, d)
+    cache = (k_cache.shape[0], hkv, PAGE_SIZE, d)
+    half, axes = inv_freq.numel(), positions.shape[0]
+    st = (_lib or load_library()).k16v8_rope_axes_kv_append(
+        q_ptr, q_ts, k.data_ptr(), _rows(k, "k", dt, row, dev), v.data_ptr(),
+        _rows(v, "v", dt, row, dev), _X_DTYPES[dt],
+        _dense(positions, "positions", _I32, (axes, T), dev), axes, _axes(pair_axis, half),
+        _dense(inv_freq, "inv_freq", _F32, (half,), dev), 2 * half, 1 if interleaved else 0,
+        attn_factor, _dense(slot_mapping, "slot_mapping", _I64, (T,), dev), T,
+        _dense(v_scale, "v_scale", _F32, (hkv,), dev), out_ptr,
+        _dense(k_cache, "k_cache", _F16, cache, dev),
+        _dense(v_cache, "v_cache", _U8, cache, dev), cache[0], hq, hkv, d,
+        _error_word(dev_error, dev), _stream_on(stream, dev))
+    if st != K16V8_OK:
+        raise K16V8Error("k16v8_rope_axes_kv_append", st)
+
+
+def k16v8_rope_kv_append_k8v8(q, k, v, qo_indptr, positions, pair_axis, inv_freq, block_table,
+                              seq_lens, q_out, k_cache, v_cache, kv_scale, interleaved=False,
+                              attn_factor=1.0, dev_error=None, stream=None) -> None:
+    """The K8/V8 cache write: q [T,Hq,D] (or None), k, v [T,Hkv,D] as for
+    k16v8_rope_axes_kv_append, rows of sequence b being qo_indptr[b] ..
+    qo_indptr[b+1] - 1 (int32 [B+1]) and its last positions of seq_lens int32
+    [B]; positions int32 [axes,T], pair_axis and inv_freq as there, or None
+    for rows that are not turned; k_cache, v_cache uint8 [P,Hkv,16,D],
+    kv_scale fp32 [P,Hkv,2]."""
+    T, hkv, d = k.shape
+    dt, dev = k.dtype, _device(k)
+    if dt not in _X_DTYPES:
+        raise ValueError(f"k must be fp16, fp32 or bf16, got {dt}")
+    hq = 0 if q is None else q.shape[1]
+    if q is None:
+        q_ptr, q_ts, out_ptr = None, 0, None
+    else:
+        q_ptr, q_ts = q.data_ptr(), _rows(q, "q", dt, (T, hq, d), dev)
+        out_ptr = _dense(q_out, "q_out", _F16, (T, hq, d), dev)
+    row, (B, maxp) = (T, hkv, d), block_table.shape
+    P = k_cache.shape[0]
+    cache = (P, hkv, PAGE_SIZE, d)
+    if inv_freq is None:
+        half = axes = 0
+        pos_ptr = freq_ptr = pair = None
+        if positions is not None or pair_axis is not None:
+            raise ValueError("positions and pair_axis need inv_freq")
+    else:
+        half, axes = inv_freq.numel(), positions.shape[0]
+        pos_ptr = _dense(positions, "positions", _I32, (axes, T), dev)
+        freq_ptr = _dense(inv_freq, "inv_freq", _F32, (half,), dev)
+        pair = _axes(pair_axis, half)
+    st = (_lib or load_library()).k16v8_rope_kv_append_k8v8(
+        q_ptr, q_ts, k.data_ptr(), _rows(k, "k", dt, row, dev), v.data_ptr(),
+        _rows(v, "v", dt, row, dev), _X_DTYPES[dt],
+        _dense(qo_indptr, "qo_indptr", _I32, (B + 1,), dev), T, pos_ptr, axes, pair, freq_ptr,
+        2 * half, 1 if interleaved else 0, attn_factor,
+        _dense(block_table, "block_table", _I32, (B, maxp), dev), maxp,
+        _dense(seq_lens, "seq_lens", _I32, (B,), dev), B, out_ptr,
+        _dense(k_cache, "k_cache", _U8, cache, dev), _dense(v_cache, "v_cache", _U8, cache, dev),
+        _dense(kv_scale, "kv_scale", _F32, (P, hkv, 2), dev), P, hq, hkv, d,
+        _error_word(dev_error, dev), _stream_on(stream, dev))
+    if st != K16V8_OK:
+        raise K16V8Error("k16v8_rope_kv_append_k8v8", st)
+
+
+def k16v8_decode_workspace_size_k8v8(batch, num_qo_heads, head_dim) -> int:
+    """Bytes of workspace k16v8_paged_decode_attention_k8v8 needs on the current
+    device (0 for an unsupported shape)."""
+    return int(load_library().k16v8_decode_workspace_size_k8v8(batch, num_qo_heads, head_dim))
+
+
+def _workspace(workspace, dev: int):
+    """(address, bytes) of a dense workspace tensor."""
+    if workspace is None:
+        return None, 0
+    return (_dense(workspace, "workspace", workspace.dtype, workspace.shape, dev),
+            workspace.numel() * workspace.element_size())
+
+
+def k16v8_paged_decode_attention_k8v8(q, k_cache, v_cache, kv_scale, block_table, seq_lens, sm_scale,
+                                      workspace, out, lse=None, dev_error=None, stream=None) -> None:
+    """Decode attention over the K8/V8 cache: q, out fp16 [B,Hq,D], lse fp32
+    [B,Hq]; workspace uint8 of k16v8_decode_workspace_size_k8v8 bytes, not
+    shared by calls that overlap."""
+    B, hq, d = q.shape
+    dev = _device(q)
+    P, hkv = k_cache.shape[0], k_cache.shape[1]
+    cache, maxp = (P, hkv, PAGE_SIZE, d), block_table.shape[1]
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = (_lib or load_library()).k16v8_paged_decode_attention_k8v8(
+        _dense(q, "q", _F16, (B, hq, d), dev), _dense(k_cache, "k_cache", _U8, cache, dev),
+        _dense(v_cache, "v_cache", _U8, cache, dev),
+        _dense(kv_scale, "kv_scale", _F32, (P, hkv, 2), dev),
+        _dense(block_table, "block_table", _I32, (B, maxp), dev), maxp,
+        _dense(seq_lens, "seq_lens", _I32, (B,), dev), B, hq, hkv, d, P, sm_scale, ws, ws_bytes,
+        _dense(out, "out", _F16, (B, hq, d), dev),
+        None if lse is None else _dense(lse, "lse", _F32, (B, hq), dev),
+        _error_word(dev_error, dev), _stream_on(stream, dev))
+    if st != K16V8_OK:
+        raise K16V8Error("k16v8_paged_decode_attention_k8v8", st)
 
 
 def k16v8_read_device_error(dev_error, stream=None) -> int:

@@ -1,6 +1,7 @@
 """Rotary frequencies for k16v8_rope_kv_append: the plain ones and those of
 contexts longer than the model was trained on.  Host arithmetic in 64 bits;
-the result is the fp32 table the call takes."""
+the result is the fp32 table the call takes.  And which axis of a position
+turns which pair, for the calls whose positions have several."""
 from __future__ import annotations
 
 import math
@@ -58,3 +59,31 @@ def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
         freq = freq / factor * slow + freq * (1.0 - slow)
         attn_factor = 0.1 * math.log(factor) + 1.0
     return freq.to(torch.float32), attn_factor
+
+
+def rope_pair_axes(rotary_dim: int, sections, interleaved: bool = False) -> bytes:
+    """The axis of each of the rotary_dim/2 pairs, as
+    k16v8_rope_axes_kv_append takes it.  sections[a] is the number of pairs
+    that axis a turns (they sum to rotary_dim/2).
+
+    In blocks: the first sections[0] pairs are axis 0's, the next axis 1's,
+    and so on.  Interleaved: the axes take turns -- of n axes, axis a > 0 has
+    pairs a, a + n, a + 2n, ... until it has its number, axis 0 the rest."""
+    half = rotary_dim // 2
+    n = len(sections)
+    if rotary_dim < 16 or rotary_dim > 128 or rotary_dim % 16:
+        raise ValueError(f"rotary_dim must be a multiple of 16 in [16, 128], got {rotary_dim}")
+    if not 1 <= n <= 4:
+        raise ValueError(f"1 to 4 axes, got {n}")
+    if any(s < 0 for s in sections) or sum(sections) != half:
+        raise ValueError(f"sections must sum to {half} pairs, got {tuple(sections)}")
+    if not interleaved:
+        return bytes(a for a, s in enumerate(sections) for _ in range(s))
+    out = bytearray(half)
+    for a in range(1, n):
+        if sections[a] and a + n * (sections[a] - 1) >= half:
+            raise ValueError(f"{sections[a]} pairs of axis {a} do not fit {half} when {n} axes take "
+                             "turns")
+        for i in range(sections[a]):
+            out[a + n * i] = a
+    return bytes(out)

@@ -52,6 +52,8 @@ extern "C" {
 #define K16V8_MAX_SPLIT_CHUNK 8192
 #define K16V8_MAX_TREE_NODES 64   /* nodes of one sequence's drafted tree */
 #define K16V8_MAX_VOCAB (1 << 19) /* probabilities per row of tree_verify */
+#define K16V8_MAX_ROPE_AXES 4      /* axes of a position (time, height, width, ...) */
+#define K16V8_E4M3_MAX 448         /* the largest E4M3 value */
 
 typedef enum {
     K16V8_OK = 0,
@@ -700,6 +702,101 @@ int32_t k16v8_kv_compact(const uint64_t *k_caches, const uint64_t *v_caches, int
                          int32_t max_nodes, const int32_t *path_len, int32_t batch,
                          int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
                          int32_t *new_seq_lens, int32_t *dev_error, void *stream);
+
+/*
+ * rope_axes_kv_append -- k16v8_rope_kv_append for positions with several axes
+ * (time, height and width of images and video): pair i is turned by the
+ * position on axis pair_axis[i], angle positions[pair_axis[i]][t] * inv_freq[i].
+ * Everything else is as there; a token with a position outside [0, 2^24) on
+ * any axis is skipped and flags K16V8_DEVERR_POSITION.
+ *
+ *   positions  device int32 [num_axes][num_tokens]
+ *   num_axes   1 .. K16V8_MAX_ROPE_AXES
+ *   pair_axis  HOST int8 [rotary_dim/2], each in [0, num_axes); read during the
+ *              call
+ */
+int32_t k16v8_rope_axes_kv_append(
+    const void *q, int64_t q_token_stride, const void *k, int64_t k_token_stride, const void *v,
+    int64_t v_token_stride, int32_t x_dtype, const int32_t *positions, int32_t num_axes,
+    const int8_t *pair_axis, const float *inv_freq, int32_t rotary_dim, int32_t interleaved,
+    float attn_factor, const int64_t *slot_mapping, int32_t num_tokens, const float *v_scale,
+    void *q_out, void *k_cache, uint8_t *v_cache, int32_t num_pages, int32_t num_qo_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t *dev_error, void *stream);
+
+/*
+ * The K8/V8 cache: keys and values both in E4M3, with a scale for every page
+ * and KV head of either.  No counterpart on the page (whose keys are FP16); the
+ * geometry, the pages and the block tables are the same.
+ *   k_cache   E4M3 [num_pages][num_kv_heads][16][head_dim]   (one byte)
+ *   v_cache   E4M3 likewise
+ *   kv_scale  fp32 [num_pages][num_kv_heads][2]: of the keys, of the values
+ *   key = kv_scale[page][h][0] * e4m3(code),  value = kv_scale[page][h][1] * e4m3(code)
+ * A scale is a power of two in [2^-15, 2^7]; the product is then an fp16 number.
+ * All four calls need num_pages * num_kv_heads * 16 below 2^31 (the write
+ * excepted), and a batch of at most 8192 (the write: 65535).
+ */
+
+/*
+ * rope_kv_append_k8v8 -- the cache write of the K8/V8 cache, with rotary
+ * positions as in k16v8_rope_axes_kv_append (rotary_dim = 0: without).
+ * Sequence b has n = qo_indptr[b+1] - qo_indptr[b] new tokens, rows
+ * qo_indptr[b] .. of q, k and v, which take its last n positions:
+ * seq_lens[b] - n .. seq_lens[b] - 1.  Rows outside every sequence are neither
+ * read nor written.  Of every page that gets rows, and every KV head, for K
+ * (turned) and V alike, with x the new rows in fp32:
+ *   s = the smallest power of two in [2^-15, 2^7] with max |x| <= 448 s
+ *       (infinities and NaN left out); where the page holds earlier rows (a
+ *       position of it is below the first new one), not below its scale
+ *   scale = s, code = E4M3_rn_satfinite(x / s)
+ *   earlier rows of the page, where the scale has grown:
+ *   code' = E4M3_rn_satfinite(code * old scale / s)
+ * Rows behind the last position stay as they are.  q_out = fp16(turned q).
+ *
+ *   q, k, v, q_out, positions, pair_axis, inv_freq, interleaved, attn_factor
+ *                as in k16v8_rope_axes_kv_append (num_qo_heads = 0: K and V only)
+ *   rotary_dim   0 or a multiple of 16 up to head_dim; 0: positions, pair_axis
+ *                and inv_freq are not read
+ *   qo_indptr    device int32 [batch+1]
+ *   seq_lens     device int32 [batch], the new tokens included
+ *   block_table  device int32 [batch][max_pages_per_seq]; only entries of pages
+ *                that get rows are read.  A page that gets rows belongs to one
+ *                sequence (a shared one is copied first)
+ *   kv_scale     8-byte aligned, written in place
+ * A sequence with rows outside [0, num_tokens), n > seq_len or a length beyond
+ * its table flags K16V8_DEVERR_SEQLEN and is skipped; a page id outside the pool
+ * flags K16V8_DEVERR_PAGE and its tokens are skipped; a token with a position
+ * outside [0, 2^24) flags K16V8_DEVERR_POSITION and is skipped.
+ */
+int32_t k16v8_rope_kv_append_k8v8(
+    const void *q, int64_t q_token_stride, const void *k, int64_t k_token_stride, const void *v,
+    int64_t v_token_stride, int32_t x_dtype, const int32_t *qo_indptr, int32_t num_tokens,
+    const int32_t *positions, int32_t num_axes, const int8_t *pair_axis, const float *inv_freq,
+    int32_t rotary_dim, int32_t interleaved, float attn_factor, const int32_t *block_table,
+    int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t batch, void *q_out,
+    uint8_t *k_cache, uint8_t *v_cache, float *kv_scale, int32_t num_pages, int32_t num_qo_heads,
+    int32_t num_kv_heads, int32_t head_dim, int32_t *dev_error, void *stream);
+
+/*
+ * paged_decode_attention_k8v8 -- k16v8_paged_decode_attention_balanced over the
+ * K8/V8 cache: one query row per sequence, every position of it seen.
+ *   sm_scale   finite, >= 0
+ *   workspace  k16v8_decode_workspace_size_k8v8(...) bytes, 256-B aligned, needs
+ *              no initialisation; calls that overlap on the GPU, replays of
+ *              captured ones too, must not share one
+ *   q, out     device fp16 [batch][num_qo_heads][head_dim], 16-B aligned;
+ *   lse        device fp32 [batch][num_qo_heads] or NULL
+ * A sequence of length 0 gives out = 0, lse = -inf.  Lengths outside [0, 16 *
+ * max_pages_per_seq] flag K16V8_DEVERR_SEQLEN and are clamped; a page id outside
+ * the pool flags K16V8_DEVERR_PAGE and its positions are left out.
+ */
+size_t k16v8_decode_workspace_size_k8v8(int32_t batch, int32_t num_qo_heads, int32_t head_dim);
+
+int32_t k16v8_paged_decode_attention_k8v8(
+    const void *q, const uint8_t *k_cache, const uint8_t *v_cache, const float *kv_scale,
+    const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t batch,
+    int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
+    float sm_scale, void *workspace, size_t workspace_bytes, void *out, float *lse,
+    int32_t *dev_error, void *stream);
 
 /*
  * Wait for `stream`, then copy the device error word to *host_value and
