@@ -107,6 +107,19 @@ SIGNATURES = {
     "k16v8_decode_workspace_size_k8v8": (_sz, [_i32, _i32, _i32]),
     "k16v8_paged_decode_attention_k8v8": (_i32, [_P, _P, _P, _P, _P, _i32, _P, _i32, _i32, _i32, _i32,
                                                  _i32, _f32, _P, _sz, _P, _P, _P, _P]),
+    "k16v8_attention_workspace_size_k8v8": (_sz, [_i32, _i32, _i32, _i32]),
+    "k16v8_paged_prefill_attention_k8v8": (
+        _i32, [_P, _P, _i32, _i32, _P, _P, _P, _P, _i32, _P,
+               _i32, _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz, _P, _P,
+               _P, _P]),
+    "k16v8_paged_cross_attention_k8v8": (
+        _i32, [_P, _P, _i32, _i32, _P, _P, _P, _P, _i32, _P,
+               _i32, _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz, _P, _P,
+               _P, _P]),
+    "k16v8_paged_prefill_attention_k8v8_wait_test": (
+        _i32, [_P, _P, _i32, _i32, _P, _P, _P, _P, _i32, _P,
+               _i32, _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz, _P, _P,
+               _P, _P]),
     "k16v8_tree_workspace_size": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "k16v8_paged_tree_attention": (_i32, [_P, _P, _i32, _i32, _P, _P, _P, _P, _P, _i32, _P, _i32,
                                           _i32, _i32, _i32, _i32, _i32, _f32, _P, _sz, _P, _P, _P,
@@ -816,6 +829,71 @@ def k16v8_paged_decode_attention_k8v8(q, k_cache, v_cache, kv_scale, block_table
         _error_word(dev_error, dev), _stream_on(stream, dev))
     if st != K16V8_OK:
         raise K16V8Error("k16v8_paged_decode_attention_k8v8", st)
+
+
+def k16v8_attention_workspace_size_k8v8(max_qlen, num_qo_heads, num_kv_heads, head_dim) -> int:
+    """Bytes of workspace the prefill and cross attention over the K8/V8 cache
+    need on the current device (0 where the sizes are refused)."""
+    return int(load_library().k16v8_attention_workspace_size_k8v8(max_qlen, num_qo_heads,
+                                                                  num_kv_heads, head_dim))
+
+
+def _attention_k8v8(name, q, qo_indptr, max_qlen, k_cache, v_cache, kv_scale, block_table, seq_lens,
+                    max_seq_len, sm_scale, workspace, out, lse, dev_error, stream):
+    total_q, hq, d = q.shape
+    dev = _device(q)
+    P, hkv = k_cache.shape[0], k_cache.shape[1]
+    B, maxp = block_table.shape
+    cache = (P, hkv, PAGE_SIZE, d)
+    ws, ws_bytes = _workspace(workspace, dev)
+    st = getattr(_lib or load_library(), name)(
+        _dense(q, "q", _F16, (total_q, hq, d), dev),
+        _dense(qo_indptr, "qo_indptr", _I32, (B + 1,), dev), total_q, max_qlen,
+        _dense(k_cache, "k_cache", _U8, cache, dev), _dense(v_cache, "v_cache", _U8, cache, dev),
+        _dense(kv_scale, "kv_scale", _F32, (P, hkv, 2), dev),
+        _dense(block_table, "block_table", _I32, (B, maxp), dev), maxp,
+        _dense(seq_lens, "seq_lens", _I32, (B,), dev), max_seq_len, B, hq, hkv, d, P, sm_scale, ws,
+        ws_bytes, _dense(out, "out", _F16, (total_q, hq, d), dev),
+        None if lse is None else _dense(lse, "lse", _F32, (total_q, hq), dev),
+        _error_word(dev_error, dev), _stream_on(stream, dev))
+    if st != K16V8_OK:
+        raise K16V8Error(name, st)
+
+
+def k16v8_paged_prefill_attention_k8v8(q, qo_indptr, max_qlen, k_cache, v_cache, kv_scale,
+                                       block_table, seq_lens, max_seq_len, sm_scale, workspace, out,
+                                       lse=None, dev_error=None, stream=None) -> None:
+    """Causal attention of q fp16 [total_q,Hq,D] (ragged by qo_indptr int32
+    [B+1]) over the K8/V8 cache, whose seq_lens include these tokens; at most
+    max_qlen rows and max_seq_len positions per sequence; workspace uint8 of
+    k16v8_attention_workspace_size_k8v8 bytes, not shared by calls that
+    overlap."""
+    _attention_k8v8("k16v8_paged_prefill_attention_k8v8", q, qo_indptr, max_qlen, k_cache, v_cache,
+                    kv_scale, block_table, seq_lens, max_seq_len, sm_scale, workspace, out, lse,
+                    dev_error, stream)
+
+
+def k16v8_paged_cross_attention_k8v8(q, qo_indptr, max_qlen, k_cache, v_cache, kv_scale, block_table,
+                                     seq_lens, max_seq_len, sm_scale, workspace, out, lse=None,
+                                     dev_error=None, stream=None) -> None:
+    """Attention of q fp16 [total_q,Hq,D] (ragged by qo_indptr int32 [B+1])
+    over all seq_lens[b] positions of sequence b in the K8/V8 cache, e.g. an
+    encoder's states; arguments as for the prefill call."""
+    _attention_k8v8("k16v8_paged_cross_attention_k8v8", q, qo_indptr, max_qlen, k_cache, v_cache,
+                    kv_scale, block_table, seq_lens, max_seq_len, sm_scale, workspace, out, lse,
+                    dev_error, stream)
+
+
+def k16v8_paged_prefill_attention_k8v8_wait_test(q, qo_indptr, max_qlen, k_cache, v_cache, kv_scale,
+                                                 block_table, seq_lens, max_seq_len, sm_scale,
+                                                 workspace, out, lse=None, dev_error=None,
+                                                 stream=None) -> None:
+    """Test hook: k16v8_paged_prefill_attention_k8v8 with the keys of the first
+    CTA's first tile withheld, so that CTA's bounded wait expires
+    (K16V8_DEVERR_TIMEOUT)."""
+    _attention_k8v8("k16v8_paged_prefill_attention_k8v8_wait_test", q, qo_indptr, max_qlen, k_cache,
+                    v_cache, kv_scale, block_table, seq_lens, max_seq_len, sm_scale, workspace, out,
+                    lse, dev_error, stream)
 
 
 def k16v8_read_device_error(dev_error, stream=None) -> int:

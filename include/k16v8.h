@@ -732,8 +732,8 @@ int32_t k16v8_rope_axes_kv_append(
  *   kv_scale  fp32 [num_pages][num_kv_heads][2]: of the keys, of the values
  *   key = kv_scale[page][h][0] * e4m3(code),  value = kv_scale[page][h][1] * e4m3(code)
  * A scale is a power of two in [2^-15, 2^7]; the product is then an fp16 number.
- * All four calls need num_pages * num_kv_heads * 16 below 2^31 (the write
- * excepted), and a batch of at most 8192 (the write: 65535).
+ * The attention calls need num_pages * num_kv_heads * 16 below 2^31 and a batch
+ * of at most 8192, the write a batch of at most 65535.
  */
 
 /*
@@ -797,6 +797,71 @@ int32_t k16v8_paged_decode_attention_k8v8(
     int32_t num_qo_heads, int32_t num_kv_heads, int32_t head_dim, int32_t num_pages,
     float sm_scale, void *workspace, size_t workspace_bytes, void *out, float *lse,
     int32_t *dev_error, void *stream);
+
+/*
+ * paged_prefill_attention_k8v8, paged_cross_attention_k8v8 -- attention of
+ * several query rows per sequence over the K8/V8 cache, on the tensor cores.
+ * Sequence b has rows qo_indptr[b] .. qo_indptr[b+1] - 1 of q, n of them, and
+ * L = seq_lens[b] cached positions.
+ *   prefill: causal; its rows are the last n positions (already in the cache),
+ *            row i sees positions 0 .. L - n + i
+ *   cross:   every row sees all L positions (an encoder's states, written with
+ *            k16v8_rope_kv_append_k8v8 and num_qo_heads = 0); n and L are
+ *            unrelated, L may be 0
+ * Over what a row sees: lse = ln sum exp(s_j), out = sum exp(s_j - lse) v_j, s_j
+ * = sm_scale * q.k_j.  A row that sees nothing gives out = 0, lse = -inf.  What
+ * is stored at a position that a row does not see (NaN, inf) does not reach it.
+ * The weights are rounded to fp16 before they meet the values: 2^-11 relative,
+ * or 2^-32 of the row's largest weight where that is more.
+ *
+ *   q            device fp16 [total_q][num_qo_heads][head_dim], 16-B aligned
+ *   qo_indptr    device int32 [batch+1]
+ *   max_qlen     host: no sequence has more rows
+ *   max_seq_len  host: no sequence is longer; at most 2^30 and 16 *
+ *                max_pages_per_seq.  num_kv_heads at most 4095
+ *   sm_scale     finite, >= 0
+ *   workspace    device, 256-B aligned, k16v8_attention_workspace_size_k8v8(...)
+ *                bytes for the same arguments on the same device (0 only where
+ *                they are refused); needs no initialisation.  Calls that overlap
+ *                on the GPU, replays of captured ones too, must not share one.
+ *   out          device fp16 like q; lse device fp32 [total_q][num_qo_heads] or
+ *                NULL.  Rows of no sequence are left as they are
+ * A sequence with rows outside [0, total_q), n > max_qlen, a length outside [0,
+ * max_seq_len] or (prefill) n > L flags K16V8_DEVERR_SEQLEN and is skipped; a
+ * page id outside the pool flags K16V8_DEVERR_PAGE and its positions are seen by
+ * no row.
+ */
+size_t k16v8_attention_workspace_size_k8v8(int32_t max_qlen, int32_t num_qo_heads,
+                                           int32_t num_kv_heads, int32_t head_dim);
+
+int32_t k16v8_paged_prefill_attention_k8v8(
+    const void *q, const int32_t *qo_indptr, int32_t total_q, int32_t max_qlen,
+    const uint8_t *k_cache, const uint8_t *v_cache, const float *kv_scale,
+    const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+    int32_t max_seq_len, int32_t batch, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t num_pages, float sm_scale, void *workspace, size_t workspace_bytes,
+    void *out, float *lse, int32_t *dev_error, void *stream);
+
+int32_t k16v8_paged_cross_attention_k8v8(
+    const void *q, const int32_t *qo_indptr, int32_t total_q, int32_t max_qlen,
+    const uint8_t *k_cache, const uint8_t *v_cache, const float *kv_scale,
+    const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+    int32_t max_seq_len, int32_t batch, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t num_pages, float sm_scale, void *workspace, size_t workspace_bytes,
+    void *out, float *lse, int32_t *dev_error, void *stream);
+
+/*
+ * Test hook of its bounded waits, as k16v8_paged_tree_attention_wait_test: CTA 0
+ * (the first tiles of the first sequence's KV head 0) withholds the keys of its
+ * first tile, so its rows, and those joined with them, are not valid.
+ */
+int32_t k16v8_paged_prefill_attention_k8v8_wait_test(
+    const void *q, const int32_t *qo_indptr, int32_t total_q, int32_t max_qlen,
+    const uint8_t *k_cache, const uint8_t *v_cache, const float *kv_scale,
+    const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *seq_lens,
+    int32_t max_seq_len, int32_t batch, int32_t num_qo_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t num_pages, float sm_scale, void *workspace, size_t workspace_bytes,
+    void *out, float *lse, int32_t *dev_error, void *stream);
 
 /*
  * Wait for `stream`, then copy the device error word to *host_value and
