@@ -130,7 +130,8 @@ static bool layout(int32_t max_q, Layout *w) {
 }
 
 template <bool kWide, bool kTest>
-static int32_t launch_split(const CUtensorMap &mq, const Args &a, int ctas, cudaStream_t s) {
+static int32_t launch_split(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
+                            const Args &a, int ctas, cudaStream_t s) {
   static bool configured[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return K16V8_ERR_CUDA;
@@ -143,7 +144,7 @@ static int32_t launch_split(const CUtensorMap &mq, const Args &a, int ctas, cuda
     if (dev < 64) configured[dev] = true;
   }
   return k16v8_launch_pdl(attention_kernel<kWide, kTest>, dim3(ctas), dim3(kThreads), smem, s, mq,
-                          a);
+                          mk, mv, a);
 }
 
 }  // namespace attn8
@@ -222,10 +223,13 @@ static int32_t attention_k8v8(bool causal, const void *q, const int32_t *qo_indp
                       lse,
                       dev_error};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CUtensorMap mq;
-  if (!map_rows(&mq, q, num_qo_heads, total_q)) return K16V8_ERR_CUDA;
-  st = max_qlen > attn8::kTileTokens ? attn8::launch_split<true, kTest>(mq, a, w.ctas, s)
-                                     : attn8::launch_split<false, kTest>(mq, a, w.ctas, s);
+  CUtensorMap mq, mk, mv;
+  const uint64_t pool = static_cast<uint64_t>(num_pages) * num_kv_heads * kPage;
+  if (!map_rows(&mq, q, num_qo_heads, total_q) || !map_codes(&mk, k_cache, pool) ||
+      !map_codes(&mv, v_cache, pool))
+    return K16V8_ERR_CUDA;
+  st = max_qlen > attn8::kTileTokens ? attn8::launch_split<true, kTest>(mq, mk, mv, a, w.ctas, s)
+                                     : attn8::launch_split<false, kTest>(mq, mk, mv, a, w.ctas, s);
   if (st != K16V8_OK) return st;
   return max_qlen > 16 ? attn8::launch_merge<4>(a, w.ctas, s)
                        : attn8::launch_merge<2>(a, w.ctas, s);

@@ -16,7 +16,7 @@
 // two parts of 64 positions, each with half of the slot's S columns, so that one
 // part's S and P V run under the other's softmax.
 //
-// Keys and values arrive as codes (bulk copies of 2 KB, a page and head) with
+// Keys and values arrive as codes (TMA boxes of 2 KB, a page and head) with
 // their pages' scales (4-byte asynchronous copies on the same barrier), and are
 // widened to fp16 half tiles of 64 positions in the layouts the MMAs read: a code
 // times a power of two in the cache's range is an fp16 number, so the MMAs see
@@ -41,7 +41,7 @@ constexpr int kRows = kTileTokens * kGroup;  // 128
 constexpr int kPagesPerTile = kKv / kPage;   // 8
 constexpr int kThreads = 512;
 constexpr int kOutWarp = 9, kLoadVWarp = 12, kLoadKWarp = 13, kScoreWarp = 15;
-constexpr int kWidenThreads = 64;            // for keys, and for values
+constexpr int kWidenWarps = 2;               // for keys, and for values
 constexpr int kPieceRing = 4;
 constexpr int kPieceReaders = 16;            // every warp
 constexpr int kHalves = 3;                   // half tiles of fp16 keys, and of values
@@ -85,12 +85,12 @@ enum {
   kBarQFull = 0,      // +slot
   kBarQEmpty = 2,     // +slot
   kBarKstFull = 4,    // +stage, 33 arrivals: the bytes' and one per lane for the scales
-  kBarKstEmpty = 7,   // +stage, kWidenThreads arrivals
+  kBarKstEmpty = 7,   // +stage, kWidenWarps arrivals
   kBarVstFull = 10,   // +stage, as for keys
   kBarVstEmpty = 13,  // +stage
-  kBarKFull = 16,     // +half, kWidenThreads arrivals
+  kBarKFull = 16,     // +half, kWidenWarps arrivals
   kBarKEmpty = 19,    // +half
-  kBarVFull = 22,     // +half, kWidenThreads arrivals
+  kBarVFull = 22,     // +half, kWidenWarps arrivals
   kBarVEmpty = 25,    // +half
   kBarSFull = 28,     // +slot + 2 * part
   kBarPFull = 32,     // +slot + 2 * part, 4 arrivals (one per warp)
@@ -189,17 +189,20 @@ __device__ __forceinline__ void widen16(const uint4 &raw, __half2 scale, uint4 &
   lo = make_uint4(h[0], h[1], h[2], h[3]);
   hi = make_uint4(h[4], h[5], h[6], h[7]);
 }
-// Dims 16c .. 16c + 15 of position hp of a half tile: two 16-byte chunks in one of
-// its two blocks.  The lanes of the second block store their chunks in the other
-// order, so the eight lanes of a row meet in no bank.
-__device__ __forceinline__ void put16(uint8_t *half, int hp, int c, const uint4 &lo,
-                                      const uint4 &hi) {
-  const bool second = c & 4;
-  uint8_t *blk = half + (second ? kBlk : 0);
-  const uint32_t off = hp * 128 + (c & 3) * 32;
-  *reinterpret_cast<uint4 *>(blk + tc::sw128(off + (second ? 16 : 0))) = second ? hi : lo;
-  *reinterpret_cast<uint4 *>(blk + tc::sw128(off + (second ? 0 : 16))) = second ? lo : hi;
-}
+// Where a lane of a widening warp finds and puts 16 codes.  Eight lanes take the
+// same 16 dims of eight neighbouring positions: the codes are staged with the
+// 128-byte swizzle and the fp16 tile has it too, so they meet in no bank on either
+// side, and every step of eight positions is a constant further.
+struct Lanes {
+  uint32_t from, to0, to1;
+  __device__ __forceinline__ Lanes(int rank, int lane) {
+    const uint32_t row = lane & 7, c = rank * 4 + (lane >> 3);  // dims 16c .. 16c + 15
+    from = row * 128 + ((c ^ row) << 4);
+    const uint32_t to = (c >> 2) * kBlk + row * 128, pair = (c & 3) * 2;
+    to0 = to + ((pair ^ row) << 4);
+    to1 = to + (((pair + 1) ^ row) << 4);
+  }
+};
 
 // An asynchronous load's registers stay its own until here.
 __device__ __forceinline__ void keep(const uint32_t (&r)[32]) {
@@ -247,7 +250,8 @@ __device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[16],
 // after kTestSpins polls and every role takes the abort path.
 template <bool kWide, bool kTest>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
-    const __grid_constant__ CUtensorMap tmap_q, const Args a) {
+    const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+    const __grid_constant__ CUtensorMap tmap_v, const Args a) {
   using M = Smem<kWide>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sQ = smem_raw + M::kQ;
@@ -281,6 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   // ---- set-up that needs nothing of the preceding kernel ----
   if (warp == kLoadKWarp && lane == 0) {
     tc::prefetch_tensormap(&tmap_q);
+    tc::prefetch_tensormap(&tmap_k);
+    tc::prefetch_tensormap(&tmap_v);
   }
   if (warp == 0) {
     tc::tmem_alloc(tmem_slot, kTmemCols);
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       if ((i >= kBarKstFull && i < kBarKstEmpty) || (i >= kBarVstFull && i < kBarVstEmpty)) count = 33;
       if ((i >= kBarKstEmpty && i < kBarVstFull) || (i >= kBarVstEmpty && i < kBarKEmpty) ||
           (i >= kBarVFull && i < kBarVEmpty))
-        count = kWidenThreads;
+        count = kWidenWarps;
       if (i >= kBarPFull && i < kBarPV) count = 4;
       if (i == kBarJoin) count = 8;
       if (i == kBarOEmpty) count = 8;
@@ -577,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     pdl_launch_dependents();
   } else if (warp == 8 || warp == 10) {
     // ================= keys to fp16 =================
-    const int dt = (warp == 10 ? 32 : 0) + lane;
+    const Lanes at(warp == 10, lane);
     Piece pc;
     Ring<kPieceRing> ring;
     Ring<M::kStages> src;
@@ -592,31 +598,36 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           if (dst.wrapped) ok = __all_sync(kFull, wait(kBarKEmpty + dst.s, dst.phase ^ 1));
           if (!ok) break;
           uint8_t *half = sK + dst.s * kHalfBytes;
-          // 16 codes of position hp of the half; two steps to a page.  What lies
-          // behind the last position, or in a rejected page, is masked as scores
-          const int hp0 = dt >> 3, c16 = dt & 7;
-          const uint8_t *from = sKst + src.s * kStage + (h * kHalf + hp0) * 128 + c16 * 16;
-          uint4 raw[8];
+          // (what lies behind the last position, or in a rejected page, is masked as
+          // scores)
+          const uint8_t *from = sKst + src.s * kStage + h * (kStage / 2) + at.from;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 8; i0 += 4) {  // two pages
+            uint4 raw[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) raw[i] = *reinterpret_cast<const uint4 *>(from + i * 8 * 128);
+            for (int i = 0; i < 4; ++i)
+              raw[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i) * 1024);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4 lo, hi;
-            widen16(raw[i], __float2half2_rn(sc[h * 4 + (i >> 1)]), lo, hi);
-            put16(half, hp0 + 8 * i, c16, lo, hi);
+            for (int i = 0; i < 4; ++i) {
+              uint4 lo, hi;
+              widen16(raw[i], __float2half2_rn(sc[h * 4 + ((i0 + i) >> 1)]), lo, hi);
+              *reinterpret_cast<uint4 *>(half + (i0 + i) * 1024 + at.to0) = lo;
+              *reinterpret_cast<uint4 *>(half + (i0 + i) * 1024 + at.to1) = hi;
+            }
           }
           fence_proxy_async();
-          mbar_arrive(&bars[kBarKFull + dst.s]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarKFull + dst.s]);
           dst.next();
         }
         if (!ok) break;
-        mbar_arrive(&bars[kBarKstEmpty + src.s]);
+        if (lane == 0) mbar_arrive(&bars[kBarKstEmpty + src.s]);
         src.next();
       }
     }
   } else if (warp == 11 || warp == 14) {
     // ================= values to fp16 =================
-    const int dt = (warp == 14 ? 32 : 0) + lane;
+    const Lanes at(warp == 14, lane);
     Piece pc;
     Ring<kPieceRing> ring;
     Ring<M::kStages> src;
@@ -634,42 +645,50 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           if (dst.wrapped) ok = __all_sync(kFull, wait(kBarVEmpty + dst.s, dst.phase ^ 1));
           if (!ok) break;
           uint8_t *half = sV + dst.s * kHalfBytes;
-          const int hp0 = dt >> 3, c16 = dt & 7;
-          const uint8_t *from = sVst + src.s * kStage + (h * kHalf + hp0) * 128 + c16 * 16;
-          uint4 raw[8];
+          const uint8_t *from = sVst + src.s * kStage + h * (kStage / 2) + at.from;
+          const bool special = fresh < (h + 1) * kHalf || bad;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 8; i0 += 4) {
+            uint4 raw[4];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) raw[i] = *reinterpret_cast<const uint4 *>(from + i * 8 * 128);
-          if (fresh < (h + 1) * kHalf || bad) {
+            for (int i = 0; i < 4; ++i)
+              raw[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i) * 1024);
+            if (special) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int pos = h * kHalf + hp0 + 8 * i;
-              if (pos >= live || (bad >> (pos >> 4) & 1)) {
-                raw[i] = make_uint4(0, 0, 0, 0);  // may hold anything, NaN too
-              } else if (pos >= fresh) {  // NaN codes must not reach rows that do not see it
-                const uint32_t n0 = nan_bytes(raw[i].x), n1 = nan_bytes(raw[i].y),
-                               n2 = nan_bytes(raw[i].z), n3 = nan_bytes(raw[i].w);
-                if (n0 | n1 | n2 | n3) {
-                  raw[i] = make_uint4(raw[i].x & ~n0, raw[i].y & ~n1, raw[i].z & ~n2, raw[i].w & ~n3);
-                  const int rel = pos - fresh;
-                  atomicOr(&nan_rows[(p_idx & 3) * 2 + (rel >> 5)], 1u << (rel & 31));
+              for (int i = 0; i < 4; ++i) {
+                const int pos = h * kHalf + 8 * (i0 + i) + (lane & 7);
+                if (pos >= live || (bad >> (pos >> 4) & 1)) {
+                  raw[i] = make_uint4(0, 0, 0, 0);  // may hold anything, NaN too
+                } else if (pos >= fresh) {  // NaN codes must not reach rows that do not see it
+                  const uint32_t n0 = nan_bytes(raw[i].x), n1 = nan_bytes(raw[i].y),
+                                 n2 = nan_bytes(raw[i].z), n3 = nan_bytes(raw[i].w);
+                  if (n0 | n1 | n2 | n3) {
+                    raw[i] =
+                        make_uint4(raw[i].x & ~n0, raw[i].y & ~n1, raw[i].z & ~n2, raw[i].w & ~n3);
+                    const int rel = pos - fresh;
+                    atomicOr(&nan_rows[(p_idx & 3) * 2 + (rel >> 5)], 1u << (rel & 31));
+                  }
                 }
               }
             }
-          }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int page = h * 4 + (i >> 1);
-            const bool none = (bad >> page & 1) || page * kPage >= live;  // its scale is not there
-            uint4 lo, hi;
-            widen16(raw[i], __float2half2_rn(none ? 0.f : sc[page]), lo, hi);
-            put16(half, hp0 + 8 * i, c16, lo, hi);
+            for (int i = 0; i < 4; ++i) {
+              const int page = h * 4 + ((i0 + i) >> 1);
+              // (a scale that was not copied may be anything)
+              const bool none = special && ((bad >> page & 1) || page * kPage >= live);
+              uint4 lo, hi;
+              widen16(raw[i], __float2half2_rn(none ? 0.f : sc[page]), lo, hi);
+              *reinterpret_cast<uint4 *>(half + (i0 + i) * 1024 + at.to0) = lo;
+              *reinterpret_cast<uint4 *>(half + (i0 + i) * 1024 + at.to1) = hi;
+            }
           }
           fence_proxy_async();
-          mbar_arrive(&bars[kBarVFull + dst.s]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarVFull + dst.s]);
           dst.next();
         }
         if (!ok) break;
-        mbar_arrive(&bars[kBarVstEmpty + src.s]);
+        if (lane == 0) mbar_arrive(&bars[kBarVstEmpty + src.s]);
         src.next();
       }
     }
@@ -716,10 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         }
         __syncwarp();
         if (pid >= 0) {
-          const int64_t tile = static_cast<int64_t>(pid) * a.hkv + pc.g;
-          bulk_g2s(sVst + dst.s * kStage + lane * 2048, a.v_cache + tile * k8v8::kTileBytes, 2048,
-                   &bars[kBarVstFull + dst.s]);
-          copy4(scale_v + dst.s * kPagesPerTile + lane, a.kv_scale + 2 * tile + 1);
+          const int tile = pid * a.hkv + pc.g;
+          tc::tma_load_2d(sVst + dst.s * kStage + lane * 2048, &tmap_v, 0, tile * kPage,
+                          &bars[kBarVstFull + dst.s]);
+          copy4(scale_v + dst.s * kPagesPerTile + lane, a.kv_scale + 2 * static_cast<int64_t>(tile) + 1);
         }
         arrive_behind_copies(&bars[kBarVstFull + dst.s]);
         if (t + 1 < pc.t1) pid = page_id(a, pc, t + 1, lane);
@@ -758,10 +777,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         __syncwarp();
         if (!withheld) {
           if (pid >= 0) {
-            const int64_t tile = static_cast<int64_t>(pid) * a.hkv + pc.g;
-            bulk_g2s(sKst + dst.s * kStage + lane * 2048, a.k_cache + tile * k8v8::kTileBytes, 2048,
-                     &bars[kBarKstFull + dst.s]);
-            copy4(scale_k + dst.s * kPagesPerTile + lane, a.kv_scale + 2 * tile);
+            const int tile = pid * a.hkv + pc.g;
+            tc::tma_load_2d(sKst + dst.s * kStage + lane * 2048, &tmap_k, 0, tile * kPage,
+                            &bars[kBarKstFull + dst.s]);
+            copy4(scale_k + dst.s * kPagesPerTile + lane, a.kv_scale + 2 * static_cast<int64_t>(tile));
           }
           arrive_behind_copies(&bars[kBarKstFull + dst.s]);
         }
