@@ -204,6 +204,26 @@ struct Lanes {
   }
 };
 
+__device__ __forceinline__ void put16(uint8_t *half, const Lanes &at, int step, const uint4 &raw,
+                                      float scale) {
+  uint4 lo, hi;
+  widen16(raw, __float2half2_rn(scale), lo, hi);
+  *reinterpret_cast<uint4 *>(half + step * 1024 + at.to0) = lo;
+  *reinterpret_cast<uint4 *>(half + step * 1024 + at.to1) = hi;
+}
+// A half tile, every position of it: scales of its four pages at sc.
+__device__ __forceinline__ void widen_half(uint8_t *half, const uint8_t *from, const Lanes &at,
+                                           const float *sc) {
+#pragma unroll 1
+  for (int i0 = 0; i0 < 8; i0 += 4) {  // two pages
+    uint4 raw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) raw[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put16(half, at, i0 + i, raw[i], sc[(i0 + i) >> 1]);
+  }
+}
+
 // An asynchronous load's registers stay its own until here.
 __device__ __forceinline__ void keep(const uint32_t (&r)[32]) {
 #pragma unroll
@@ -601,20 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           // (what lies behind the last position, or in a rejected page, is masked as
           // scores)
           const uint8_t *from = sKst + src.s * kStage + h * (kStage / 2) + at.from;
-#pragma unroll 1
-          for (int i0 = 0; i0 < 8; i0 += 4) {  // two pages
-            uint4 raw[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              raw[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i) * 1024);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 lo, hi;
-              widen16(raw[i], __float2half2_rn(sc[h * 4 + ((i0 + i) >> 1)]), lo, hi);
-              *reinterpret_cast<uint4 *>(half + (i0 + i) * 1024 + at.to0) = lo;
-              *reinterpret_cast<uint4 *>(half + (i0 + i) * 1024 + at.to1) = hi;
-            }
-          }
+          widen_half(half, from, at, sc + h * 4);
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarKFull + dst.s]);
@@ -646,40 +653,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           if (!ok) break;
           uint8_t *half = sV + dst.s * kHalfBytes;
           const uint8_t *from = sVst + src.s * kStage + h * (kStage / 2) + at.from;
-          const bool special = fresh < (h + 1) * kHalf || bad;
+          if (fresh >= (h + 1) * kHalf && !bad) {  // seen by every row
+            widen_half(half, from, at, sc + h * 4);
+          } else {
 #pragma unroll 1
-          for (int i0 = 0; i0 < 8; i0 += 4) {
-            uint4 raw[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              raw[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i) * 1024);
-            if (special) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int pos = h * kHalf + 8 * (i0 + i) + (lane & 7);
-                if (pos >= live || (bad >> (pos >> 4) & 1)) {
-                  raw[i] = make_uint4(0, 0, 0, 0);  // may hold anything, NaN too
-                } else if (pos >= fresh) {  // NaN codes must not reach rows that do not see it
-                  const uint32_t n0 = nan_bytes(raw[i].x), n1 = nan_bytes(raw[i].y),
-                                 n2 = nan_bytes(raw[i].z), n3 = nan_bytes(raw[i].w);
+            for (int i = 0; i < 8; ++i) {
+              const int pos = h * kHalf + 8 * i + (lane & 7), page = pos >> 4;
+              uint4 raw = make_uint4(0, 0, 0, 0);  // what is not seen may hold anything, NaN too
+              float scale = 0.f;
+              if (pos < live && !(bad >> page & 1)) {
+                raw = *reinterpret_cast<const uint4 *>(from + i * 1024);
+                scale = sc[page];
+                if (pos >= fresh) {  // NaN codes must not reach rows that do not see them
+                  const uint32_t n0 = nan_bytes(raw.x), n1 = nan_bytes(raw.y),
+                                 n2 = nan_bytes(raw.z), n3 = nan_bytes(raw.w);
                   if (n0 | n1 | n2 | n3) {
-                    raw[i] =
-                        make_uint4(raw[i].x & ~n0, raw[i].y & ~n1, raw[i].z & ~n2, raw[i].w & ~n3);
+                    raw = make_uint4(raw.x & ~n0, raw.y & ~n1, raw.z & ~n2, raw.w & ~n3);
                     const int rel = pos - fresh;
                     atomicOr(&nan_rows[(p_idx & 3) * 2 + (rel >> 5)], 1u << (rel & 31));
                   }
                 }
               }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int page = h * 4 + ((i0 + i) >> 1);
-              // (a scale that was not copied may be anything)
-              const bool none = special && ((bad >> page & 1) || page * kPage >= live);
-              uint4 lo, hi;
-              widen16(raw[i], __float2half2_rn(none ? 0.f : sc[page]), lo, hi);
-              *reinterpret_cast<uint4 *>(half + (i0 + i) * 1024 + at.to0) = lo;
-              *reinterpret_cast<uint4 *>(half + (i0 + i) * 1024 + at.to1) = hi;
+              put16(half, at, i, raw, scale);
             }
           }
           fence_proxy_async();
