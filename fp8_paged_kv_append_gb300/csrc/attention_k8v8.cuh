@@ -23,7 +23,7 @@
 // the cache's values exactly and nothing is scaled afterwards.
 //
 // Warp roles (16 warps): 0-3 / 4-7 softmax of slot 0 / 1, one thread per row; 8,
-// 10 widen keys, 11, 14 values; 15 issues S = Q K^T and 9 O += P V; 13 loads Q
+// 10 widen keys, 11, 14 values; 9 / 15 issue the MMAs of slot 0 / 1; 13 loads Q
 // (TMA) and key pages; 12 loads value pages, walks the CTA's pieces and hands them
 // to the others.  Every hand-off is an mbarrier, every wait is bounded.
 #pragma once
@@ -40,7 +40,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kRows = kTileTokens * kGroup;  // 128
 constexpr int kPagesPerTile = kKv / kPage;   // 8
 constexpr int kThreads = 512;
-constexpr int kOutWarp = 9, kLoadVWarp = 12, kLoadKWarp = 13, kScoreWarp = 15;
+constexpr int kMmaWarp0 = 9, kMmaWarp1 = 15, kLoadVWarp = 12, kLoadKWarp = 13;
 constexpr int kWidenWarps = 2;               // for keys, and for values
 constexpr int kPieceRing = 4;
 constexpr int kPieceReaders = 16;            // every warp
@@ -83,24 +83,24 @@ struct Smem {
 
 enum {
   kBarQFull = 0,      // +slot
-  kBarQEmpty = 2,     // +slot
+  kBarQEmpty = 2,     // +slot, 2 arrivals: of either slot's MMAs
   kBarKstFull = 4,    // +stage, 33 arrivals: the bytes' and one per lane for the scales
   kBarKstEmpty = 7,   // +stage, kWidenWarps arrivals
   kBarVstFull = 10,   // +stage, as for keys
   kBarVstEmpty = 13,  // +stage
   kBarKFull = 16,     // +half, kWidenWarps arrivals
-  kBarKEmpty = 19,    // +half
+  kBarKEmpty = 19,    // +half, 2 arrivals: both slots' MMAs have read it
   kBarVFull = 22,     // +half, kWidenWarps arrivals
-  kBarVEmpty = 25,    // +half
+  kBarVEmpty = 25,    // +half, as for keys
   kBarSFull = 28,     // +slot + 2 * part
   kBarPFull = 32,     // +slot + 2 * part, 4 arrivals (one per warp)
   kBarPV = 36,        // +slot + 2 * part: the part's P V is done
-  kBarODone = 40,     // +slot: the slot's last P V of a piece
+  kBarODone = 40,     // +slot: the slot's last P V of a piece (or it has none)
   kBarOEmpty = 42,    // 8 arrivals: both O tiles have been read
   kBarJoin = 43,      // 8 arrivals (one per warp): both slots' statistics are in shared memory
   kBarPiece = 44,     // +ring entry: described
   kBarTaken = 48,     // +ring entry: kPieceReaders arrivals
-  kBarDrain = 52,     // +0, 1: every S, every P V
+  kBarDrain = 52,     // +slot: every MMA
   kNumBars = 54
 };
 static_assert(kNumBars * 8 + 16 <= kBarBytes, "barriers");
@@ -320,6 +320,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           (i >= kBarVFull && i < kBarVEmpty))
         count = kWidenWarps;
       if (i >= kBarPFull && i < kBarPV) count = 4;
+      if ((i >= kBarQEmpty && i < kBarKstFull) || (i >= kBarKEmpty && i < kBarVFull) ||
+          (i >= kBarVEmpty && i < kBarSFull))
+        count = 2;
       if (i == kBarJoin) count = 8;
       if (i == kBarOEmpty) count = 8;
       if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
@@ -366,7 +369,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     const uint32_t tOther = tmem + 256 + (w ^ 1) * 128;
     Ring<kPieceRing> ring;
     uint32_t units = 0;             // of this slot so far
-    Pair last;                      // pieces in which a slot had units, so far
     uint32_t tiles = 0;             // of the CTA so far
     uint32_t joins = 0;             // pieces with one row tile, so far
     bool ok = true;
@@ -381,9 +383,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       const bool warp_live = (two ? w * kTileTokens : 0) + (warp & 3) * 8 < pc.n;
       // the new tokens this row sees: itself and those before it
       const uint64_t mask_word = a.causal && row_valid ? ~0ull >> (63 - token) : 0;
-      const int mine = two ? pc.tiles : (pc.tiles + 1 - w) / 2;
+      const int after = two ? 0 : w ^ pc.turn;  // the slot's first tile
+      const int mine = two ? pc.tiles : (pc.tiles + 1 - after) / 2;
       const int n_tiles = pc.tiles, d0 = pc.base - pc.t0 * kKv;
-      const int theirs = two ? 0 : (pc.tiles + w) / 2;  // units of the other slot to join
+      const int theirs = two ? 0 : (pc.tiles + after) / 2;  // units of the other slot to join
       float m_used = -INFINITY, l = 0.f;
       for (int k = 0; ok && k < mine; ++k, ++units) {
 #pragma unroll 1
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             continue;
           }
           tc::fence_after_sync();
-          const int tile = two ? k : 2 * k + w;
+          const int tile = two ? k : 2 * k + after;
           const int d = d0 - tile * kKv;  // prefix columns of this tile
           const uint32_t bad = info[(tiles + tile) & 7];
           const uint32_t tSp = tS + lane_base + part * kChunks * 32;
@@ -495,12 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       if (!ok) break;
       tiles += n_tiles;
       // ---- end of the piece: this slot's O, and with one row tile the other's ----
-      const bool second = two || pc.tiles > 1;  // slot 1 has units
-      if (mine > 0) ok = __all_sync(kFull, wait(kBarODone + w, last[w] & 1));
-      if (ok && theirs > 0) ok = __all_sync(kFull, wait(kBarODone + (w ^ 1), last[w ^ 1] & 1));
+      ok = __all_sync(kFull, wait(kBarODone + w, p_idx & 1));
+      if (ok && !two) ok = __all_sync(kFull, wait(kBarODone + (w ^ 1), p_idx & 1));
       if (!ok) break;
-      last.add(0);
-      last.add(1, second);
       tc::fence_after_sync();
       const int pn = (p_idx & 3) * 2;
       const uint64_t nan_mask = nan_rows[pn] | static_cast<uint64_t>(nan_rows[pn + 1]) << 32;
@@ -811,20 +811,35 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         if (uses[s] > 0) mbar_wait_bounded(&bars[kBarQFull + s], (uses[s] - 1) & 1);
     }
     __syncwarp();
-  } else if (warp == kScoreWarp || warp == kOutWarp) {
-    // ================= MMA issue: S = Q K^T by one warp, O += P V by the other =================
-    // Each whole warp walks the units, so every operand stays uniform; one lane
-    // issues.  Every lane tests one barrier, for the phase that its next use
-    // needs, and a unit waits for those in a mask: a test takes ~140 cycles, and
-    // what a unit's issue takes bounds the tile.
+  } else if (warp == kMmaWarp0 || warp == kMmaWarp1) {
+    // ================= MMA issue for slot w: O += P V, then the next S = Q K^T =================
+    // The MMAs of one thread execute in the order of their issue, so an S may follow
+    // the P V that reads the same columns without waiting for it.  The whole warp
+    // walks the units, so every operand stays uniform; one lane issues.  Every lane
+    // tests one barrier, for the phase that its next use needs, and a unit waits for
+    // those in a mask: a test takes ~140 cycles.
+    // A test tells a phase from the one before or behind it by parity alone, so the
+    // barrier must be in that phase or have completed it and no other.  Half tiles:
+    // the slots take turns over tiles with one row tile, so of any two tiles in a
+    // row one at least is the slot's, and a half implies those before it; its stage
+    // is not filled again before the slot has released it.  Queries and O tiles: a
+    // slot without a tile of a piece waits and arrives for that piece all the same.
+    const int w = warp == kMmaWarp1;
     const bool leader = tc::elect_one();
-    uint64_t *bar = bars;  // this lane's
-    uint32_t parity = 0;
+    // lane 0: the K half; 1: the V half; 2, 3: P of either part; 4, 5: the queries;
+    // 6: the last piece's O tiles have been read (the first passes)
+    constexpr uint32_t kK = 1u, kV = 2u, kP = 4u, kQ = 16u, kO = 64u;
+    uint64_t *bar = bars + (lane == 0   ? kBarKFull
+                            : lane == 1 ? kBarVFull
+                            : lane < 4  ? kBarPFull + w + 2 * (lane - 2)
+                            : lane < 6  ? kBarQFull + lane - 4
+                                        : kBarOEmpty);
+    uint32_t parity = lane == 6;
     uint32_t ready = 0;  // lanes whose barrier is known to be there
     auto poll = [&](uint32_t need) {
       for (uint32_t i = 0; (ready & need) != need; ++i) {
         ready = __ballot_sync(kFull, mbar_test_wait(bar, parity));
-        const uint32_t limit = withholds && warp == kScoreWarp ? kTestSpins : kMaxSpins;
+        const uint32_t limit = withholds ? kTestSpins : kMaxSpins;
         if ((i & 255u) == 255u && (i >= limit || *abort_flag)) {
           if (!*abort_flag) flag_error(a.dev_error, K16V8_DEVERR_TIMEOUT);
           *abort_flag = 1;
@@ -838,120 +853,135 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       parity ^= lanes >> lane & 1u;
       ready &= ~lanes;
     };
+    Ring<kHalves> kr, vr;
+    auto next_k = [&]() {
+      kr.next();
+      ready &= ~kK;
+      if (lane == 0) {
+        bar = &bars[kBarKFull + kr.s];
+        parity = kr.phase;
+      }
+    };
+    auto next_v = [&]() {
+      vr.next();
+      ready &= ~kV;
+      if (lane == 1) {
+        bar = &bars[kBarVFull + vr.s];
+        parity = vr.phase;
+      }
+    };
+    constexpr uint32_t kIdescS = tc::idesc_f16_f32(kRows, kHalf, false, false);
+    constexpr uint32_t kIdescO = tc::idesc_f16_f32(kRows, kHeadDim, false, true);
+    const uint64_t dk = tc::smem_desc_sw128(smem_addr(sK), 16, 1024);
+    const uint64_t dv = tc::smem_desc_sw128(smem_addr(sV), kBlk, 1024);
+    const uint32_t dk_lo = static_cast<uint32_t>(dk), dk_hi = static_cast<uint32_t>(dk >> 32);
+    const uint32_t dv_lo = static_cast<uint32_t>(dv), dv_hi = static_cast<uint32_t>(dv >> 32);
+    const uint32_t dq_lo = dk_lo + (M::kQ >> 4) - (M::kK >> 4);
+    const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
+
+    // the tile whose S has been issued and whose P V has not
+    bool have = false, o_first = false, o_last = false, o_two = false;
+    int o_skip = 0;  // tiles of the other slot before it
+    auto out = [&](int part) {
+      if (part == 0) {
+        for (; o_skip > 0; --o_skip) {
+          next_v();
+          next_v();
+        }
+        if (o_first) {
+          if (!poll(kO)) return false;
+          used(kO);
+        }
+      }
+      if (!poll(kV | kP << part)) return false;
+      used(kP << part);
+      const uint32_t b0 = dv_lo + vr.s * (kHalfBytes / 16), p0 = tS + part * kHalf;
+      const bool add = !o_first || part > 0;
+#pragma unroll
+      for (int kk = 0; kk < kHalf / 16; ++kk)
+        if (leader) tc::mma_f16_ts(tO, p0 + kk * 8, b0 + kk * 128, dv_hi, kIdescO, add || kk > 0);
+      if (leader) {
+        tc::mma_commit(&bars[kBarPV + w + 2 * part]);
+        tc::mma_commit(&bars[kBarVEmpty + vr.s]);
+        if (!o_two) mbar_arrive(&bars[kBarVEmpty + vr.s]);  // (the other slot does not read it)
+        if (o_last && part == kParts - 1) tc::mma_commit(&bars[kBarODone + w]);
+      }
+      next_v();
+      return true;
+    };
+    auto flush = [&]() {
+      const bool done = !have || (out(0) && out(1));
+      have = false;
+      return done;
+    };
     Piece pc;
     Ring<kPieceRing> ring;
-    bool ok = true;
-    if (warp == kScoreWarp) {
-      constexpr uint32_t kIdesc = tc::idesc_f16_f32(kRows, kHalf, false, false);
-      const uint64_t dk = tc::smem_desc_sw128(smem_addr(sK), 16, 1024);
-      const uint32_t dk_lo = static_cast<uint32_t>(dk), d_hi = static_cast<uint32_t>(dk >> 32);
-      const uint32_t dq_lo = dk_lo + (M::kQ >> 4) - (M::kK >> 4);
-      // lane 0: the K half; 1 + slot + 2 * part: P V of the S tile's last use
-      // (the first passes); 5, 6: the query
-      constexpr uint32_t kK = 1u, kPV = 2u, kQ = 32u;
-      Ring<kHalves> kr;
-      bar += lane == 0 ? kBarKFull : lane <= 4 ? kBarPV + lane - 1 : kBarQFull + (lane == 6);
-      parity = lane >= 1 && lane <= 4;
-      for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
-        const bool two = kWide && pc.n > kTileTokens;
-        const int slots = two ? 2 : 1;
-        const int q0 = kWide && !two ? p_idx & 1 : 0;  // the first slot's query
-        const int tiles = pc.tiles;
-        for (int t = 0; ok && t < tiles; ++t) {
+    int k_skip = 0, v_skip = 0;  // tiles of the other slot to pass over
+    bool ok = get_piece(pc, ring);
+    for (uint32_t p_idx = 0; ok; ++p_idx) {
+      const bool two = kWide && pc.n > kTileTokens;
+      const int tiles = pc.tiles, step = two ? 1 : 2, t_first = two ? 0 : w ^ pc.turn;
+      const int q = two ? w : kWide ? p_idx & 1 : 0;
+      const uint32_t q_need = two ? 3 * kQ : kQ << q;
+      k_skip += t_first;
+      v_skip += t_first;
+      if (t_first >= tiles) {  // one tile, the other slot's
+        // (no wait with a P V due: the other slot's next pieces may depend on it)
+        ok = flush() && poll(q_need);
+        if (ok && leader) mbar_arrive(&bars[kBarQEmpty + q]);
+        ok = ok && poll(kO);
+        used(kO);
+        if (ok && leader) mbar_arrive(&bars[kBarODone + w]);
+      } else {
+        const uint32_t a0 = dq_lo + q * (kQBytes / 16);
+        int t = t_first;
+        while (true) {
 #pragma unroll 1
           for (int part = 0; part < kParts; ++part) {
-#pragma unroll 1
-            for (int i = 0; i < slots; ++i) {
-              const int w = two ? i : t & 1;
-              const int tile = w + 2 * part;
-              uint32_t need = kPV << tile;
-              if (i == 0) need |= kK;
-              if (t == 0 && part == 0) need |= kQ << (q0 + i);
-              ok = poll(need);
-              if (!ok) break;
-              used(kPV << tile);
-              const uint32_t a0 = dq_lo + (q0 + i) * (kQBytes / 16);
-              const uint32_t b0 = dk_lo + kr.s * (kHalfBytes / 16);
-              const uint32_t d = tmem + w * 128 + part * kHalf;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                if (leader)
-                  tc::mma_f16_ss(d, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, d_hi,
-                                 b0 + (kk >> 2) * (kBlk / 16) + (kk & 3) * 2, d_hi, kIdesc, kk > 0);
-              if (leader) tc::mma_commit(&bars[kBarSFull + tile]);
-            }
-            // (a half that did not arrive is not to be filled again: its barrier's
-            // phase is still open)
+            if (have) ok = out(part);
             if (!ok) break;
-            if (leader) tc::mma_commit(&bars[kBarKEmpty + kr.s]);
-            kr.next();
-            ready &= ~kK;
-            if (lane == 0) {
-              bar = &bars[kBarKFull + kr.s];
-              parity = kr.phase;
+            for (; k_skip > 0; --k_skip) {
+              next_k();
+              next_k();
             }
+            ok = poll(t == t_first ? kK | q_need : kK);
+            if (!ok) break;
+            const uint32_t b0 = dk_lo + kr.s * (kHalfBytes / 16), d = tS + part * kHalf;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              if (leader)
+                tc::mma_f16_ss(d, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, dk_hi,
+                               b0 + (kk >> 2) * (kBlk / 16) + (kk & 3) * 2, dk_hi, kIdescS, kk > 0);
+            if (leader) {
+              tc::mma_commit(&bars[kBarSFull + w + 2 * part]);
+              tc::mma_commit(&bars[kBarKEmpty + kr.s]);
+              if (!two) mbar_arrive(&bars[kBarKEmpty + kr.s]);  // (the other slot does not read it)
+            }
+            next_k();
           }
+          if (!ok) break;
+          have = true;
+          o_two = two;
+          o_first = t == t_first;
+          o_skip = v_skip;
+          v_skip = 0;
+          t += step;
+          o_last = t >= tiles;
+          if (!two && t <= tiles) k_skip = v_skip = 1;  // the other slot's tile behind it
+          if (o_last) break;
         }
         if (!ok) break;
-        if (leader) tc::mma_commit(&bars[kBarQEmpty + q0]);
-        if (leader && two) tc::mma_commit(&bars[kBarQEmpty + 1]);
-        used(two ? 3 * kQ : kQ << q0);
-      }
-    } else {
-      constexpr uint32_t kIdesc = tc::idesc_f16_f32(kRows, kHeadDim, false, true);
-      const uint64_t dv = tc::smem_desc_sw128(smem_addr(sV), kBlk, 1024);
-      const uint32_t dv_lo = static_cast<uint32_t>(dv), d_hi = static_cast<uint32_t>(dv >> 32);
-      // lane 0: the V half; 2 + slot + 2 * part: P; 6: the last piece's O tiles have
-      // been read (the first passes)
-      constexpr uint32_t kV = 1u, kP = 4u, kO = 64u;
-      Ring<kHalves> vr;
-      bar += lane < 2 ? kBarVFull : lane < 6 ? kBarPFull + lane - 2 : kBarOEmpty;
-      parity = lane == 6;
-      while (ok && get_piece(pc, ring)) {
-        const bool two = kWide && pc.n > kTileTokens;
-        const int slots = two ? 2 : 1;
-        const int tiles = pc.tiles;
-        for (int t = 0; ok && t < tiles; ++t) {
-#pragma unroll 1
-          for (int part = 0; part < kParts; ++part) {
-#pragma unroll 1
-            for (int i = 0; i < slots; ++i) {
-              const int w = two ? i : t & 1;
-              const int tile = w + 2 * part;
-              uint32_t need = kP << tile;
-              if (i == 0) need |= kV;
-              if (t == 0 && part == 0) need |= kO;
-              ok = poll(need);
-              if (!ok) break;
-              used(kP << tile);
-              const bool more_o = (two ? t : t >> 1) + part > 0;  // O is added to
-              const uint32_t p0 = tmem + w * 128 + part * kHalf;
-              const uint32_t b0 = dv_lo + vr.s * (kHalfBytes / 16);
-#pragma unroll
-              for (int kk = 0; kk < kHalf / 16; ++kk)
-                if (leader)
-                  tc::mma_f16_ts(tmem + 256 + w * 128, p0 + kk * 8, b0 + kk * 128, d_hi, kIdesc,
-                                 more_o || kk > 0);
-              if (leader && i + 1 == slots) tc::mma_commit(&bars[kBarVEmpty + vr.s]);
-              if (leader) tc::mma_commit(&bars[kBarPV + tile]);
-              // the slot's last of the piece
-              if (leader && part == kParts - 1 && t + (two ? 1 : 2) >= tiles)
-                tc::mma_commit(&bars[kBarODone + w]);
-            }
-            if (!ok) break;
-            vr.next();
-            ready &= ~kV;
-            if (lane < 2) {
-              bar = &bars[kBarVFull + vr.s];
-              parity = vr.phase;
-            }
-          }
+        if (leader) {  // the queries have been read
+          tc::mma_commit(&bars[kBarQEmpty + (two ? 0 : q)]);
+          if (two) tc::mma_commit(&bars[kBarQEmpty + 1]);
         }
-        used(kO);
       }
+      used(q_need);
+      ok = ok && get_piece(pc, ring);
     }
+    if (!*abort_flag) flush();
     // every MMA issued has to land before tensor memory is released
-    const int drain = kBarDrain + (warp == kOutWarp);
+    const int drain = kBarDrain + w;
     if (leader) tc::mma_commit(&bars[drain]);
     mbar_wait_bounded(&bars[drain], 0);
     __syncwarp();

@@ -159,6 +159,8 @@ struct Piece {
   int32_t whole;   // all of the segment
   int32_t slot;    // workspace slot of a cut piece
   int32_t tiles;   // t1 - t0, 0: the end of the CTA's pieces
+  int32_t turn;    // of one row tile: the slot of the first KV tile, such that the
+                   // slots take turns over all such tiles of the CTA
 };
 
 // Walks the pieces of a range in order.  Of a cut segment that begins in the CTA
@@ -166,7 +168,7 @@ struct Piece {
 struct Walker {
   Sequence s;
   Piece p;
-  int group, nt, shift;
+  int group, nt, shift, turn;
   int64_t start;  // of the segment, in units
 
   __device__ __forceinline__ void set_group(const Args &a, int k) {
@@ -180,6 +182,7 @@ struct Walker {
   }
   __device__ __forceinline__ void init(const Args &a, const Range &r) {
     bool bad;
+    turn = 0;
     p.b = r.b;
     s.load(a, r.b, bad);  // it holds the range's first unit, so it has tiles
     const int64_t head = s.units(a.causal);
@@ -212,6 +215,8 @@ struct Walker {
           a.cut[r.cta] = make_int4(
               p.q0, p.n, p.g,
               static_cast<int>(divide(start + (static_cast<int64_t>(nt - 1) << shift), r.width)));
+        p.turn = turn;
+        if (shift == 0) turn ^= p.tiles & 1;
         out = p;
         found = true;
       }
