@@ -164,6 +164,19 @@ __device__ __forceinline__ int page_id(const Args &a, const Piece &p, int t, int
   return pid >= 0 && pid < a.num_pages ? pid : -1;
 }
 
+// mbar_test_wait of a shared address.
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // A 4-byte asynchronous copy, and this thread's arrival when its copies so far are
 // there (the barrier's count includes it).
 __device__ __forceinline__ void copy4(void *dst, const void *src) {
@@ -601,40 +614,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       ring.next();
     }
     pdl_launch_dependents();
-  } else if (warp == 8 || warp == 10) {
-    // ================= keys to fp16 =================
-    const Lanes at(warp == 10, lane);
-    Piece pc;
-    Ring<kPieceRing> ring;
-    Ring<M::kStages> src;
-    Ring<kHalves> dst;
-    bool ok = true;
-    while (ok && get_piece(pc, ring)) {
-      for (int t = pc.t0; ok && t < pc.t1; ++t) {
-        ok = __all_sync(kFull, wait(kBarKstFull + src.s, src.phase));
-        const float *sc = scale_k + src.s * kPagesPerTile;
-#pragma unroll 1
-        for (int h = 0; ok && h < 2; ++h) {
-          if (dst.wrapped) ok = __all_sync(kFull, wait(kBarKEmpty + dst.s, dst.phase ^ 1));
-          if (!ok) break;
-          uint8_t *half = sK + dst.s * kHalfBytes;
-          // (what lies behind the last position, or in a rejected page, is masked as
-          // scores)
-          const uint8_t *from = sKst + src.s * kStage + h * (kStage / 2) + at.from;
-          widen_half(half, from, at, sc + h * 4);
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kBarKFull + dst.s]);
-          dst.next();
-        }
-        if (!ok) break;
-        if (lane == 0) mbar_arrive(&bars[kBarKstEmpty + src.s]);
-        src.next();
-      }
-    }
-  } else if (warp == 11 || warp == 14) {
-    // ================= values to fp16 =================
-    const Lanes at(warp == 14, lane);
+  } else if (warp == 8 || warp == 10 || warp == 11 || warp == 14) {
+    // ================= codes to fp16: two warps for keys, two for values =================
+    // (one code for both: the instruction cache holds little more than the roles' loops)
+    const bool is_v = warp & 1 || warp == 14;
+    const Lanes at(warp == 10 || warp == 14, lane);
+    const int bar_staged = is_v ? kBarVstFull : kBarKstFull, bar_read = is_v ? kBarVstEmpty : kBarKstEmpty;
+    const int bar_full = is_v ? kBarVFull : kBarKFull, bar_empty = is_v ? kBarVEmpty : kBarKEmpty;
+    const uint8_t *stages = is_v ? sVst : sKst;
+    uint8_t *halves = is_v ? sV : sK;
+    const float *scales = is_v ? scale_v : scale_k;
     Piece pc;
     Ring<kPieceRing> ring;
     Ring<M::kStages> src;
@@ -642,18 +631,19 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     bool ok = true;
     for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
       for (int t = pc.t0; ok && t < pc.t1; ++t) {
-        ok = __all_sync(kFull, wait(kBarVstFull + src.s, src.phase));
+        ok = __all_sync(kFull, wait(bar_staged + src.s, src.phase));
         const int live = pc.L - t * kKv;       // positions of the tile that are seen
         const int fresh = pc.base - t * kKv;   // those from here on are new tokens
-        const uint32_t bad = info_v[src.s];
-        const float *sc = scale_v + src.s * kPagesPerTile;
+        const uint32_t bad = is_v ? info_v[src.s] : 0;
+        const float *sc = scales + src.s * kPagesPerTile;
 #pragma unroll 1
         for (int h = 0; ok && h < 2; ++h) {
-          if (dst.wrapped) ok = __all_sync(kFull, wait(kBarVEmpty + dst.s, dst.phase ^ 1));
+          if (dst.wrapped) ok = __all_sync(kFull, wait(bar_empty + dst.s, dst.phase ^ 1));
           if (!ok) break;
-          uint8_t *half = sV + dst.s * kHalfBytes;
-          const uint8_t *from = sVst + src.s * kStage + h * (kStage / 2) + at.from;
-          if (fresh >= (h + 1) * kHalf && !bad) {  // seen by every row
+          uint8_t *half = halves + dst.s * kHalfBytes;
+          const uint8_t *from = stages + src.s * kStage + h * (kStage / 2) + at.from;
+          // (keys that are not seen are masked as scores, whatever is stored there)
+          if (!is_v || (fresh >= (h + 1) * kHalf && !bad)) {
             widen_half(half, from, at, sc + h * 4);
           } else {
 #pragma unroll 1
@@ -679,111 +669,94 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           }
           fence_proxy_async();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kBarVFull + dst.s]);
+          if (lane == 0) mbar_arrive(&bars[bar_full + dst.s]);
           dst.next();
         }
         if (!ok) break;
-        if (lane == 0) mbar_arrive(&bars[kBarVstEmpty + src.s]);
+        if (lane == 0) mbar_arrive(&bars[bar_read + src.s]);
         src.next();
       }
     }
-  } else if (warp == kLoadVWarp) {
-    // ================= V loads, and the CTA's pieces =================
-    // Lane 0 also walks the pieces: the first at the start, the next one behind
-    // the copies of a piece's first tile.
+  } else if (warp == kLoadVWarp || warp == kLoadKWarp) {
+    // ================= loads; V's: the CTA's pieces, K's: the queries =================
+    // V's lane 0 walks the pieces: the first at the start, the next one behind the
+    // copies of a piece's first tile.
+    const bool is_v = warp == kLoadVWarp;
+    const int bar_staged = is_v ? kBarVstFull : kBarKstFull, bar_read = is_v ? kBarVstEmpty : kBarKstEmpty;
+    const CUtensorMap *map = is_v ? &tmap_v : &tmap_k;
+    uint8_t *stages = is_v ? sVst : sKst;
+    float *scales = is_v ? scale_v : scale_k;
+    const float *pool_scales = a.kv_scale + is_v;
     Walker walker;
-    Ring<kPieceRing> out;
+    Ring<kPieceRing> described;
     bool more = true;
-    if (lane == 0) walker.init(a, range);
-    auto describe = [&]() {
-      bool done = true;
-      if (lane == 0 && more) {
-        done = !out.wrapped || wait(kBarTaken + out.s, out.phase ^ 1);
-        if (done) {
-          Piece p;
-          more = walker.next(a, range, p);
-          if (!more) p.tiles = 0;  // the end
-          pieces[out.s] = p;
-          nan_rows[2 * out.s] = nan_rows[2 * out.s + 1] = 0;  // (a ring like the pieces')
-          mbar_arrive(&bars[kBarPiece + out.s]);
-          out.next();
-        }
-      }
-      return __all_sync(kFull, done) != 0;
-    };
+    if (is_v && lane == 0) walker.init(a, range);
     Piece pc;
     Ring<kPieceRing> ring;
     Ring<M::kStages> dst;
     uint32_t issued = 0;
-    bool ok = describe();
-    while (ok && get_piece(pc, ring)) {
-      int pid = page_id(a, pc, pc.t0, lane);
-      for (int t = pc.t0; t < pc.t1; ++t) {
-        if (dst.wrapped) ok = __all_sync(kFull, wait(kBarVstEmpty + dst.s, dst.phase ^ 1));
+    Pair uses;  // of the query buffers
+    bool ok = true;
+    uint32_t p_idx = 0;
+    int t = 0, pid = -2;
+    pc.t0 = pc.t1 = 0;
+    bool start = true;  // a description is due (V), at the start and behind a first tile
+    while (true) {
+      if (start) {
+        bool done = true;
+        if (is_v && lane == 0 && more) {
+          done = !described.wrapped || wait(kBarTaken + described.s, described.phase ^ 1);
+          if (done) {
+            Piece p;
+            more = walker.next(a, range, p);
+            if (!more) p.tiles = 0;  // the end
+            pieces[described.s] = p;
+            nan_rows[2 * described.s] = nan_rows[2 * described.s + 1] = 0;  // (a ring like the pieces')
+            mbar_arrive(&bars[kBarPiece + described.s]);
+            described.next();
+          }
+        }
+        start = false;
+        ok = __all_sync(kFull, done);
         if (!ok) break;
-        const uint32_t bad = __ballot_sync(kFull, pid == -1);
-        const uint32_t bytes = __popc(__ballot_sync(kFull, pid >= 0)) * 2048u;
-        if (lane == 0) {
+      }
+      if (t == pc.t1) {
+        if (!get_piece(pc, ring)) break;
+        t = pc.t0;
+        pid = page_id(a, pc, t, lane);
+      }
+      if (dst.wrapped) ok = __all_sync(kFull, wait(bar_read + dst.s, dst.phase ^ 1));
+      if (!ok) break;
+      const uint32_t bad = __ballot_sync(kFull, pid == -1);
+      const uint32_t bytes = __popc(__ballot_sync(kFull, pid >= 0)) * 2048u;
+      const bool withheld = withholds && !is_v && issued == 0;
+      if (lane == 0) {
+        if (is_v) {
           if (bad) flag_error(a.dev_error, K16V8_DEVERR_PAGE);
           info_v[dst.s] = bad;
-          mbar_arrive_expect_tx(&bars[kBarVstFull + dst.s], bytes);
+        } else {
+          info[issued & 7] = bad;
         }
-        __syncwarp();
+        if (!withheld) mbar_arrive_expect_tx(&bars[bar_staged + dst.s], bytes);
+      }
+      __syncwarp();
+      if (!withheld) {
         if (pid >= 0) {
           const int tile = pid * a.hkv + pc.g;
-          tc::tma_load_2d(sVst + dst.s * kStage + lane * 2048, &tmap_v, 0, tile * kPage,
-                          &bars[kBarVstFull + dst.s]);
-          copy4(scale_v + dst.s * kPagesPerTile + lane, a.kv_scale + 2 * static_cast<int64_t>(tile) + 1);
+          tc::tma_load_2d(stages + dst.s * kStage + lane * 2048, map, 0, tile * kPage,
+                          &bars[bar_staged + dst.s]);
+          copy4(scales + dst.s * kPagesPerTile + lane, pool_scales + 2 * static_cast<int64_t>(tile));
         }
-        arrive_behind_copies(&bars[kBarVstFull + dst.s]);
-        if (t + 1 < pc.t1) pid = page_id(a, pc, t + 1, lane);
-        __syncwarp();
-        dst.next();
-        ++issued;
-        if (t == pc.t0) ok = ok && describe();
-        if (!ok) break;
+        arrive_behind_copies(&bars[bar_staged + dst.s]);
       }
-    }
-    // let the copies issued last land before shared memory is released
-    if (lane == 0)
-      for (uint32_t n = M::kStages, i = issued < n ? 0 : issued - n; i < issued; ++i)
-        mbar_wait_bounded(&bars[kBarVstFull + i % n], (i / n) & 1);
-    __syncwarp();
-  } else if (warp == kLoadKWarp) {
-    // ================= Q and K loads =================
-    Piece pc;
-    Ring<kPieceRing> ring;
-    Ring<M::kStages> dst;
-    uint32_t issued = 0;
-    Pair uses;
-    bool ok = true;
-    for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
-      int pid = page_id(a, pc, pc.t0, lane);
-      for (int t = pc.t0; ok && t < pc.t1; ++t) {
-        if (dst.wrapped) ok = __all_sync(kFull, wait(kBarKstEmpty + dst.s, dst.phase ^ 1));
-        if (!ok) break;
-        const uint32_t bad = __ballot_sync(kFull, pid == -1);
-        const uint32_t bytes = __popc(__ballot_sync(kFull, pid >= 0)) * 2048u;
-        const bool withheld = withholds && issued == 0;
-        if (lane == 0) {
-          info[issued & 7] = bad;
-          if (!withheld) mbar_arrive_expect_tx(&bars[kBarKstFull + dst.s], bytes);
-        }
-        __syncwarp();
-        if (!withheld) {
-          if (pid >= 0) {
-            const int tile = pid * a.hkv + pc.g;
-            tc::tma_load_2d(sKst + dst.s * kStage + lane * 2048, &tmap_k, 0, tile * kPage,
-                            &bars[kBarKstFull + dst.s]);
-            copy4(scale_k + dst.s * kPagesPerTile + lane, a.kv_scale + 2 * static_cast<int64_t>(tile));
-          }
-          arrive_behind_copies(&bars[kBarKstFull + dst.s]);
-        }
-        if (t + 1 < pc.t1) pid = page_id(a, pc, t + 1, lane);
-        __syncwarp();
-        dst.next();
-        ++issued;
-        if (t == pc.t0) {  // the query, behind the first tile's copies
+      const bool first = t == pc.t0;
+      if (++t < pc.t1) pid = page_id(a, pc, t, lane);
+      __syncwarp();
+      dst.next();
+      ++issued;
+      if (first) {
+        start = true;
+        if (!is_v) {  // the query, behind the first tile's copies
           const bool two = kWide && pc.n > kTileTokens;
           for (int i = 0; ok && i < (two ? 2 : 1); ++i) {
             const int qs = two ? i : (kWide ? p_idx & 1 : 0);
@@ -798,15 +771,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
                                 &bars[kBarQFull + qs]);
             }
           }
+          if (!ok) break;
+          ++p_idx;
           __syncwarp();
         }
       }
     }
+    // let the copies issued last land before shared memory is released
     if (lane == 0) {
       constexpr uint32_t n = M::kStages;
       for (uint32_t i = issued < n ? 0 : issued - n; i < issued; ++i)
-        if (!(withholds && i == 0))
-          mbar_wait_bounded(&bars[kBarKstFull + i % n], (i / n) & 1);
+        if (!(withholds && !is_v && i == 0))
+          mbar_wait_bounded(&bars[bar_staged + i % n], (i / n) & 1);
       for (int s = 0; s < 2; ++s)
         if (uses[s] > 0) mbar_wait_bounded(&bars[kBarQFull + s], (uses[s] - 1) & 1);
     }
@@ -829,17 +805,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     // lane 0: the K half; 1: the V half; 2, 3: P of either part; 4, 5: the queries;
     // 6: the last piece's O tiles have been read (the first passes)
     constexpr uint32_t kK = 1u, kV = 2u, kP = 4u, kQ = 16u, kO = 64u;
-    uint64_t *bar = bars + (lane == 0   ? kBarKFull
-                            : lane == 1 ? kBarVFull
-                            : lane < 4  ? kBarPFull + w + 2 * (lane - 2)
-                            : lane < 6  ? kBarQFull + lane - 4
-                                        : kBarOEmpty);
+    const uint32_t bar0 = smem_addr(bars);
+    uint32_t bar = bar0 + 8 * (lane == 0   ? kBarKFull
+                               : lane == 1 ? kBarVFull
+                               : lane < 4  ? kBarPFull + w + 2 * (lane - 2)
+                               : lane < 6  ? kBarQFull + lane - 4
+                                           : kBarOEmpty);
     uint32_t parity = lane == 6;
     uint32_t ready = 0;  // lanes whose barrier is known to be there
+    const uint32_t limit = withholds ? kTestSpins : kMaxSpins;
     auto poll = [&](uint32_t need) {
       for (uint32_t i = 0; (ready & need) != need; ++i) {
-        ready = __ballot_sync(kFull, mbar_test_wait(bar, parity));
-        const uint32_t limit = withholds ? kTestSpins : kMaxSpins;
+        ready = __ballot_sync(kFull, test_wait(bar, parity));
         if ((i & 255u) == 255u && (i >= limit || *abort_flag)) {
           if (!*abort_flag) flag_error(a.dev_error, K16V8_DEVERR_TIMEOUT);
           *abort_flag = 1;
@@ -853,22 +830,25 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       parity ^= lanes >> lane & 1u;
       ready &= ~lanes;
     };
-    Ring<kHalves> kr, vr;
+    // the half tiles to come, and on to the one behind
+    int k_at = 0, v_at = 0;
     auto next_k = [&]() {
-      kr.next();
-      ready &= ~kK;
+      const bool wrap = k_at == kHalves - 1;
+      k_at = wrap ? 0 : k_at + 1;
       if (lane == 0) {
-        bar = &bars[kBarKFull + kr.s];
-        parity = kr.phase;
+        bar = wrap ? bar - 8 * (kHalves - 1) : bar + 8;
+        parity ^= wrap;
       }
+      ready &= ~kK;
     };
     auto next_v = [&]() {
-      vr.next();
-      ready &= ~kV;
+      const bool wrap = v_at == kHalves - 1;
+      v_at = wrap ? 0 : v_at + 1;
       if (lane == 1) {
-        bar = &bars[kBarVFull + vr.s];
-        parity = vr.phase;
+        bar = wrap ? bar - 8 * (kHalves - 1) : bar + 8;
+        parity ^= wrap;
       }
+      ready &= ~kV;
     };
     constexpr uint32_t kIdescS = tc::idesc_f16_f32(kRows, kHalf, false, false);
     constexpr uint32_t kIdescO = tc::idesc_f16_f32(kRows, kHeadDim, false, true);
@@ -879,107 +859,115 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     const uint32_t dq_lo = dk_lo + (M::kQ >> 4) - (M::kK >> 4);
     const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
 
-    // the tile whose S has been issued and whose P V has not
-    bool have = false, o_first = false, o_last = false, o_two = false;
-    int o_skip = 0;  // tiles of the other slot before it
-    auto out = [&](int part) {
-      if (part == 0) {
-        for (; o_skip > 0; --o_skip) {
-          next_v();
-          next_v();
-        }
-        if (o_first) {
-          if (!poll(kO)) return false;
-          used(kO);
-        }
-      }
-      if (!poll(kV | kP << part)) return false;
-      used(kP << part);
-      const uint32_t b0 = dv_lo + vr.s * (kHalfBytes / 16), p0 = tS + part * kHalf;
-      const bool add = !o_first || part > 0;
-#pragma unroll
-      for (int kk = 0; kk < kHalf / 16; ++kk)
-        if (leader) tc::mma_f16_ts(tO, p0 + kk * 8, b0 + kk * 128, dv_hi, kIdescO, add || kk > 0);
-      if (leader) {
-        tc::mma_commit(&bars[kBarPV + w + 2 * part]);
-        tc::mma_commit(&bars[kBarVEmpty + vr.s]);
-        if (!o_two) mbar_arrive(&bars[kBarVEmpty + vr.s]);  // (the other slot does not read it)
-        if (o_last && part == kParts - 1) tc::mma_commit(&bars[kBarODone + w]);
-      }
-      next_v();
-      return true;
-    };
-    auto flush = [&]() {
-      const bool done = !have || (out(0) && out(1));
-      have = false;
-      return done;
-    };
+    // A step is a tile's S and the P V of the slot's tile before it, part by part: at
+    // the start there is no P V, at the end no S, and neither overlaps where the
+    // next piece holds no tile of the slot.
     Piece pc;
     Ring<kPieceRing> ring;
+    uint32_t p_idx = 0;
+    int t = 0, tiles = 0, t_first = 0, q = 0;  // of the piece whose S are issued
+    uint32_t q_need = 0;
+    bool two = false, more = true, pass = false;
     int k_skip = 0, v_skip = 0;  // tiles of the other slot to pass over
-    bool ok = get_piece(pc, ring);
-    for (uint32_t p_idx = 0; ok; ++p_idx) {
-      const bool two = kWide && pc.n > kTileTokens;
-      const int tiles = pc.tiles, step = two ? 1 : 2, t_first = two ? 0 : w ^ pc.turn;
-      const int q = two ? w : kWide ? p_idx & 1 : 0;
-      const uint32_t q_need = two ? 3 * kQ : kQ << q;
-      k_skip += t_first;
-      v_skip += t_first;
-      if (t_first >= tiles) {  // one tile, the other slot's
-        // (no wait with a P V due: the other slot's next pieces may depend on it)
-        ok = flush() && poll(q_need);
-        if (ok && leader) mbar_arrive(&bars[kBarQEmpty + q]);
-        ok = ok && poll(kO);
-        used(kO);
-        if (ok && leader) mbar_arrive(&bars[kBarODone + w]);
-      } else {
-        const uint32_t a0 = dq_lo + q * (kQBytes / 16);
-        int t = t_first;
-        while (true) {
-#pragma unroll 1
-          for (int part = 0; part < kParts; ++part) {
-            if (have) ok = out(part);
-            if (!ok) break;
-            for (; k_skip > 0; --k_skip) {
-              next_k();
-              next_k();
-            }
-            ok = poll(t == t_first ? kK | q_need : kK);
-            if (!ok) break;
-            const uint32_t b0 = dk_lo + kr.s * (kHalfBytes / 16), d = tS + part * kHalf;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              if (leader)
-                tc::mma_f16_ss(d, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, dk_hi,
-                               b0 + (kk >> 2) * (kBlk / 16) + (kk & 3) * 2, dk_hi, kIdescS, kk > 0);
-            if (leader) {
-              tc::mma_commit(&bars[kBarSFull + w + 2 * part]);
-              tc::mma_commit(&bars[kBarKEmpty + kr.s]);
-              if (!two) mbar_arrive(&bars[kBarKEmpty + kr.s]);  // (the other slot does not read it)
-            }
-            next_k();
-          }
-          if (!ok) break;
-          have = true;
-          o_two = two;
-          o_first = t == t_first;
-          o_skip = v_skip;
-          v_skip = 0;
-          t += step;
-          o_last = t >= tiles;
-          if (!two && t <= tiles) k_skip = v_skip = 1;  // the other slot's tile behind it
-          if (o_last) break;
-        }
-        if (!ok) break;
-        if (leader) {  // the queries have been read
-          tc::mma_commit(&bars[kBarQEmpty + (two ? 0 : q)]);
-          if (two) tc::mma_commit(&bars[kBarQEmpty + 1]);
+    bool o_on = false, o_first = false, o_last = false, o_two = false;  // the tile before
+    int o_skip = 0;
+    bool ok = true;
+    while (ok) {
+      bool s_on = t < tiles;
+      if (!s_on && more && !pass) {
+        more = get_piece(pc, ring);
+        if (more) {
+          two = kWide && pc.n > kTileTokens;
+          tiles = pc.tiles;
+          t = t_first = two ? 0 : w ^ pc.turn;
+          q = two ? w : kWide ? p_idx & 1 : 0;
+          q_need = two ? 3 * kQ : kQ << q;
+          ++p_idx;
+          k_skip += t_first;
+          v_skip += t_first;
+          s_on = t < tiles;
+          pass = !s_on;  // one tile, the other slot's
         }
       }
-      used(q_need);
-      ok = ok && get_piece(pc, ring);
+      if (!s_on && !o_on && !pass) break;
+      const uint32_t a0 = dq_lo + q * (kQBytes / 16);
+      for (; o_skip > 0; --o_skip) {
+        next_v();
+        next_v();
+      }
+      for (; k_skip > 0; --k_skip) {
+        next_k();
+        next_k();
+      }
+      const uint32_t o_need = o_on ? kV : 0, o_fresh = o_on && o_first ? kO : 0;
+      const uint32_t s_need = s_on ? (t == t_first ? kK | q_need : kK) : 0;
+#pragma unroll 1
+      for (int part = 0; part < kParts; ++part) {
+        const uint32_t p_need = o_on ? kP << part | (part == 0 ? o_fresh : 0u) : 0u;
+        ok = poll(o_need | s_need | p_need);
+        if (!ok) break;
+        // P V, then S into the columns it has read
+        const uint32_t d = tS + part * kHalf;
+        if (o_on) {
+          const uint32_t b0 = dv_lo + v_at * (kHalfBytes / 16);
+          const bool add = part > 0 || !o_first;  // O is added to
+#pragma unroll
+          for (int kk = 0; kk < kHalf / 16; ++kk)
+            if (leader) tc::mma_f16_ts(tO, d + kk * 8, b0 + kk * 128, dv_hi, kIdescO, add || kk > 0);
+        }
+        if (s_on) {
+          const uint32_t b0 = dk_lo + k_at * (kHalfBytes / 16);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (leader)
+              tc::mma_f16_ss(d, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, dk_hi,
+                             b0 + (kk >> 2) * (kBlk / 16) + (kk & 3) * 2, dk_hi, kIdescS, kk > 0);
+          if (leader) {
+            tc::mma_commit(&bars[kBarSFull + w + 2 * part]);
+            tc::mma_commit(&bars[kBarKEmpty + k_at]);
+            if (!two) mbar_arrive(&bars[kBarKEmpty + k_at]);  // (the other slot does not read it)
+          }
+          next_k();
+        }
+        if (o_on) {
+          if (leader) {
+            tc::mma_commit(&bars[kBarPV + w + 2 * part]);
+            tc::mma_commit(&bars[kBarVEmpty + v_at]);
+            if (!o_two) mbar_arrive(&bars[kBarVEmpty + v_at]);
+            if (o_last && part == kParts - 1) tc::mma_commit(&bars[kBarODone + w]);
+          }
+          used(p_need);
+          next_v();
+        }
+      }
+      if (!ok) break;
+      o_on = s_on;
+      if (s_on) {
+        o_two = two;
+        o_first = t == t_first;
+        o_skip = v_skip;
+        v_skip = 0;
+        t += two ? 1 : 2;
+        o_last = t >= tiles;
+        if (!two && t <= tiles) k_skip = v_skip = 1;  // the other slot's tile behind it
+        if (o_last) {
+          if (leader) {  // the queries have been read
+            tc::mma_commit(&bars[kBarQEmpty + (two ? 0 : q)]);
+            if (two) tc::mma_commit(&bars[kBarQEmpty + 1]);
+          }
+          used(q_need);
+        }
+      } else if (pass) {
+        // (no wait with a P V due: the other slot's next pieces may depend on it)
+        pass = false;
+        tiles = 0;
+        ok = poll(q_need);
+        if (ok && leader) mbar_arrive(&bars[kBarQEmpty + q]);
+        ok = ok && poll(kO);
+        used(q_need | kO);
+        if (ok && leader) mbar_arrive(&bars[kBarODone + w]);
+      }
     }
-    if (!*abort_flag) flush();
     // every MMA issued has to land before tensor memory is released
     const int drain = kBarDrain + w;
     if (leader) tc::mma_commit(&bars[drain]);
