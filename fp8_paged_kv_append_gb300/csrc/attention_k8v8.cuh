@@ -38,21 +38,22 @@ namespace attn8 {
 constexpr unsigned kFull = 0xffffffffu;
 
 constexpr int kRows = kTileTokens * kGroup;  // 128
-constexpr int kPagesPerTile = kKv / kPage;   // 8
+constexpr int kHalf = kKv / 2;               // positions of a half tile
+constexpr int kPagesPerHalf = kHalf / kPage; // 4
 constexpr int kThreads = 512;
 constexpr int kMmaWarp0 = 9, kMmaWarp1 = 15, kLoadVWarp = 12, kLoadKWarp = 13;
 constexpr int kWidenWarps = 2;               // for keys, and for values
 constexpr int kPieceRing = 4;
 constexpr int kPieceReaders = 16;            // every warp
-constexpr int kHalves = 3;                   // half tiles of fp16 keys, and of values
-constexpr int kParts = 2;                    // of a unit
-constexpr int kChunks = 2;                   // of 32 columns in a part
+constexpr int kKTiles = 2;                   // fp16 tiles of keys
+constexpr int kVHalves = 3;                  // fp16 half tiles of values
 
 constexpr uint32_t kQBytes = kRows * 256;
-constexpr uint32_t kStage = kKv * 128;       // [128 pos][128] codes
-constexpr int kHalf = kKv / 2;               // positions of a half tile
-constexpr uint32_t kBlk = kHalf * 128;       // [64 pos][64 dims] fp16
-constexpr uint32_t kHalfBytes = 2 * kBlk;
+constexpr uint32_t kStage = kHalf * 128;     // [64 pos][128] codes
+constexpr uint32_t kVBlk = kHalf * 128;      // [64 pos][64 dims] fp16
+constexpr uint32_t kVBytes = 2 * kVBlk;
+constexpr uint32_t kKBlk = kKv * 128;        // [128 pos][64 dims] fp16
+constexpr uint32_t kKBytes = 2 * kKBlk;
 constexpr uint32_t kTmemCols = 512;  // S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512)
 
 constexpr uint32_t kBarBytes = 512;
@@ -61,23 +62,23 @@ constexpr uint32_t kBarBytes = 512;
 template <bool kWide>
 struct Smem {
   static constexpr int kQSlots = kWide ? 2 : 1;
-  static constexpr int kStages = kWide ? 2 : 3;  // of codes, keys and values each
+  static constexpr int kStages = kWide ? 3 : 5;  // of codes, keys and values each
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kKst = kQ + kQSlots * kQBytes;
   static constexpr uint32_t kVst = kKst + kStages * kStage;
   static constexpr uint32_t kK = kVst + kStages * kStage;
-  static constexpr uint32_t kV = kK + kHalves * kHalfBytes;
-  static constexpr uint32_t kBar = kV + kHalves * kHalfBytes;
+  static constexpr uint32_t kV = kK + kKTiles * kKBytes;
+  static constexpr uint32_t kBar = kV + kVHalves * kVBytes;
   static constexpr uint32_t kPieces = kBar + kBarBytes;
-  static constexpr uint32_t kInfo = kPieces + kPieceRing * 48;
+  static constexpr uint32_t kInfo = kPieces + kPieceRing * 56;
   static constexpr uint32_t kNan = kInfo + 16 * 4;   // new tokens with NaN value codes
   static constexpr uint32_t kStat = kNan + 4 * 8;    // [slot][max, sum][row]
   static constexpr uint32_t kScale = kStat + 2 * 2 * kRows * 4;  // [keys, values][stage][page]
-  static constexpr uint32_t kBytes = kScale + 2 * 3 * kPagesPerTile * 4;
+  static constexpr uint32_t kBytes = kScale + 2 * kStages * kPagesPerHalf * 4;
   static_assert(kBytes <= 227 * 1024, "one CTA's shared memory");
   static_assert(sizeof(int64_t) * (kMaxBatch + 1) <= kBar, "the scan's scratch");
   static_assert(sizeof(int64_t) * 33 <= kBytes - kStat, "the scan's warp sums");
-  static_assert(sizeof(Piece) <= 48 && kInfo % 8 == 0 && kNan % 8 == 0 && kStat % 16 == 0,
+  static_assert(sizeof(Piece) <= 56 && kInfo % 8 == 0 && kNan % 8 == 0 && kStat % 16 == 0,
                 "alignment");
 };
 
@@ -85,16 +86,15 @@ enum {
   kBarQFull = 0,      // +slot
   kBarQEmpty = 2,     // +slot, 2 arrivals: of either slot's MMAs
   kBarKstFull = 4,    // +stage, 33 arrivals: the bytes' and one per lane for the scales
-  kBarKstEmpty = 7,   // +stage, kWidenWarps arrivals
-  kBarVstFull = 10,   // +stage, as for keys
-  kBarVstEmpty = 13,  // +stage
-  kBarKFull = 16,     // +half, kWidenWarps arrivals
-  kBarKEmpty = 19,    // +half, 2 arrivals: both slots' MMAs have read it
-  kBarVFull = 22,     // +half, kWidenWarps arrivals
-  kBarVEmpty = 25,    // +half, as for keys
-  kBarSFull = 28,     // +slot + 2 * part
-  kBarPFull = 32,     // +slot + 2 * part, 4 arrivals (one per warp)
-  kBarPV = 36,        // +slot + 2 * part: the part's P V is done
+  kBarKstEmpty = 9,   // +stage, kWidenWarps arrivals
+  kBarVstFull = 14,   // +stage, as for keys
+  kBarVstEmpty = 19,  // +stage
+  kBarKFull = 24,     // +tile, kWidenWarps arrivals
+  kBarVFull = 26,     // +half, kWidenWarps arrivals
+  kBarKEmpty = 29,    // +tile, 2 arrivals: both slots' MMAs have read it
+  kBarVEmpty = 31,    // +half, as for keys
+  kBarSFull = 34,     // +slot
+  kBarPFull = 36,     // +slot + 2 * part, 4 arrivals (one per warp)
   kBarODone = 40,     // +slot: the slot's last P V of a piece (or it has none)
   kBarOEmpty = 42,    // 8 arrivals: both O tiles have been read
   kBarJoin = 43,      // 8 arrivals (one per warp): both slots' statistics are in shared memory
@@ -119,12 +119,11 @@ struct Pair {
 };
 
 // Position in a ring of n stages: the stage, and the parity of its phase.
-template <int n>
 struct Ring {
   int s = 0;
   uint32_t phase = 0;
   bool wrapped = false;  // every stage has been used once
-  __device__ __forceinline__ void next() {
+  __device__ __forceinline__ void next(int n) {
     if (++s == n) {
       s = 0;
       phase ^= 1;
@@ -155,11 +154,11 @@ __device__ __forceinline__ uint64_t visible(int rel, uint64_t m) {
   return m >> rel;
 }
 
-// Page id of page `lane` of a piece's tile t: -1 outside the pool, -2 behind
-// the last position (and for lanes without a page).
-__device__ __forceinline__ int page_id(const Args &a, const Piece &p, int t, int lane) {
-  const int page = t * kPagesPerTile + lane;
-  if (lane >= kPagesPerTile || page * kPage >= p.L) return -2;
+// Page id of page `lane` of half tile h: -1 outside the pool, -2 behind the last
+// position (and for lanes without a page).
+__device__ __forceinline__ int page_id(const Args &a, const Piece &p, int h, int lane) {
+  const int page = h * kPagesPerHalf + lane;
+  if (lane >= kPagesPerHalf || page * kPage >= p.L) return -2;
   const int pid = __ldg(a.block_table + static_cast<int64_t>(p.b) * a.maxp + page);
   return pid >= 0 && pid < a.num_pages ? pid : -1;
 }
@@ -208,10 +207,10 @@ __device__ __forceinline__ void widen16(const uint4 &raw, __half2 scale, uint4 &
 // side, and every step of eight positions is a constant further.
 struct Lanes {
   uint32_t from, to0, to1;
-  __device__ __forceinline__ Lanes(int rank, int lane) {
+  __device__ __forceinline__ Lanes(int rank, int lane, uint32_t blk) {
     const uint32_t row = lane & 7, c = rank * 4 + (lane >> 3);  // dims 16c .. 16c + 15
     from = row * 128 + ((c ^ row) << 4);
-    const uint32_t to = (c >> 2) * kBlk + row * 128, pair = (c & 3) * 2;
+    const uint32_t to = (c >> 2) * blk + row * 128, pair = (c & 3) * 2;
     to0 = to + ((pair ^ row) << 4);
     to1 = to + (((pair + 1) ^ row) << 4);
   }
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   uint8_t *sK = smem_raw + M::kK;
   uint8_t *sV = smem_raw + M::kV;
   float *scale_k = reinterpret_cast<float *>(smem_raw + M::kScale);
-  float *scale_v = scale_k + 3 * kPagesPerTile;
+  float *scale_v = scale_k + M::kStages * kPagesPerHalf;
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem_raw + M::kBar);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + kNumBars);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kNumBars) + 1;
@@ -329,13 +328,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     for (int i = 0; i < kNumBars; ++i) {
       uint32_t count = 1;
       if ((i >= kBarKstFull && i < kBarKstEmpty) || (i >= kBarVstFull && i < kBarVstEmpty)) count = 33;
-      if ((i >= kBarKstEmpty && i < kBarVstFull) || (i >= kBarVstEmpty && i < kBarKEmpty) ||
-          (i >= kBarVFull && i < kBarVEmpty))
+      if ((i >= kBarKstEmpty && i < kBarVstFull) || (i >= kBarVstEmpty && i < kBarKEmpty))
         count = kWidenWarps;
-      if (i >= kBarPFull && i < kBarPV) count = 4;
-      if ((i >= kBarQEmpty && i < kBarKstFull) || (i >= kBarKEmpty && i < kBarVFull) ||
-          (i >= kBarVEmpty && i < kBarSFull))
-        count = 2;
+      if (i >= kBarPFull && i < kBarODone) count = 4;
+      if ((i >= kBarQEmpty && i < kBarKstFull) || (i >= kBarKEmpty && i < kBarSFull)) count = 2;
       if (i == kBarJoin) count = 8;
       if (i == kBarOEmpty) count = 8;
       if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
@@ -361,12 +357,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     return cta_wait(&bars[bar], parity, abort_flag, a.dev_error);
   };
   // The next piece, for a whole warp; false at the end (or after an abort).
-  auto get_piece = [&](Piece &pc, Ring<kPieceRing> &r) {
+  auto get_piece = [&](Piece &pc, Ring &r) {
     if (!__all_sync(kFull, wait(kBarPiece + r.s, r.phase))) return false;
     pc = pieces[r.s];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars[kBarTaken + r.s]);
-    r.next();
+    r.next(kPieceRing);
     return pc.tiles > 0;
   };
 
@@ -380,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     const uint32_t tS = tmem + w * 128;
     const uint32_t tO = tmem + 256 + w * 128;
     const uint32_t tOther = tmem + 256 + (w ^ 1) * 128;
-    Ring<kPieceRing> ring;
+    Ring ring;
     uint32_t units = 0;             // of this slot so far
     uint32_t tiles = 0;             // of the CTA so far
     uint32_t joins = 0;             // pieces with one row tile, so far
@@ -401,112 +397,117 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       const int n_tiles = pc.tiles, d0 = pc.base - pc.t0 * kKv;
       const int theirs = two ? 0 : (pc.tiles + after) / 2;  // units of the other slot to join
       float m_used = -INFINITY, l = 0.f;
-      for (int k = 0; ok && k < mine; ++k, ++units) {
-#pragma unroll 1
-        for (int part = 0; part < kParts; ++part) {
-          if (!__all_sync(kFull, wait(kBarSFull + w + 2 * part, units & 1))) {
-            ok = false;
-            break;
+      for (int k = 0; k < mine; ++k, ++units) {
+        ok = __all_sync(kFull, wait(kBarSFull + w, units & 1));
+        if (!ok) break;
+        const int tile = two ? k : 2 * k + after;
+        const int parts = pc.halves(tile);
+        if (!warp_live) {
+          if (lane == 0) {
+            mbar_arrive(&bars[kBarPFull + w]);
+            if (parts > 1) mbar_arrive(&bars[kBarPFull + w + 2]);
           }
-          if (!warp_live) {
-            if (lane == 0) mbar_arrive(&bars[kBarPFull + w + 2 * part]);
-            continue;
-          }
-          tc::fence_after_sync();
-          const int tile = two ? k : 2 * k + after;
-          const int d = d0 - tile * kKv;  // prefix columns of this tile
-          const uint32_t bad = info[(tiles + tile) & 7];
-          const uint32_t tSp = tS + lane_base + part * kChunks * 32;
-          // pass 1: row max
-          float rmax = -INFINITY;
-          bool need_mask = d < (part + 1) * kHalf;
-          if (!need_mask) {
+          continue;
+        }
+        tc::fence_after_sync();
+        const int d = d0 - tile * kKv;  // columns of this tile that every row sees
+        const uint32_t bad = info[(tiles + tile) & 7];
+        const uint32_t tSp = tS + lane_base;
+        // pass 1: row max
+        float rmax = -INFINITY;
+        bool need_mask = d < kKv;
+        if (!need_mask) {
 #pragma unroll 1
-            for (int c = kChunks - 2; c >= 0; c -= 2) {
-              uint32_t s0[32], s1[32];
-              float m0, m1;
-              tc::tmem_ld32_max(tSp + c * 32 + 32, s1, m1);
-              tc::tmem_ld32_max(tSp + c * 32, s0, m0);
-              tc::tmem_wait_ld();
-              keep(s1);
-              keep(s0);
-              rmax = fmaxf(rmax, fmaxf(m0, m1));
-            }
-            need_mask = (bad >> 4 * part & 15u) != 0;  // (seldom; its load took place meanwhile)
+          for (int c = 0; c < 4; c += 2) {
+            uint32_t s0[32], s1[32];
+            float m0, m1;
+            tc::tmem_ld32_max(tSp + c * 32, s0, m0);
+            tc::tmem_ld32_max(tSp + c * 32 + 32, s1, m1);
+            tc::tmem_wait_ld();
+            keep(s0);
+            keep(s1);
+            rmax = fmaxf(rmax, fmaxf(m0, m1));
           }
-          uint64_t seen = 0;
-          if (need_mask) {
-            seen = visible(part * kHalf - d, mask_word);
-            for (uint32_t pages = bad >> 4 * part & 15u; pages; pages &= pages - 1)
-              seen &= ~(0xffffull << (__ffs(static_cast<int>(pages)) - 1) * 16);
-            rmax = -INFINITY;
+          need_mask = bad != 0;  // (seldom; its load took place meanwhile)
+        }
+        uint64_t seen_lo = 0, seen_hi = 0;
+        if (need_mask) {
+          seen_lo = visible(-d, mask_word);
+          seen_hi = visible(kHalf - d, mask_word);
+          for (uint32_t pages = bad; pages; pages &= pages - 1) {
+            const int page = __ffs(static_cast<int>(pages)) - 1;
+            const uint64_t out = 0xffffull << (page & 3) * 16;
+            if (page < 4)
+              seen_lo &= ~out;
+            else
+              seen_hi &= ~out;
+          }
+          rmax = -INFINITY;
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-              uint32_t s0[32];
-              tc::tmem_ld32(tSp + c * 32, s0);
-              tc::tmem_wait_ld();
-              const uint32_t v = static_cast<uint32_t>(seen >> c * 32);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s0[32];
+            tc::tmem_ld32(tSp + c * 32, s0);
+            tc::tmem_wait_ld();
+            const uint32_t v = static_cast<uint32_t>((c & 2 ? seen_hi : seen_lo) >> (c & 1) * 32);
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (v >> e & 1) rmax = fmaxf(rmax, __uint_as_float(s0[e]));
-            }
+            for (int e = 0; e < 32; ++e)
+              if (v >> e & 1) rmax = fmaxf(rmax, __uint_as_float(s0[e]));
           }
-          rmax *= qk_scale;
-          float alpha = 1.f;
-          if (rmax > m_used + (kLift + kSlack)) {
-            alpha = ex2(m_used - (rmax - kLift));
-            m_used = rmax - kLift;
-          }
-          if (k + part > 0 && __any_sync(kFull, alpha != 1.f)) {
-            // S of this part was issued after the P V of the part kParts before it;
-            // any in between have to be done as well
-            if (!__all_sync(kFull, wait(kBarPV + w + 2 * (part ^ 1), (units + part + 1) & 1))) {
-              ok = false;
-              break;
-            }
-            tc::fence_after_sync();
+        }
+        rmax *= qk_scale;
+        float alpha = 1.f;
+        if (rmax > m_used + (kLift + kSlack)) {
+          alpha = ex2(m_used - (rmax - kLift));
+          m_used = rmax - kLift;
+        }
+        // (S was issued behind the slot's P V so far: O is at rest)
+        if (k > 0 && __any_sync(kFull, alpha != 1.f)) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tc::tmem_ld32(tO + lane_base + c * 32, o);
-              tc::tmem_wait_ld();
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tc::tmem_ld32(tO + lane_base + c * 32, o);
+            tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc::tmem_st32(tO + lane_base + c * 32, o);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st32(tO + lane_base + c * 32, o);
           }
-          // pass 2: p = 2^(s * scale - m), fp32 row sum, P (fp16) over the S columns read
-          const float neg = m_used == -INFINITY ? 0.f : -m_used;
-          const float2 sc2 = make_float2(qk_scale, qk_scale);
-          const float2 nm2 = make_float2(neg, neg);
-          float2 ps2 = make_float2(0.f, 0.f);
+        }
+        // pass 2: p = 2^(s * scale - m), fp32 row sum, P (fp16) over the S columns read
+        const float neg = m_used == -INFINITY ? 0.f : -m_used;
+        const float2 sc2 = make_float2(qk_scale, qk_scale);
+        const float2 nm2 = make_float2(neg, neg);
+        float2 ps2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int part = 0; part < parts; ++part) {
+          const uint32_t at = tSp + part * kHalf;
           uint32_t s0[16], s1[16];
           if (!need_mask) {  // 16 columns are on their way while 16 are worked on
-            tc::tmem_ld16(tSp, s0);
+            tc::tmem_ld16(at, s0);
             tc::tmem_wait_ld();
 #pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-              tc::tmem_ld16(tSp + c * 32 + 16, s1);
-              exp_chunk<false>(tSp + c * 16, s0, 0, sc2, nm2, ps2);
+            for (int c = 0; c < 2; ++c) {
+              tc::tmem_ld16(at + c * 32 + 16, s1);
+              exp_chunk<false>(at + c * 16, s0, 0, sc2, nm2, ps2);
               tc::tmem_wait_ld();
-              tc::tmem_ld16(tSp + ((c + 1) & (kChunks - 1)) * 32, s0);  // (the last is unused)
-              exp_chunk<false>(tSp + c * 16 + 8, s1, 0, sc2, nm2, ps2);
+              tc::tmem_ld16(at + ((c + 1) & 1) * 32, s0);  // (the last is unused)
+              exp_chunk<false>(at + c * 16 + 8, s1, 0, sc2, nm2, ps2);
               tc::tmem_wait_ld();
             }
           } else {
+            const uint64_t seen = part ? seen_hi : seen_lo;
 #pragma unroll 1
-            for (int c = 0; c < 2 * kChunks; ++c) {
-              tc::tmem_ld16(tSp + c * 16, s0);
+            for (int c = 0; c < 4; ++c) {
+              tc::tmem_ld16(at + c * 16, s0);
               tc::tmem_wait_ld();
-              exp_chunk<true>(tSp + c * 8, s0, static_cast<uint32_t>(seen >> c * 16), sc2, nm2, ps2);
+              exp_chunk<true>(at + c * 8, s0, static_cast<uint32_t>(seen >> c * 16), sc2, nm2, ps2);
             }
           }
           tc::tmem_wait_st();
-          l = l * alpha + (ps2.x + ps2.y);
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarPFull + w + 2 * part]);
         }
+        l = l * alpha + (ps2.x + ps2.y);
       }
       if (!ok) break;
       tiles += n_tiles;
@@ -611,70 +612,71 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         mbar_arrive(&bars[kBarOEmpty]);  // O is read: the next piece may write it
         mbar_arrive(&bars[kBarTaken + ring.s]);
       }
-      ring.next();
+      ring.next(kPieceRing);
     }
     pdl_launch_dependents();
   } else if (warp == 8 || warp == 10 || warp == 11 || warp == 14) {
     // ================= codes to fp16: two warps for keys, two for values =================
     // (one code for both: the instruction cache holds little more than the roles' loops)
     const bool is_v = warp & 1 || warp == 14;
-    const Lanes at(warp == 10 || warp == 14, lane);
+    const Lanes at(warp == 10 || warp == 14, lane, is_v ? kVBlk : kKBlk);
     const int bar_staged = is_v ? kBarVstFull : kBarKstFull, bar_read = is_v ? kBarVstEmpty : kBarKstEmpty;
     const int bar_full = is_v ? kBarVFull : kBarKFull, bar_empty = is_v ? kBarVEmpty : kBarKEmpty;
     const uint8_t *stages = is_v ? sVst : sKst;
-    uint8_t *halves = is_v ? sV : sK;
+    uint8_t *tiles = is_v ? sV : sK;
+    const uint32_t tile_bytes = is_v ? kVBytes : kKBytes;
     const float *scales = is_v ? scale_v : scale_k;
     Piece pc;
-    Ring<kPieceRing> ring;
-    Ring<M::kStages> src;
-    Ring<kHalves> dst;
+    Ring ring, src, dst;
     bool ok = true;
     for (uint32_t p_idx = 0; ok && get_piece(pc, ring); ++p_idx) {
-      for (int t = pc.t0; ok && t < pc.t1; ++t) {
+#pragma unroll 1
+      for (int h = 2 * pc.t0; h < pc.h1; ++h) {
         ok = __all_sync(kFull, wait(bar_staged + src.s, src.phase));
-        const int live = pc.L - t * kKv;       // positions of the tile that are seen
-        const int fresh = pc.base - t * kKv;   // those from here on are new tokens
+        if (!ok) break;
+        // a tile of keys is filled half by half, values are handed over by halves
+        if ((is_v || !(h & 1)) && dst.wrapped)
+          ok = __all_sync(kFull, wait(bar_empty + dst.s, dst.phase ^ 1));
+        if (!ok) break;
+        const int live = pc.L - h * kHalf;      // positions of the half that are seen
+        const int fresh = pc.base - h * kHalf;  // those from here on are new tokens
         const uint32_t bad = is_v ? info_v[src.s] : 0;
-        const float *sc = scales + src.s * kPagesPerTile;
+        const float *sc = scales + src.s * kPagesPerHalf;
+        uint8_t *half = tiles + dst.s * tile_bytes + (is_v ? 0 : (h & 1) * kVBlk);
+        const uint8_t *from = stages + src.s * kStage + at.from;
+        // (keys that are not seen are masked as scores, whatever is stored there)
+        if (!is_v || (fresh >= kHalf && !bad)) {
+          widen_half(half, from, at, sc);
+        } else {
 #pragma unroll 1
-        for (int h = 0; ok && h < 2; ++h) {
-          if (dst.wrapped) ok = __all_sync(kFull, wait(bar_empty + dst.s, dst.phase ^ 1));
-          if (!ok) break;
-          uint8_t *half = halves + dst.s * kHalfBytes;
-          const uint8_t *from = stages + src.s * kStage + h * (kStage / 2) + at.from;
-          // (keys that are not seen are masked as scores, whatever is stored there)
-          if (!is_v || (fresh >= (h + 1) * kHalf && !bad)) {
-            widen_half(half, from, at, sc + h * 4);
-          } else {
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-              const int pos = h * kHalf + 8 * i + (lane & 7), page = pos >> 4;
-              uint4 raw = make_uint4(0, 0, 0, 0);  // what is not seen may hold anything, NaN too
-              float scale = 0.f;
-              if (pos < live && !(bad >> page & 1)) {
-                raw = *reinterpret_cast<const uint4 *>(from + i * 1024);
-                scale = sc[page];
-                if (pos >= fresh) {  // NaN codes must not reach rows that do not see them
-                  const uint32_t n0 = nan_bytes(raw.x), n1 = nan_bytes(raw.y),
-                                 n2 = nan_bytes(raw.z), n3 = nan_bytes(raw.w);
-                  if (n0 | n1 | n2 | n3) {
-                    raw = make_uint4(raw.x & ~n0, raw.y & ~n1, raw.z & ~n2, raw.w & ~n3);
-                    const int rel = pos - fresh;
-                    atomicOr(&nan_rows[(p_idx & 3) * 2 + (rel >> 5)], 1u << (rel & 31));
-                  }
+          for (int i = 0; i < 8; ++i) {
+            const int pos = 8 * i + (lane & 7), page = pos >> 4;
+            uint4 raw = make_uint4(0, 0, 0, 0);  // what is not seen may hold anything, NaN too
+            float scale = 0.f;
+            if (pos < live && !(bad >> page & 1)) {
+              raw = *reinterpret_cast<const uint4 *>(from + i * 1024);
+              scale = sc[page];
+              if (pos >= fresh) {  // NaN codes must not reach rows that do not see them
+                const uint32_t n0 = nan_bytes(raw.x), n1 = nan_bytes(raw.y),
+                               n2 = nan_bytes(raw.z), n3 = nan_bytes(raw.w);
+                if (n0 | n1 | n2 | n3) {
+                  raw = make_uint4(raw.x & ~n0, raw.y & ~n1, raw.z & ~n2, raw.w & ~n3);
+                  const int rel = pos - fresh;
+                  atomicOr(&nan_rows[(p_idx & 3) * 2 + (rel >> 5)], 1u << (rel & 31));
                 }
               }
-              put16(half, at, i, raw, scale);
             }
+            put16(half, at, i, raw, scale);
           }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[bar_full + dst.s]);
-          dst.next();
         }
-        if (!ok) break;
+        fence_proxy_async();
+        __syncwarp();
         if (lane == 0) mbar_arrive(&bars[bar_read + src.s]);
-        src.next();
+        src.next(M::kStages);
+        if (is_v || (h & 1) || h + 1 == pc.h1) {
+          if (lane == 0) mbar_arrive(&bars[bar_full + dst.s]);
+          dst.next(is_v ? kVHalves : kKTiles);
+        }
       }
     }
   } else if (warp == kLoadVWarp || warp == kLoadKWarp) {
@@ -688,18 +690,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     float *scales = is_v ? scale_v : scale_k;
     const float *pool_scales = a.kv_scale + is_v;
     Walker walker;
-    Ring<kPieceRing> described;
+    Ring ring, dst, described;
     bool more = true;
     if (is_v && lane == 0) walker.init(a, range);
     Piece pc;
-    Ring<kPieceRing> ring;
-    Ring<M::kStages> dst;
     uint32_t issued = 0;
     Pair uses;  // of the query buffers
     bool ok = true;
-    uint32_t p_idx = 0;
-    int t = 0, pid = -2;
-    pc.t0 = pc.t1 = 0;
+    uint32_t p_idx = 0, tiles = 0;
+    int h = 0, pid = -2;
+    pc.t0 = pc.h1 = 0;
     bool start = true;  // a description is due (V), at the start and behind a first tile
     while (true) {
       if (start) {
@@ -713,17 +713,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             pieces[described.s] = p;
             nan_rows[2 * described.s] = nan_rows[2 * described.s + 1] = 0;  // (a ring like the pieces')
             mbar_arrive(&bars[kBarPiece + described.s]);
-            described.next();
+            described.next(kPieceRing);
           }
         }
         start = false;
         ok = __all_sync(kFull, done);
         if (!ok) break;
       }
-      if (t == pc.t1) {
+      if (h == pc.h1) {
         if (!get_piece(pc, ring)) break;
-        t = pc.t0;
-        pid = page_id(a, pc, t, lane);
+        h = 2 * pc.t0;
+        pid = page_id(a, pc, h, lane);
       }
       if (dst.wrapped) ok = __all_sync(kFull, wait(bar_read + dst.s, dst.phase ^ 1));
       if (!ok) break;
@@ -734,8 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         if (is_v) {
           if (bad) flag_error(a.dev_error, K16V8_DEVERR_PAGE);
           info_v[dst.s] = bad;
+        } else if (h & 1) {
+          if (bad) info[tiles & 7] |= bad << kPagesPerHalf;
         } else {
-          info[issued & 7] = bad;
+          info[tiles & 7] = bad;
         }
         if (!withheld) mbar_arrive_expect_tx(&bars[bar_staged + dst.s], bytes);
       }
@@ -745,14 +747,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           const int tile = pid * a.hkv + pc.g;
           tc::tma_load_2d(stages + dst.s * kStage + lane * 2048, map, 0, tile * kPage,
                           &bars[bar_staged + dst.s]);
-          copy4(scales + dst.s * kPagesPerTile + lane, pool_scales + 2 * static_cast<int64_t>(tile));
+          copy4(scales + dst.s * kPagesPerHalf + lane, pool_scales + 2 * static_cast<int64_t>(tile));
         }
         arrive_behind_copies(&bars[bar_staged + dst.s]);
       }
-      const bool first = t == pc.t0;
-      if (++t < pc.t1) pid = page_id(a, pc, t, lane);
+      const bool first = h == 2 * pc.t0;
+      ++h;
+      if (!(h & 1) || h == pc.h1) ++tiles;
+      if (h < pc.h1) pid = page_id(a, pc, h, lane);
       __syncwarp();
-      dst.next();
+      dst.next(M::kStages);
       ++issued;
       if (first) {
         start = true;
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     // slot without a tile of a piece waits and arrives for that piece all the same.
     const int w = warp == kMmaWarp1;
     const bool leader = tc::elect_one();
-    // lane 0: the K half; 1: the V half; 2, 3: P of either part; 4, 5: the queries;
+    // lane 0: the K tile; 1: the V half; 2, 3: P of either part; 4, 5: the queries;
     // 6: the last piece's O tiles have been read (the first passes)
     constexpr uint32_t kK = 1u, kV = 2u, kP = 4u, kQ = 16u, kO = 64u;
     const uint32_t bar0 = smem_addr(bars);
@@ -830,47 +834,47 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       parity ^= lanes >> lane & 1u;
       ready &= ~lanes;
     };
-    // the half tiles to come, and on to the one behind
+    // the tile of keys and the half of values to come, and on to the one behind
     int k_at = 0, v_at = 0;
     auto next_k = [&]() {
-      const bool wrap = k_at == kHalves - 1;
-      k_at = wrap ? 0 : k_at + 1;
       if (lane == 0) {
-        bar = wrap ? bar - 8 * (kHalves - 1) : bar + 8;
-        parity ^= wrap;
+        bar = k_at ? bar - 8 : bar + 8;
+        parity ^= k_at;
       }
+      k_at ^= 1;
       ready &= ~kK;
     };
+    static_assert(kKTiles == 2, "next_k");
     auto next_v = [&]() {
-      const bool wrap = v_at == kHalves - 1;
+      const bool wrap = v_at == kVHalves - 1;
       v_at = wrap ? 0 : v_at + 1;
       if (lane == 1) {
-        bar = wrap ? bar - 8 * (kHalves - 1) : bar + 8;
+        bar = wrap ? bar - 8 * (kVHalves - 1) : bar + 8;
         parity ^= wrap;
       }
       ready &= ~kV;
     };
-    constexpr uint32_t kIdescS = tc::idesc_f16_f32(kRows, kHalf, false, false);
+    constexpr uint32_t kIdescS = tc::idesc_f16_f32(kRows, kKv, false, false);
     constexpr uint32_t kIdescO = tc::idesc_f16_f32(kRows, kHeadDim, false, true);
     const uint64_t dk = tc::smem_desc_sw128(smem_addr(sK), 16, 1024);
-    const uint64_t dv = tc::smem_desc_sw128(smem_addr(sV), kBlk, 1024);
+    const uint64_t dv = tc::smem_desc_sw128(smem_addr(sV), kVBlk, 1024);
     const uint32_t dk_lo = static_cast<uint32_t>(dk), dk_hi = static_cast<uint32_t>(dk >> 32);
     const uint32_t dv_lo = static_cast<uint32_t>(dv), dv_hi = static_cast<uint32_t>(dv >> 32);
     const uint32_t dq_lo = dk_lo + (M::kQ >> 4) - (M::kK >> 4);
     const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
 
-    // A step is a tile's S and the P V of the slot's tile before it, part by part: at
-    // the start there is no P V, at the end no S, and neither overlaps where the
-    // next piece holds no tile of the slot.
+    // A step is the P V of a tile's two parts and the S of the slot's next tile: at
+    // the start there is no P V, at the end no S, and where the next piece holds no
+    // tile of the slot they are apart.
     Piece pc;
-    Ring<kPieceRing> ring;
+    Ring ring;
     uint32_t p_idx = 0;
     int t = 0, tiles = 0, t_first = 0, q = 0;  // of the piece whose S are issued
     uint32_t q_need = 0;
     bool two = false, more = true, pass = false;
-    int k_skip = 0, v_skip = 0;  // tiles of the other slot to pass over
+    int v_skip = 0;       // halves of the other slot that do
     bool o_on = false, o_first = false, o_last = false, o_two = false;  // the tile before
-    int o_skip = 0;
+    int o_skip = 0, o_parts = 0;
     bool ok = true;
     while (ok) {
       bool s_on = t < tiles;
@@ -883,73 +887,75 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           q = two ? w : kWide ? p_idx & 1 : 0;
           q_need = two ? 3 * kQ : kQ << q;
           ++p_idx;
-          k_skip += t_first;
-          v_skip += t_first;
+          if (t_first) {
+            next_k();
+            v_skip += pc.halves(0);
+          }
           s_on = t < tiles;
           pass = !s_on;  // one tile, the other slot's
         }
       }
       if (!s_on && !o_on && !pass) break;
-      const uint32_t a0 = dq_lo + q * (kQBytes / 16);
-      for (; o_skip > 0; --o_skip) {
-        next_v();
-        next_v();
-      }
-      for (; k_skip > 0; --k_skip) {
-        next_k();
-        next_k();
-      }
-      const uint32_t o_need = o_on ? kV : 0, o_fresh = o_on && o_first ? kO : 0;
       const uint32_t s_need = s_on ? (t == t_first ? kK | q_need : kK) : 0;
+      if (o_on) {
+        for (; o_skip > 0; --o_skip) next_v();
 #pragma unroll 1
-      for (int part = 0; part < kParts; ++part) {
-        const uint32_t p_need = o_on ? kP << part | (part == 0 ? o_fresh : 0u) : 0u;
-        ok = poll(o_need | s_need | p_need);
-        if (!ok) break;
-        // P V, then S into the columns it has read
-        const uint32_t d = tS + part * kHalf;
-        if (o_on) {
-          const uint32_t b0 = dv_lo + v_at * (kHalfBytes / 16);
-          const bool add = part > 0 || !o_first;  // O is added to
+        for (int part = 0; part < o_parts; ++part) {
+          const bool end = part + 1 == o_parts;
+          const bool fresh = o_first && part == 0;  // O is written, not added to
+          ok = poll(kV | kP << part | (fresh ? kO : 0u) | (end ? s_need : 0u));
+          if (!ok) break;
+          const uint32_t b0 = dv_lo + v_at * (kVBytes / 16), p0 = tS + part * kHalf;
 #pragma unroll
           for (int kk = 0; kk < kHalf / 16; ++kk)
-            if (leader) tc::mma_f16_ts(tO, d + kk * 8, b0 + kk * 128, dv_hi, kIdescO, add || kk > 0);
-        }
-        if (s_on) {
-          const uint32_t b0 = dk_lo + k_at * (kHalfBytes / 16);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
             if (leader)
-              tc::mma_f16_ss(d, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, dk_hi,
-                             b0 + (kk >> 2) * (kBlk / 16) + (kk & 3) * 2, dk_hi, kIdescS, kk > 0);
-          if (leader) {
-            tc::mma_commit(&bars[kBarSFull + w + 2 * part]);
-            tc::mma_commit(&bars[kBarKEmpty + k_at]);
-            if (!two) mbar_arrive(&bars[kBarKEmpty + k_at]);  // (the other slot does not read it)
-          }
-          next_k();
-        }
-        if (o_on) {
-          if (leader) {
-            tc::mma_commit(&bars[kBarPV + w + 2 * part]);
+              tc::mma_f16_ts(tO, p0 + kk * 8, b0 + kk * 128, dv_hi, kIdescO, !fresh || kk > 0);
+          if (leader && !(end && s_on)) {  // (else behind S)
             tc::mma_commit(&bars[kBarVEmpty + v_at]);
-            if (!o_two) mbar_arrive(&bars[kBarVEmpty + v_at]);
-            if (o_last && part == kParts - 1) tc::mma_commit(&bars[kBarODone + w]);
+            if (!o_two) mbar_arrive(&bars[kBarVEmpty + v_at]);  // (the other slot does not read it)
+            if (end && o_last) tc::mma_commit(&bars[kBarODone + w]);
           }
-          used(p_need);
+          if (end && s_on) break;
+          used(kP << part | (fresh ? kO : 0u));
           next_v();
         }
+      } else if (s_on) {
+        ok = poll(s_need);
       }
       if (!ok) break;
-      o_on = s_on;
       if (s_on) {
+        const uint32_t a0 = dq_lo + q * (kQBytes / 16), b0 = dk_lo + k_at * (kKBytes / 16);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          if (leader)
+            tc::mma_f16_ss(tS, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, dk_hi,
+                           b0 + (kk >> 2) * (kKBlk / 16) + (kk & 3) * 2, dk_hi, kIdescS, kk > 0);
+        if (leader) {
+          tc::mma_commit(&bars[kBarSFull + w]);
+          tc::mma_commit(&bars[kBarKEmpty + k_at]);
+          if (!two) mbar_arrive(&bars[kBarKEmpty + k_at]);
+        }
+        if (o_on) {  // what the last part left to do
+          if (leader) {
+            tc::mma_commit(&bars[kBarVEmpty + v_at]);
+            if (!o_two) mbar_arrive(&bars[kBarVEmpty + v_at]);
+            if (o_last) tc::mma_commit(&bars[kBarODone + w]);
+          }
+          used(kP << (o_parts - 1) | (o_first && o_parts == 1 ? kO : 0u));
+          next_v();
+        }
+        next_k();
         o_two = two;
         o_first = t == t_first;
+        o_parts = pc.halves(t);
         o_skip = v_skip;
         v_skip = 0;
         t += two ? 1 : 2;
         o_last = t >= tiles;
-        if (!two && t <= tiles) k_skip = v_skip = 1;  // the other slot's tile behind it
+        if (!two && t <= tiles) {  // the other slot's tile behind it
+          next_k();
+          v_skip = pc.halves(t - 1);
+        }
         if (o_last) {
           if (leader) {  // the queries have been read
             tc::mma_commit(&bars[kBarQEmpty + (two ? 0 : q)]);
@@ -967,6 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         used(q_need | kO);
         if (ok && leader) mbar_arrive(&bars[kBarODone + w]);
       }
+      o_on = s_on;
     }
     // every MMA issued has to land before tensor memory is released
     const int drain = kBarDrain + w;

@@ -155,12 +155,16 @@ struct Piece {
   int32_t b, g;
   int32_t q0, n;   // the group's first row, its tokens
   int32_t L, base; // positions seen; those below base are seen by every token
-  int32_t t0, t1;
+  int32_t t0, h1;  // the first tile; the end, in half tiles of 64 positions
   int32_t whole;   // all of the segment
   int32_t slot;    // workspace slot of a cut piece
   int32_t tiles;   // t1 - t0, 0: the end of the CTA's pieces
   int32_t turn;    // of one row tile: the slot of the first KV tile, such that the
                    // slots take turns over all such tiles of the CTA
+
+  // Halves of the piece's tile t (from 0 on) that hold positions: one where the last
+  // tile ends in its first half.
+  __device__ __forceinline__ int halves(int t) const { return 2 * (t0 + t) + 1 < h1 ? 2 : 1; }
 };
 
 // Walks the pieces of a range in order.  Of a cut segment that begins in the CTA
@@ -206,12 +210,13 @@ struct Walker {
           p.b = a.batch;
           break;
         }
-        p.t1 = static_cast<int>(
+        const int t1 = static_cast<int>(
             min(static_cast<int64_t>(nt), (r.hi - start + (1 << shift) - 1) >> shift));
-        p.tiles = p.t1 - p.t0;
-        p.whole = p.t0 == 0 && p.t1 == nt;
+        p.tiles = t1 - p.t0;
+        p.h1 = max(2 * t1 - 1, min(2 * t1, (p.L + kKv / 2 - 1) / (kKv / 2)));
+        p.whole = p.t0 == 0 && t1 == nt;
         p.slot = 2 * r.cta + (start >= r.lo ? 1 : 0);
-        if (start >= r.lo && p.t1 < nt)
+        if (start >= r.lo && t1 < nt)
           a.cut[r.cta] = make_int4(
               p.q0, p.n, p.g,
               static_cast<int>(divide(start + (static_cast<int64_t>(nt - 1) << shift), r.width)));
