@@ -54,6 +54,10 @@ constexpr uint32_t kVBlk = kHalf * 128;      // [64 pos][64 dims] fp16
 constexpr uint32_t kVBytes = 2 * kVBlk;
 constexpr uint32_t kKBlk = kKv * 128;        // [128 pos][64 dims] fp16
 constexpr uint32_t kKBytes = 2 * kKBlk;
+// registers, together what the block was launched with
+constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
+static_assert(kSoftmaxRegs + kOtherRegs == 2 * (65536 / kThreads), "two warpgroups each");
+
 constexpr uint32_t kTmemCols = 512;  // S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512)
 
 constexpr uint32_t kBarBytes = 512;
@@ -101,7 +105,8 @@ enum {
   kBarPiece = 44,     // +ring entry: described
   kBarTaken = 48,     // +ring entry: kPieceReaders arrivals
   kBarDrain = 52,     // +slot: every MMA
-  kNumBars = 54
+  kBarTurn = 54,      // +slot, 4 arrivals: the other slot's exponentials of a tile are done
+  kNumBars = 56
 };
 static_assert(kNumBars * 8 + 16 <= kBarBytes, "barriers");
 
@@ -176,6 +181,16 @@ __device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// Registers of a thread of this warpgroup from here on.
+template <int n>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
+}
+
 // A 4-byte asynchronous copy, and this thread's arrival when its copies so far are
 // there (the barrier's count includes it).
 __device__ __forceinline__ void copy4(void *dst, const void *src) {
@@ -248,7 +263,7 @@ __device__ __forceinline__ void keep(const uint32_t (&r)[32]) {
 // moves when it grows by more than 2^8, so they stay below 2^15.
 constexpr float kLift = 7.f, kSlack = 8.f;
 
-// p = 2^(s * scale - m) of 16 scores to tensor memory, their sum in fp32; m is
+// p = 2^(s * scale - m) of n scores to tensor memory, their sum in fp32; m is
 // kLift below a maximum of the row.  P is rounded to fp16, the type of V's
 // tile: an MMA takes both operands in one type, and bf16 would round P eight
 // times as coarsely.  That is 2^-11 of a weight down to 2^-21 of the row's
@@ -257,12 +272,12 @@ constexpr float kLift = 7.f, kSlack = 8.f;
 // most L 2^-32 max|v|.  (Without the lift, L 2^-25: a score 17 above a flat tail
 // of 131,072 positions loses 0.24% of the output; the lift takes no instruction
 // per weight.)
-template <bool kMask>
-__device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[16], uint32_t seen,
+template <bool kMask, int n>
+__device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[n], uint32_t seen,
                                           float2 scale, float2 neg_m, float2 &sum) {
-  uint32_t pk[8];
+  uint32_t pk[n / 2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < n / 2; ++e) {
     const float2 x = __ffma2_rn(
         make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), scale, neg_m);
     float2 p = make_float2(ex2(x.x), ex2(x.y));
@@ -274,7 +289,10 @@ __device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[16],
     const __half2 h = __floats2half2_rn(p.x, p.y);
     pk[e] = *reinterpret_cast<const uint32_t *>(&h);
   }
-  tc::tmem_st8(t_p, pk);
+  if constexpr (n == 32)
+    tc::tmem_st16(t_p, pk);
+  else
+    tc::tmem_st8(t_p, pk);
 }
 
 // kTest: the form of the bounded-wait test hook.  CTA 0 withholds K of its first
@@ -332,6 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         count = kWidenWarps;
       if (i >= kBarPFull && i < kBarODone) count = 4;
       if ((i >= kBarQEmpty && i < kBarKstFull) || (i >= kBarKEmpty && i < kBarSFull)) count = 2;
+      if (i >= kBarTurn) count = 4;
       if (i == kBarJoin) count = 8;
       if (i == kBarOEmpty) count = 8;
       if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
@@ -366,6 +385,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     return pc.tiles > 0;
   };
 
+  if (warp < 8)
+    more_registers<kSoftmaxRegs>();
+  else
+    fewer_registers<kOtherRegs>();
   if (!work) {
   } else if (warp < 8) {
     // ================= softmax of slot w =================
@@ -380,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     uint32_t units = 0;             // of this slot so far
     uint32_t tiles = 0;             // of the CTA so far
     uint32_t joins = 0;             // pieces with one row tile, so far
+    uint32_t turns = 0;             // tiles with two row tiles, so far
     bool ok = true;
     for (uint32_t p_idx = 0; ok; ++p_idx) {
       // the piece stays in shared memory: registers are short here
@@ -406,6 +430,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           if (lane == 0) {
             mbar_arrive(&bars[kBarPFull + w]);
             if (parts > 1) mbar_arrive(&bars[kBarPFull + w + 2]);
+          }
+          if (two) {
+            ok = __all_sync(kFull, wait(kBarTurn + w, (turns++ + 1 - w) & 1));
+            if (!ok) break;
+            if (lane == 0) mbar_arrive(&bars[kBarTurn + (w ^ 1)]);
           }
           continue;
         }
@@ -472,41 +501,52 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             tc::tmem_st32(tO + lane_base + c * 32, o);
           }
         }
+        if (two) {
+          ok = __all_sync(kFull, wait(kBarTurn + w, (turns++ + 1 - w) & 1));
+          if (!ok) break;
+        }
         // pass 2: p = 2^(s * scale - m), fp32 row sum, P (fp16) over the S columns read
         const float neg = m_used == -INFINITY ? 0.f : -m_used;
         const float2 sc2 = make_float2(qk_scale, qk_scale);
         const float2 nm2 = make_float2(neg, neg);
         float2 ps2 = make_float2(0.f, 0.f);
-#pragma unroll 1
-        for (int part = 0; part < parts; ++part) {
-          const uint32_t at = tSp + part * kHalf;
-          uint32_t s0[16], s1[16];
-          if (!need_mask) {  // 16 columns are on their way while 16 are worked on
-            tc::tmem_ld16(at, s0);
-            tc::tmem_wait_ld();
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              tc::tmem_ld16(at + c * 32 + 16, s1);
-              exp_chunk<false>(at + c * 16, s0, 0, sc2, nm2, ps2);
-              tc::tmem_wait_ld();
-              tc::tmem_ld16(at + ((c + 1) & 1) * 32, s0);  // (the last is unused)
-              exp_chunk<false>(at + c * 16 + 8, s1, 0, sc2, nm2, ps2);
-              tc::tmem_wait_ld();
-            }
-          } else {
-            const uint64_t seen = part ? seen_hi : seen_lo;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tc::tmem_ld16(at + c * 16, s0);
-              tc::tmem_wait_ld();
-              exp_chunk<true>(at + c * 8, s0, static_cast<uint32_t>(seen >> c * 16), sc2, nm2, ps2);
-            }
-          }
+        auto hand_over = [&](int part) {
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarPFull + w + 2 * part]);
+        };
+        if (!need_mask) {  // 32 columns are on their way while 32 are worked on
+          uint32_t s0[32], s1[32];
+          tc::tmem_ld32(tSp, s0);
+          tc::tmem_wait_ld();
+#pragma unroll 1
+          for (int part = 0; part < 2; ++part) {
+            const uint32_t at = tSp + part * kHalf;
+            tc::tmem_ld32(at + 32, s1);
+            exp_chunk<false>(at, s0, 0, sc2, nm2, ps2);
+            tc::tmem_wait_ld();
+            tc::tmem_ld32(tSp + kHalf, s0);  // (the second time unused)
+            exp_chunk<false>(at + 16, s1, 0, sc2, nm2, ps2);
+            tc::tmem_wait_ld();
+            hand_over(part);
+          }
+        } else {
+#pragma unroll 1
+          for (int part = 0; part < parts; ++part) {
+            const uint32_t at = tSp + part * kHalf;
+            const uint64_t seen = part ? seen_hi : seen_lo;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s0[16];
+              tc::tmem_ld16(at + c * 16, s0);
+              tc::tmem_wait_ld();
+              exp_chunk<true>(at + c * 8, s0, static_cast<uint32_t>(seen >> c * 16), sc2, nm2, ps2);
+            }
+            hand_over(part);
+          }
         }
+        if (two && lane == 0) mbar_arrive(&bars[kBarTurn + (w ^ 1)]);
         l = l * alpha + (ps2.x + ps2.y);
       }
       if (!ok) break;
@@ -901,27 +941,27 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         for (; o_skip > 0; --o_skip) next_v();
 #pragma unroll 1
         for (int part = 0; part < o_parts; ++part) {
-          const bool end = part + 1 == o_parts;
+          // (the last part's P V goes with S, but for a new piece's, which may be far off)
+          const bool join = part + 1 == o_parts && s_on && t != t_first;
           const bool fresh = o_first && part == 0;  // O is written, not added to
-          ok = poll(kV | kP << part | (fresh ? kO : 0u) | (end ? s_need : 0u));
+          ok = poll(kV | kP << part | (fresh ? kO : 0u) | (join ? s_need : 0u));
           if (!ok) break;
           const uint32_t b0 = dv_lo + v_at * (kVBytes / 16), p0 = tS + part * kHalf;
 #pragma unroll
           for (int kk = 0; kk < kHalf / 16; ++kk)
             if (leader)
               tc::mma_f16_ts(tO, p0 + kk * 8, b0 + kk * 128, dv_hi, kIdescO, !fresh || kk > 0);
-          if (leader && !(end && s_on)) {  // (else behind S)
+          if (leader && !join) {  // (else behind S)
             tc::mma_commit(&bars[kBarVEmpty + v_at]);
             if (!o_two) mbar_arrive(&bars[kBarVEmpty + v_at]);  // (the other slot does not read it)
-            if (end && o_last) tc::mma_commit(&bars[kBarODone + w]);
+            if (part + 1 == o_parts && o_last) tc::mma_commit(&bars[kBarODone + w]);
           }
-          if (end && s_on) break;
+          if (join) break;
           used(kP << part | (fresh ? kO : 0u));
           next_v();
         }
-      } else if (s_on) {
-        ok = poll(s_need);
       }
+      if (ok && s_on && !(o_on && t != t_first)) ok = poll(s_need);
       if (!ok) break;
       if (s_on) {
         const uint32_t a0 = dq_lo + q * (kQBytes / 16), b0 = dk_lo + k_at * (kKBytes / 16);
@@ -935,11 +975,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           tc::mma_commit(&bars[kBarKEmpty + k_at]);
           if (!two) mbar_arrive(&bars[kBarKEmpty + k_at]);
         }
-        if (o_on) {  // what the last part left to do
+        if (o_on && t != t_first) {  // what the last part left to do
           if (leader) {
             tc::mma_commit(&bars[kBarVEmpty + v_at]);
             if (!o_two) mbar_arrive(&bars[kBarVEmpty + v_at]);
-            if (o_last) tc::mma_commit(&bars[kBarODone + w]);
           }
           used(kP << (o_parts - 1) | (o_first && o_parts == 1 ? kO : 0u));
           next_v();
