@@ -137,17 +137,65 @@ struct Ring {
   }
 };
 
-// As in prefill: a wait that runs out raises the CTA-wide abort flag, which
-// the suspending waits poll; every role leaves its loops on a failed wait.
-__device__ __forceinline__ bool cta_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                         int32_t *dev_error) {
-  for (uint32_t i = 0; i < kMaxPolls; ++i) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if ((i & 1023u) == 0 && *abort_flag) return false;
+// Barriers by their shared address: 32 bits, and no conversion at every use.  (The
+// roles' code shares an instruction cache that is short of it: every instruction
+// in here that is spared counts.)
+__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap *map, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(bar)
+      : "memory");
+}
+
+// A wait that runs out raises the CTA-wide abort flag, which the others poll; every
+// role leaves its loops on a failed wait, and the flag becomes
+// K16V8_DEVERR_TIMEOUT at the end of the kernel.
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity,
+                                              volatile int *abort_flag) {
+  for (uint32_t i = 0; !try_wait(bar, parity); ++i) {
+    if (i & 1023u) continue;
+    if (*abort_flag) return false;
+    if (i >= kMaxPolls) {
+      *abort_flag = 1;
+      return false;
+    }
   }
-  *abort_flag = 1;
-  flag_error(dev_error, K16V8_DEVERR_TIMEOUT);
-  return false;
+  return true;
 }
 
 // 64 columns from the one `rel` behind the first new token, for a row that sees the
@@ -168,19 +216,6 @@ __device__ __forceinline__ int page_id(const Args &a, const Piece &p, int h, int
   return pid >= 0 && pid < a.num_pages ? pid : -1;
 }
 
-// mbar_test_wait of a shared address.
-__device__ __forceinline__ bool test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // Registers of a thread of this warpgroup from here on.
 template <int n>
 __device__ __forceinline__ void more_registers() {
@@ -193,13 +228,11 @@ __device__ __forceinline__ void fewer_registers() {
 
 // A 4-byte asynchronous copy, and this thread's arrival when its copies so far are
 // there (the barrier's count includes it).
-__device__ __forceinline__ void copy4(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
-               : "memory");
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void arrive_behind_copies(uint64_t *bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+__device__ __forceinline__ void arrive_behind_copies(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // 16 codes times a scale, as fp16.
@@ -372,15 +405,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
 
+  const uint32_t bar0 = smem_addr(bars);
   auto wait = [&](int bar, uint32_t parity) {
-    return cta_wait(&bars[bar], parity, abort_flag, a.dev_error);
+    return wait_or_abort(bar0 + 8 * bar, parity, abort_flag);
   };
   // The next piece, for a whole warp; false at the end (or after an abort).
   auto get_piece = [&](Piece &pc, Ring &r) {
     if (!__all_sync(kFull, wait(kBarPiece + r.s, r.phase))) return false;
     pc = pieces[r.s];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars[kBarTaken + r.s]);
+    if (lane == 0) arrive(bar0 + 8 * (kBarTaken + r.s));
     r.next(kPieceRing);
     return pc.tiles > 0;
   };
@@ -428,13 +462,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         const int parts = pc.halves(tile);
         if (!warp_live) {
           if (lane == 0) {
-            mbar_arrive(&bars[kBarPFull + w]);
-            if (parts > 1) mbar_arrive(&bars[kBarPFull + w + 2]);
+            arrive(bar0 + 8 * (kBarPFull + w));
+            if (parts > 1) arrive(bar0 + 8 * (kBarPFull + w + 2));
           }
           if (two) {
             ok = __all_sync(kFull, wait(kBarTurn + w, (turns++ + 1 - w) & 1));
             if (!ok) break;
-            if (lane == 0) mbar_arrive(&bars[kBarTurn + (w ^ 1)]);
+            if (lane == 0) arrive(bar0 + 8 * (kBarTurn + (w ^ 1)));
           }
           continue;
         }
@@ -514,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars[kBarPFull + w + 2 * part]);
+          if (lane == 0) arrive(bar0 + 8 * (kBarPFull + w + 2 * part));
         };
         if (!need_mask) {  // 32 columns are on their way while 32 are worked on
           uint32_t s0[32], s1[32];
@@ -546,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             hand_over(part);
           }
         }
-        if (two && lane == 0) mbar_arrive(&bars[kBarTurn + (w ^ 1)]);
+        if (two && lane == 0) arrive(bar0 + 8 * (kBarTurn + (w ^ 1)));
         l = l * alpha + (ps2.x + ps2.y);
       }
       if (!ok) break;
@@ -565,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         stat[(w * 2 + 0) * kRows + r] = m_used;
         stat[(w * 2 + 1) * kRows + r] = l;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarJoin]);
+        if (lane == 0) arrive(bar0 + 8 * (kBarJoin));
         ok = __all_sync(kFull, wait(kBarJoin, joins++ & 1));
         if (!ok) break;
         const float m_o = stat[((w ^ 1) * 2 + 0) * kRows + r];
@@ -649,8 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(&bars[kBarOEmpty]);  // O is read: the next piece may write it
-        mbar_arrive(&bars[kBarTaken + ring.s]);
+        arrive(bar0 + 8 * (kBarOEmpty));  // O is read: the next piece may write it
+        arrive(bar0 + 8 * (kBarTaken + ring.s));
       }
       ring.next(kPieceRing);
     }
@@ -711,10 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         }
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[bar_read + src.s]);
+        if (lane == 0) arrive(bar0 + 8 * (bar_read + src.s));
         src.next(M::kStages);
         if (is_v || (h & 1) || h + 1 == pc.h1) {
-          if (lane == 0) mbar_arrive(&bars[bar_full + dst.s]);
+          if (lane == 0) arrive(bar0 + 8 * (bar_full + dst.s));
           dst.next(is_v ? kVHalves : kKTiles);
         }
       }
@@ -726,8 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     const bool is_v = warp == kLoadVWarp;
     const int bar_staged = is_v ? kBarVstFull : kBarKstFull, bar_read = is_v ? kBarVstEmpty : kBarKstEmpty;
     const CUtensorMap *map = is_v ? &tmap_v : &tmap_k;
-    uint8_t *stages = is_v ? sVst : sKst;
-    float *scales = is_v ? scale_v : scale_k;
+    const uint32_t stages = smem_addr(is_v ? sVst : sKst);
+    const uint32_t scales = smem_addr(is_v ? scale_v : scale_k);
     const float *pool_scales = a.kv_scale + is_v;
     Walker walker;
     Ring ring, dst, described;
@@ -752,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             if (!more) p.tiles = 0;  // the end
             pieces[described.s] = p;
             nan_rows[2 * described.s] = nan_rows[2 * described.s + 1] = 0;  // (a ring like the pieces')
-            mbar_arrive(&bars[kBarPiece + described.s]);
+            arrive(bar0 + 8 * (kBarPiece + described.s));
             described.next(kPieceRing);
           }
         }
@@ -779,17 +813,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         } else {
           info[tiles & 7] = bad;
         }
-        if (!withheld) mbar_arrive_expect_tx(&bars[bar_staged + dst.s], bytes);
+        if (!withheld) arrive_expect(bar0 + 8 * (bar_staged + dst.s), bytes);
       }
       __syncwarp();
       if (!withheld) {
         if (pid >= 0) {
           const int tile = pid * a.hkv + pc.g;
-          tc::tma_load_2d(stages + dst.s * kStage + lane * 2048, map, 0, tile * kPage,
-                          &bars[bar_staged + dst.s]);
-          copy4(scales + dst.s * kPagesPerHalf + lane, pool_scales + 2 * static_cast<int64_t>(tile));
+          load_box(stages + dst.s * kStage + lane * 2048, map, tile * kPage,
+                   bar0 + 8 * (bar_staged + dst.s));
+          copy4(scales + dst.s * (kPagesPerHalf * 4) + lane * 4,
+                pool_scales + 2 * static_cast<int64_t>(tile));
         }
-        arrive_behind_copies(&bars[bar_staged + dst.s]);
+        arrive_behind_copies(bar0 + 8 * (bar_staged + dst.s));
       }
       const bool first = h == 2 * pc.t0;
       ++h;
@@ -808,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             if (!ok) break;
             uses.add(qs);
             if (lane == 0) {
-              mbar_arrive_expect_tx(&bars[kBarQFull + qs], kQBytes);
+              arrive_expect(bar0 + 8 * (kBarQFull + qs), kQBytes);
               for (int h = 0; h < 2; ++h)
                 tc::tma_load_3d(sQ + qs * kQBytes + h * (kQBytes / 2), &tmap_q, 64 * h,
                                 pc.g * kGroup, pc.q0 + (two ? i * kTileTokens : 0),
@@ -849,7 +884,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     // lane 0: the K tile; 1: the V half; 2, 3: P of either part; 4, 5: the queries;
     // 6: the last piece's O tiles have been read (the first passes)
     constexpr uint32_t kK = 1u, kV = 2u, kP = 4u, kQ = 16u, kO = 64u;
-    const uint32_t bar0 = smem_addr(bars);
     uint32_t bar = bar0 + 8 * (lane == 0   ? kBarKFull
                                : lane == 1 ? kBarVFull
                                : lane < 4  ? kBarPFull + w + 2 * (lane - 2)
@@ -862,7 +896,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       for (uint32_t i = 0; (ready & need) != need; ++i) {
         ready = __ballot_sync(kFull, test_wait(bar, parity));
         if ((i & 255u) == 255u && (i >= limit || *abort_flag)) {
-          if (!*abort_flag) flag_error(a.dev_error, K16V8_DEVERR_TIMEOUT);
           *abort_flag = 1;
           return false;
         }
@@ -952,9 +985,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             if (leader)
               tc::mma_f16_ts(tO, p0 + kk * 8, b0 + kk * 128, dv_hi, kIdescO, !fresh || kk > 0);
           if (leader && !join) {  // (else behind S)
-            tc::mma_commit(&bars[kBarVEmpty + v_at]);
-            if (!o_two) mbar_arrive(&bars[kBarVEmpty + v_at]);  // (the other slot does not read it)
-            if (part + 1 == o_parts && o_last) tc::mma_commit(&bars[kBarODone + w]);
+            commit(bar0 + 8 * (kBarVEmpty + v_at));
+            if (!o_two) arrive(bar0 + 8 * (kBarVEmpty + v_at));  // (the other slot does not read it)
+            if (part + 1 == o_parts && o_last) commit(bar0 + 8 * (kBarODone + w));
           }
           if (join) break;
           used(kP << part | (fresh ? kO : 0u));
@@ -971,14 +1004,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             tc::mma_f16_ss(tS, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, dk_hi,
                            b0 + (kk >> 2) * (kKBlk / 16) + (kk & 3) * 2, dk_hi, kIdescS, kk > 0);
         if (leader) {
-          tc::mma_commit(&bars[kBarSFull + w]);
-          tc::mma_commit(&bars[kBarKEmpty + k_at]);
-          if (!two) mbar_arrive(&bars[kBarKEmpty + k_at]);
+          commit(bar0 + 8 * (kBarSFull + w));
+          commit(bar0 + 8 * (kBarKEmpty + k_at));
+          if (!two) arrive(bar0 + 8 * (kBarKEmpty + k_at));
         }
         if (o_on && t != t_first) {  // what the last part left to do
           if (leader) {
-            tc::mma_commit(&bars[kBarVEmpty + v_at]);
-            if (!o_two) mbar_arrive(&bars[kBarVEmpty + v_at]);
+            commit(bar0 + 8 * (kBarVEmpty + v_at));
+            if (!o_two) arrive(bar0 + 8 * (kBarVEmpty + v_at));
           }
           used(kP << (o_parts - 1) | (o_first && o_parts == 1 ? kO : 0u));
           next_v();
@@ -997,8 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         }
         if (o_last) {
           if (leader) {  // the queries have been read
-            tc::mma_commit(&bars[kBarQEmpty + (two ? 0 : q)]);
-            if (two) tc::mma_commit(&bars[kBarQEmpty + 1]);
+            commit(bar0 + 8 * (kBarQEmpty + (two ? 0 : q)));
+            if (two) commit(bar0 + 8 * (kBarQEmpty + 1));
           }
           used(q_need);
         }
@@ -1007,16 +1040,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         pass = false;
         tiles = 0;
         ok = poll(q_need);
-        if (ok && leader) mbar_arrive(&bars[kBarQEmpty + q]);
+        if (ok && leader) arrive(bar0 + 8 * (kBarQEmpty + q));
         ok = ok && poll(kO);
         used(q_need | kO);
-        if (ok && leader) mbar_arrive(&bars[kBarODone + w]);
+        if (ok && leader) arrive(bar0 + 8 * (kBarODone + w));
       }
       o_on = s_on;
     }
     // every MMA issued has to land before tensor memory is released
     const int drain = kBarDrain + w;
-    if (leader) tc::mma_commit(&bars[drain]);
+    if (leader) commit(bar0 + 8 * (drain));
     mbar_wait_bounded(&bars[drain], 0);
     __syncwarp();
   }
@@ -1024,6 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
+  if (tid == 0 && *abort_flag) flag_error(a.dev_error, K16V8_DEVERR_TIMEOUT);
 }
 
 }  // namespace attn8
