@@ -969,54 +969,47 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         }
       }
       if (!s_on && !o_on && !pass) break;
-      const uint32_t s_need = s_on ? (t == t_first ? kK | q_need : kK) : 0;
-      if (o_on) {
-        for (; o_skip > 0; --o_skip) next_v();
+      for (; o_skip > 0; --o_skip) next_v();
 #pragma unroll 1
-        for (int part = 0; part < o_parts; ++part) {
-          // (the last part's P V goes with S, but for a new piece's, which may be far off)
-          const bool join = part + 1 == o_parts && s_on && t != t_first;
-          const bool fresh = o_first && part == 0;  // O is written, not added to
-          ok = poll(kV | kP << part | (fresh ? kO : 0u) | (join ? s_need : 0u));
+      for (int op = 0; op <= o_parts; ++op) {
+        if (op < o_parts) {  // P V of a part
+          const uint32_t need = kV | kP << op | (o_first && op == 0 ? kO : 0u);
+          ok = poll(need);
           if (!ok) break;
-          const uint32_t b0 = dv_lo + v_at * (kVBytes / 16), p0 = tS + part * kHalf;
+          const uint32_t b0 = dv_lo + v_at * (kVBytes / 16), p0 = tS + op * kHalf;
+          const bool add = !o_first || op > 0;  // else O is written
 #pragma unroll
           for (int kk = 0; kk < kHalf / 16; ++kk)
             if (leader)
-              tc::mma_f16_ts(tO, p0 + kk * 8, b0 + kk * 128, dv_hi, kIdescO, !fresh || kk > 0);
-          if (leader && !join) {  // (else behind S)
-            commit(bar0 + 8 * (kBarVEmpty + v_at));
-            if (!o_two) arrive(bar0 + 8 * (kBarVEmpty + v_at));  // (the other slot does not read it)
-            if (part + 1 == o_parts && o_last) commit(bar0 + 8 * (kBarODone + w));
-          }
-          if (join) break;
-          used(kP << part | (fresh ? kO : 0u));
-          next_v();
-        }
-      }
-      if (ok && s_on && !(o_on && t != t_first)) ok = poll(s_need);
-      if (!ok) break;
-      if (s_on) {
-        const uint32_t a0 = dq_lo + q * (kQBytes / 16), b0 = dk_lo + k_at * (kKBytes / 16);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          if (leader)
-            tc::mma_f16_ss(tS, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, dk_hi,
-                           b0 + (kk >> 2) * (kKBlk / 16) + (kk & 3) * 2, dk_hi, kIdescS, kk > 0);
-        if (leader) {
-          commit(bar0 + 8 * (kBarSFull + w));
-          commit(bar0 + 8 * (kBarKEmpty + k_at));
-          if (!two) arrive(bar0 + 8 * (kBarKEmpty + k_at));
-        }
-        if (o_on && t != t_first) {  // what the last part left to do
+              tc::mma_f16_ts(tO, p0 + kk * 8, b0 + kk * 128, dv_hi, kIdescO, add || kk > 0);
           if (leader) {
             commit(bar0 + 8 * (kBarVEmpty + v_at));
-            if (!o_two) arrive(bar0 + 8 * (kBarVEmpty + v_at));
+            if (!o_two) arrive(bar0 + 8 * (kBarVEmpty + v_at));  // (the other slot does not read it)
+            if (o_last && op + 1 == o_parts) commit(bar0 + 8 * (kBarODone + w));
           }
-          used(kP << (o_parts - 1) | (o_first && o_parts == 1 ? kO : 0u));
+          used(need & ~kV);
           next_v();
+        } else if (s_on) {
+          ok = poll(t == t_first ? kK | q_need : kK);
+          if (!ok) break;
+          const uint32_t a0 = dq_lo + q * (kQBytes / 16), b0 = dk_lo + k_at * (kKBytes / 16);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            if (leader)
+              tc::mma_f16_ss(tS, a0 + (kk >> 2) * (kQBytes / 2 / 16) + (kk & 3) * 2, dk_hi,
+                             b0 + (kk >> 2) * (kKBlk / 16) + (kk & 3) * 2, dk_hi, kIdescS, kk > 0);
+          if (leader) {
+            commit(bar0 + 8 * (kBarSFull + w));
+            commit(bar0 + 8 * (kBarKEmpty + k_at));
+            if (!two) arrive(bar0 + 8 * (kBarKEmpty + k_at));
+          }
+          next_k();
         }
-        next_k();
+      }
+      if (!ok) break;
+      o_on = s_on;
+      o_parts = 0;
+      if (s_on) {
         o_two = two;
         o_first = t == t_first;
         o_parts = pc.halves(t);
@@ -1045,7 +1038,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         used(q_need | kO);
         if (ok && leader) arrive(bar0 + 8 * (kBarODone + w));
       }
-      o_on = s_on;
     }
     // every MMA issued has to land before tensor memory is released
     const int drain = kBarDrain + w;
