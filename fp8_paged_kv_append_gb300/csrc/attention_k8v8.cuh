@@ -328,6 +328,19 @@ __device__ __forceinline__ void exp_chunk(uint32_t t_p, const uint32_t (&s)[n], 
     tc::tmem_st8(t_p, pk);
 }
 
+// 32 bytes of a lane in one store where the address allows: every lane's row is a
+// line of its own, so stores take the time of their lines.
+__device__ __forceinline__ void store32(__half *p, const uint32_t (&x)[8]) {
+  if (reinterpret_cast<uintptr_t>(p) & 31) {
+    reinterpret_cast<uint4 *>(p)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4 *>(p)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+  } else {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+  }
+}
+
 // kTest: the form of the bounded-wait test hook.  CTA 0 withholds K of its first
 // tile (no arrival, nothing in flight), so the score warp's wait for it runs out
 // after kTestSpins polls and every role takes the abort path.
@@ -656,16 +669,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
               if ((__ldg(vr + e) & 0x7f) == 0x7f) o[e] = NAN;
           }
           if (row_valid && whole) {
+            uint32_t pk[8];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t pk[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const __half2 hh = __floats2half2_rn(o[q * 8 + 2 * e], o[q * 8 + 2 * e + 1]);
-                pk[e] = *reinterpret_cast<const uint32_t *>(&hh);
-              }
-              reinterpret_cast<uint4 *>(po)[2 * c + q] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            for (int e = 0; e < 8; ++e) {
+              const __half2 hh = __floats2half2_rn(o[2 * e], o[2 * e + 1]);
+              pk[e] = *reinterpret_cast<const uint32_t *>(&hh);
             }
+            store32(po + 16 * c, pk);
           } else if (row_valid) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
