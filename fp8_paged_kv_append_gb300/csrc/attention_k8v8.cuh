@@ -100,13 +100,14 @@ enum {
   kBarSFull = 34,     // +slot
   kBarPFull = 36,     // +slot + 2 * part, 4 arrivals (one per warp)
   kBarODone = 40,     // +slot: the slot's last P V of a piece (or it has none)
-  kBarOEmpty = 42,    // 8 arrivals: both O tiles have been read
   kBarJoin = 43,      // 8 arrivals (one per warp): both slots' statistics are in shared memory
   kBarPiece = 44,     // +ring entry: described
   kBarTaken = 48,     // +ring entry: kPieceReaders arrivals
   kBarDrain = 52,     // +slot: every MMA
   kBarTurn = 54,      // +slot, 4 arrivals: the other slot's exponentials of a tile are done
-  kNumBars = 56
+  kBarOEmpty = 56,    // +slot, 8 arrivals: the O tile has been read (two by each warp of its
+                      // slot, or with one row tile one by every warp)
+  kNumBars = 58
 };
 static_assert(kNumBars * 8 + 16 <= kBarBytes, "barriers");
 
@@ -396,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         count = kWidenWarps;
       if (i >= kBarPFull && i < kBarODone) count = 4;
       if ((i >= kBarQEmpty && i < kBarKstFull) || (i >= kBarKEmpty && i < kBarSFull)) count = 2;
-      if (i >= kBarTurn) count = 4;
+      if (i >= kBarTurn && i < kBarOEmpty) count = 4;
       if (i == kBarJoin) count = 8;
-      if (i == kBarOEmpty) count = 8;
+      if (i >= kBarOEmpty) count = 8;
       if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
       mbar_init(&bars[i], count);
     }
@@ -600,7 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       tiles += n_tiles;
       // ---- end of the piece: this slot's O, and with one row tile the other's ----
       ok = __all_sync(kFull, wait(kBarODone + w, p_idx & 1));
-      if (ok && !two) ok = __all_sync(kFull, wait(kBarODone + (w ^ 1), p_idx & 1));
       if (!ok) break;
       tc::fence_after_sync();
       const int pn = (p_idx & 3) * 2;
@@ -613,8 +613,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         stat[(w * 2 + 1) * kRows + r] = l;
         __syncwarp();
         if (lane == 0) arrive(bar0 + 8 * (kBarJoin));
-        ok = __all_sync(kFull, wait(kBarJoin, joins++ & 1));
+        // (the other slot's warps are in this piece, so its phase before is over)
+        ok = __all_sync(kFull, wait(kBarJoin, joins++ & 1)) &&
+             __all_sync(kFull, wait(kBarODone + (w ^ 1), p_idx & 1));
         if (!ok) break;
+        tc::fence_after_sync();
         const float m_o = stat[((w ^ 1) * 2 + 0) * kRows + r];
         const float l_o = stat[((w ^ 1) * 2 + 1) * kRows + r];
         m_all = fmaxf(m_used, m_o);
@@ -657,17 +660,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
               for (int e = 0; e < 16; ++e) o[e] = fmaf(__uint_as_float(x[e]), g_other, o[e]);
             }
           }
-          // NaN value codes of new tokens this row sees
-          for (uint64_t nm = mask_word & nan_mask; nm; nm &= nm - 1) {
-            const int pos = pc.base + __ffsll(static_cast<long long>(nm)) - 1;
-            const int page = __ldg(a.block_table + static_cast<int64_t>(pc.b) * a.maxp + pos / kPage);
-            if (page < 0 || page >= a.num_pages) continue;
-            const uint8_t *vr = a.v_cache + ((static_cast<int64_t>(page) * a.hkv + pc.g) * kPage +
-                                             pos % kPage) * kHeadDim + c * 16;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if ((__ldg(vr + e) & 0x7f) == 0x7f) o[e] = NAN;
-          }
           if (row_valid && whole) {
             uint32_t pk[8];
 #pragma unroll
@@ -683,6 +675,22 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
                   make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
           }
         }
+        // (seldom) NaN value codes of new tokens this row sees, over what was stored
+        for (uint64_t nm = row_valid ? mask_word & nan_mask : 0; nm; nm &= nm - 1) {
+          const int pos = pc.base + __ffsll(static_cast<long long>(nm)) - 1;
+          const int page = __ldg(a.block_table + static_cast<int64_t>(pc.b) * a.maxp + pos / kPage);
+          if (page < 0 || page >= a.num_pages) continue;
+          const uint8_t *vr = a.v_cache + ((static_cast<int64_t>(page) * a.hkv + pc.g) * kPage +
+                                           pos % kPage) * kHeadDim;
+#pragma unroll 1
+          for (int d = 16 * c_lo; d < 16 * c_hi; ++d) {
+            if ((__ldg(vr + d) & 0x7f) != 0x7f) continue;
+            if (whole)
+              po[d] = __ushort_as_half(0x7fff);
+            else
+              reinterpret_cast<float *>(pp + static_cast<int64_t>(d >> 2) * a.max_rows)[d & 3] = NAN;
+          }
+        }
         if (row_valid && (two || w == 0)) {
           if (!whole)
             a.part_lse[static_cast<int64_t>(pc.slot) * a.max_rows + row] = lse;
@@ -693,7 +701,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       tc::fence_before_sync();
       __syncwarp();
       if (lane == 0) {
-        arrive(bar0 + 8 * (kBarOEmpty));  // O is read: the next piece may write it
+        arrive(bar0 + 8 * (kBarOEmpty + w));  // O is read: the next piece may write it
+        arrive(bar0 + 8 * (kBarOEmpty + (two ? w : w ^ 1)));
         arrive(bar0 + 8 * (kBarTaken + ring.s));
       }
       ring.next(kPieceRing);
@@ -898,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
                                : lane == 1 ? kBarVFull
                                : lane < 4  ? kBarPFull + w + 2 * (lane - 2)
                                : lane < 6  ? kBarQFull + lane - 4
-                                           : kBarOEmpty);
+                                           : kBarOEmpty + w);
     uint32_t parity = lane == 6;
     uint32_t ready = 0;  // lanes whose barrier is known to be there
     const uint32_t limit = withholds ? kTestSpins : kMaxSpins;
