@@ -45,6 +45,7 @@ constexpr int kMmaWarp0 = 9, kMmaWarp1 = 15, kLoadVWarp = 12, kLoadKWarp = 13;
 constexpr int kWidenWarps = 2;               // for keys, and for values
 constexpr int kPieceRing = 4;
 constexpr int kPieceReaders = 16;            // every warp
+constexpr int kTurnTiles = 5;
 constexpr int kKTiles = 2;                   // fp16 tiles of keys
 constexpr int kVHalves = 3;                  // fp16 half tiles of values
 
@@ -55,7 +56,7 @@ constexpr uint32_t kVBytes = 2 * kVBlk;
 constexpr uint32_t kKBlk = kKv * 128;        // [128 pos][64 dims] fp16
 constexpr uint32_t kKBytes = 2 * kKBlk;
 // registers, together what the block was launched with
-constexpr int kSoftmaxRegs = 152, kOtherRegs = 104;
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 static_assert(kSoftmaxRegs + kOtherRegs == 2 * (65536 / kThreads), "two warpgroups each");
 
 constexpr uint32_t kTmemCols = 512;  // S_0 [0,128) S_1 [128,256) O_0 [256,384) O_1 [384,512)
@@ -276,12 +277,12 @@ __device__ __forceinline__ void put16(uint8_t *half, const Lanes &at, int step, 
 __device__ __forceinline__ void widen_half(uint8_t *half, const uint8_t *from, const Lanes &at,
                                            const float *sc) {
 #pragma unroll 1
-  for (int i0 = 0; i0 < 8; i0 += 4) {  // two pages
-    uint4 raw[4];
+  for (int i0 = 0; i0 < 8; i0 += 2) {  // two pages
+    uint4 raw[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) raw[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i) * 1024);
+    for (int i = 0; i < 2; ++i) raw[i] = *reinterpret_cast<const uint4 *>(from + (i0 + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) put16(half, at, i0 + i, raw[i], sc[(i0 + i) >> 1]);
+    for (int i = 0; i < 2; ++i) put16(half, at, i0 + i, raw[i], sc[(i0 + i) >> 1]);
   }
 }
 
@@ -467,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       const int after = two ? 0 : w ^ pc.turn;  // the slot's first tile
       const int mine = two ? pc.tiles : (pc.tiles + 1 - after) / 2;
       const int n_tiles = pc.tiles, d0 = pc.base - pc.t0 * kKv;
+      const bool in_turn = two && pc.tiles >= kTurnTiles;
       const int theirs = two ? 0 : (pc.tiles + after) / 2;  // units of the other slot to join
       float m_used = -INFINITY, l = 0.f;
       for (int k = 0; k < mine; ++k, ++units) {
@@ -479,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             arrive(bar0 + 8 * (kBarPFull + w));
             if (parts > 1) arrive(bar0 + 8 * (kBarPFull + w + 2));
           }
-          if (two) {
+          if (in_turn) {
             ok = __all_sync(kFull, wait(kBarTurn + w, (turns++ + 1 - w) & 1));
             if (!ok) break;
             if (lane == 0) arrive(bar0 + 8 * (kBarTurn + (w ^ 1)));
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             tc::tmem_st32(tO + lane_base + c * 32, o);
           }
         }
-        if (two) {
+        if (in_turn) {
           ok = __all_sync(kFull, wait(kBarTurn + w, (turns++ + 1 - w) & 1));
           if (!ok) break;
         }
@@ -594,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             hand_over(part);
           }
         }
-        if (two && lane == 0) arrive(bar0 + 8 * (kBarTurn + (w ^ 1)));
+        if (in_turn && lane == 0) arrive(bar0 + 8 * (kBarTurn + (w ^ 1)));
         l = l * alpha + (ps2.x + ps2.y);
       }
       if (!ok) break;
