@@ -38,6 +38,10 @@ using rope::widen8;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+// 16-bit rows: 80 registers and 24 warps per SM, 45.4 us for 8,192 tokens of 40 + 10
+// heads (5: 46.7, 7: 47.6; the turned rows kept in registers, 128 of them: 49.8).
+template <typename T>
+constexpr int kCtasPerSm = sizeof(T) == 2 ? 6 : 3;
 constexpr int kUnits = kPage * kUnitsPerRow / 32;  // of a lane and task
 
 struct Args {
@@ -91,6 +95,14 @@ __device__ __forceinline__ void turn_unit(float (&x)[8], float (&y)[8], const fl
   }
 }
 
+// Makes the compiler read these words again, in place of what it computed from them.
+template <typename T>
+__device__ __forceinline__ void keep(Raw<T> &r) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+    asm volatile("" : "+r"(r.w[i].x), "+r"(r.w[i].y), "+r"(r.w[i].z), "+r"(r.w[i].w));
+}
+
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
   uint32_t w[2];
 #pragma unroll
@@ -110,10 +122,11 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float ratio) {
 
 // grid: (pages that sequences may write, an upper bound; parts of the heads).
 template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads) append_k8v8_kernel(const Args a, int kv_per_cta,
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<T>) append_k8v8_kernel(const Args a, int kv_per_cta,
                                                                int q_per_cta) {
   extern __shared__ __align__(16) float2 table[];  // pair 8c + 2i + e of a token at [i][c][e]
-  __shared__ int s_sum[kWarps];
+  __shared__ int s_last[kWarps];
+  __shared__ int s_seq[3][kThreads];  // q0, n, L of the first sequences
   __shared__ uint32_t s_live;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int item = blockIdx.x;
@@ -121,24 +134,36 @@ __global__ void __launch_bounds__(kThreads) append_k8v8_kernel(const Args a, int
   pdl_launch_dependents();
 
   // Items of sequence b start at qo_indptr[b] / 16 + 2b, which leaves room for
-  // every page that its rows can touch: the sequence is the last that starts
-  // at or before the item.
-  int before = 0;
+  // every page that its rows can touch: the item's sequence is the last (of those
+  // in range) that starts at or before it.
+  int last = -1;
   for (int b = tid; b < a.batch; b += kThreads) {
-    before += (__ldg(a.qo_indptr + b) >> 4) + 2 * b <= item;
-    if (item == 0 && blockIdx.y == 0) {
-      int q0, n, L;
-      if (!sequence(a, b, q0, n, L)) flag_error(a.dev_error, K16V8_DEVERR_SEQLEN);
+    int q0, n, L;
+    const bool ok = sequence(a, b, q0, n, L);
+    if (!ok && item == 0 && blockIdx.y == 0) flag_error(a.dev_error, K16V8_DEVERR_SEQLEN);
+    if (ok && (q0 >> 4) + 2 * b <= item) last = b;
+    if (b < kThreads) {
+      s_seq[0][b] = q0;
+      s_seq[1][b] = n;
+      s_seq[2][b] = L;
     }
   }
-  before = __reduce_add_sync(kFull, before);
-  if (lane == 0) s_sum[warp] = before;
+  last = __reduce_max_sync(kFull, last);
+  if (lane == 0) s_last[warp] = last;
   __syncthreads();
   int b = -1;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) b += s_sum[w];
+  for (int w = 0; w < kWarps; ++w) b = max(b, s_last[w]);
+  if (b < 0) return;
   int q0, n, L;
-  if (b < 0 || !sequence(a, b, q0, n, L) || n == 0) return;
+  if (b < kThreads) {
+    q0 = s_seq[0][b];
+    n = s_seq[1][b];
+    L = s_seq[2][b];
+  } else {
+    sequence(a, b, q0, n, L);
+  }
+  if (n == 0) return;
   const int first = L - n;  // the first new position
   const int page = first / kPage + (item - (q0 >> 4) - 2 * b);
   if (page > (L - 1) / kPage || page < first / kPage) return;
@@ -146,10 +171,6 @@ __global__ void __launch_bounds__(kThreads) append_k8v8_kernel(const Args a, int
   const int rows = p1 - p0, lo = p0 - page * kPage;  // new rows, from this offset on
   const int64_t t0 = q0 + (p0 - first);
   const int pid = __ldg(a.block_table + static_cast<int64_t>(b) * a.maxp + page);
-  if (pid < 0 || pid >= a.num_pages) {
-    if (tid == 0 && blockIdx.y == 0) flag_error(a.dev_error, K16V8_DEVERR_PAGE);
-    return;
-  }
 
   // Tasks: keys and values of the part's KV heads, then its query heads.
   const int h0 = blockIdx.y * kv_per_cta, nh = min(kv_per_cta, a.hkv - h0);
@@ -185,6 +206,10 @@ __global__ void __launch_bounds__(kThreads) append_k8v8_kernel(const Args a, int
     }
   };
   if (warp < tasks) load(warp);
+  if (pid < 0 || pid >= a.num_pages) {
+    if (tid == 0 && blockIdx.y == 0) flag_error(a.dev_error, K16V8_DEVERR_PAGE);
+    return;
+  }
 
   if (warp == 0) {  // rows whose positions are in range
     bool ok = lane < rows;
@@ -209,31 +234,37 @@ __global__ void __launch_bounds__(kThreads) append_k8v8_kernel(const Args a, int
     if (task != warp) load(task);
     const bool is_k = task < nh, is_v = !is_k && task < 2 * nh;
     const bool turns = !is_v && turned_unit;
-    float x[kUnits][8], y[kUnits][8];
-    float top = 0.f;
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int r = r0 + 4 * i;
-      if (!(live >> r & 1)) continue;
-      widen8(raw[i].w, x[i], static_cast<const T *>(nullptr));
-      widen8(raw[i].w + sizeof(T) / 2, y[i], static_cast<const T *>(nullptr));
-      if (turns)
-        turn_unit<kInterleaved>(x[i], y[i], reinterpret_cast<const float4 *>(table + r * half) + c,
-                                half);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x[i][e]), fabsf(y[i][e])));
-    }
     const bool apart = !kInterleaved && turns;
+    // a unit of this lane, turned; 16-bit rows stay as they were loaded and are turned
+    // again for the codes, which costs less than the registers of their turned form
+    auto unit = [&](int i, float (&x)[8], float (&y)[8]) {
+      widen8(raw[i].w, x, static_cast<const T *>(nullptr));
+      widen8(raw[i].w + sizeof(T) / 2, y, static_cast<const T *>(nullptr));
+      if (turns)
+        turn_unit<kInterleaved>(
+            x, y, reinterpret_cast<const float4 *>(table + (r0 + 4 * i) * half) + c, half);
+    };
     if (!is_k && !is_v) {  // a query head
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const int r = r0 + 4 * i;
         if (!(live >> r & 1)) continue;
+        float x[8], y[8];
+        unit(i, x, y);
         __half *dst = a.q_out + ((t0 + r) * a.hq + qh0 + task - 2 * nh) * kHeadDim;
-        *reinterpret_cast<uint4 *>(dst + (apart ? 8 : 16) * c) = narrow8(x[i]);
-        *reinterpret_cast<uint4 *>(dst + (apart ? 8 * c + half : 16 * c + 8)) = narrow8(y[i]);
+        *reinterpret_cast<uint4 *>(dst + (apart ? 8 : 16) * c) = narrow8(x);
+        *reinterpret_cast<uint4 *>(dst + (apart ? 8 * c + half : 16 * c + 8)) = narrow8(y);
       }
       continue;
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      if (!(live >> (r0 + 4 * i) & 1)) continue;
+      float x[8], y[8];
+      unit(i, x, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(x[e]), fabsf(y[e])));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
@@ -242,14 +273,20 @@ __global__ void __launch_bounds__(kThreads) append_k8v8_kernel(const Args a, int
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         if (!(live >> (r0 + 4 * i) & 1)) continue;
+        float x[8], y[8];
+        unit(i, x, y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float ax = fabsf(x[i][e]), ay = fabsf(y[i][e]);
+          const float ax = fabsf(x[e]), ay = fabsf(y[e]);
           top = fmaxf(top, fmaxf(ax < INFINITY ? ax : 0.f, ay < INFINITY ? ay : 0.f));
         }
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    }
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) keep(raw[i]);
     }
     const int h = is_k ? h0 + task : h0 + task - nh;
     const int64_t tile = static_cast<int64_t>(pid) * a.hkv + h;
@@ -279,8 +316,10 @@ __global__ void __launch_bounds__(kThreads) append_k8v8_kernel(const Args a, int
     for (int i = 0; i < kUnits; ++i) {
       const int r = r0 + 4 * i;
       if (!(live >> r & 1)) continue;
+      float x[8], y[8];
+      unit(i, x, y);
       uint8_t *dst = codes + (lo + r) * kHeadDim;
-      const uint2 cx = codes8(x[i], inv), cy = codes8(y[i], inv);
+      const uint2 cx = codes8(x, inv), cy = codes8(y, inv);
       if (apart) {
         *reinterpret_cast<uint2 *>(dst + 8 * c) = cx;
         *reinterpret_cast<uint2 *>(dst + 8 * c + half) = cy;

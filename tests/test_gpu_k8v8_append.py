@@ -378,3 +378,20 @@ def test_append_refusals(K):
                 dict(inv_freq=freq[:4].contiguous(), pair_axis=bytes(4))):
         with pytest.raises(K.K16V8Error):
             call(**bad)
+
+
+def test_append_garbage_offsets_spare_the_others(K):
+    """Offsets out of range before and behind a sequence do not lose it."""
+    g = torch.ones((12, 6, 128), dtype=torch.float16, device=dev())
+    kc = torch.full((4, 1, 16, 128), 0x31, dtype=torch.uint8, device=dev())
+    vc, sc = kc.clone(), torch.full((4, 1, 2), 4.0, dtype=torch.float32, device=dev())
+    qo = torch.full((12, 4, 128), 7.5, dtype=torch.float16, device=dev())
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    indptr = np.array([0, 1000000, 8, 12, -2 ** 31, 2 ** 31 - 1], np.int32)
+    K.k16v8_rope_kv_append_k8v8(g[:, :4], g[:, 4:5], g[:, 5:], to_dev(indptr), None, None, None,
+                                to_dev(np.array([[0], [1], [2], [3], [3]], np.int32)),
+                                to_dev(np.full(5, 9, np.int32)), qo, kc, vc, sc, dev_error=err)
+    assert K.k16v8_read_device_error(err) == K.DEVERR_SEQLEN
+    touched = (kc.cpu() != 0x31).any(-1).any(1).numpy()
+    assert touched[2, 5:9].all() and touched.sum() == 4
+    assert (qo.cpu() != 7.5).any(-1).any(-1).tolist() == [False] * 8 + [True] * 4
