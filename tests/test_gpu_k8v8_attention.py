@@ -92,6 +92,21 @@ def test_many_sequences(K, causal):
     check(K, causal, 5, counts, [c + int(x) for c, x in zip(counts, rng.integers(0, 60, 400))], 1)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("most", [20, 120])
+def test_many_pieces_per_cta(K, causal, most):
+    """Every CTA goes through many segments, with one and with two row tiles in turn,
+    of one tile and of several, ending in either half of a tile."""
+    rng = np.random.default_rng(most)
+    B, hkv = 48, 4
+    counts = [int(x) for x in rng.integers(0, most + 1, B)]
+    if most > 32:
+        counts[::3] = [int(x) for x in rng.integers(1, 33, len(counts[::3]))]
+    lens = [c + int(x) for c, x in zip(counts, rng.integers(0, 700, B))]
+    lens[5], lens[17], lens[30] = counts[5], counts[17], counts[30]
+    check(K, causal, most, counts, lens, hkv, pad=3)
+
+
 @pytest.mark.parametrize("exps", [(-15, -15), (-15, 7), (7, 7)])
 @pytest.mark.parametrize("counts", [[20], [60, 5]])
 def test_scales(K, exps, counts):
