@@ -10,7 +10,7 @@
 // scales are constant over a page, which is a warp's unit of work, so kappa
 // joins the score's factor and nu the weight: no element is multiplied by one.
 //
-// The cut into equal tile ranges, its plan and the merge are those of the
+// The cut into equal tile ranges, its plan and the workspace are those of the
 // K16/V8 balanced decode (decode_balanced.cu): CTA i of one full wave takes flat
 // (sequence, KV head, page) tiles [i W, (i + 1) W), warps take tiles in turn.
 //
@@ -552,6 +552,117 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
   }
 }
 
+// Joins the pieces of the segments that were cut: o = sum_p e^(lse_p - lse) o_p, lse
+// = log sum_p e^lse_p.  A CTA takes a (sequence, KV head), kSplit warps one of its
+// query heads, a lane 4 dims; kFlight pieces of a warp are in flight.
+constexpr int kFlight = 8;
+
+struct Joined {
+  float M = -INFINITY, S = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ float scale_to(float top) {  // 2^(M - top) of the state
+    const float fade = M == -INFINITY ? (S != S ? S : 0.f) : ex2((M - top) * kLog2e);
+    return fade;
+  }
+};
+
+template <int kSplit>
+__global__ void __launch_bounds__(kGroup * kSplit * 32) merge_k8v8_kernel(
+    const float *__restrict__ part_o, const float *__restrict__ part_lse,
+    const int32_t *__restrict__ plan, int32_t hkv, __half *__restrict__ out,
+    float *__restrict__ lse_out) {
+  __shared__ float4 s_o[kSplit][kGroup][32];
+  __shared__ float2 s_ms[kSplit][kGroup];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = warp % kGroup, part = warp / kGroup;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int b = blockIdx.x / hkv, g = blockIdx.x - b * hkv;
+  const int W = __ldg(plan + 1), pb = __ldg(plan + 2 + b), np = __ldg(plan + 3 + b) - pb;
+  Joined st;
+  if (np > 0) {
+    const int s0 = pb * hkv + g * np;
+    const int i0 = s0 / W, i1 = (s0 + np - 1) / W;
+    if (i0 == i1) return;  // held whole by one CTA, which wrote the rows
+    const int n = i1 - i0 + 1;
+    auto row_of = [&](int p) {  // the first piece's slot, the first slot of the CTAs behind
+      return (static_cast<int64_t>(i0 + p) * 2 + (p == 0 && s0 != i0 * W ? 1 : 0)) * kGroup + head;
+    };
+    for (int p0 = part * kFlight; p0 < n; p0 += kSplit * kFlight) {
+      float4 x[kFlight];
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {  // (asked for in one go, the last one again: no branch)
+        const float *p = part_o + row_of(min(p0 + u, n - 1)) * kHeadDim + lane * 4;
+        asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x[u].x), "=f"(x[u].y), "=f"(x[u].z), "=f"(x[u].w)
+                     : "l"(p));
+      }
+      const float l_own =
+          lane < kFlight && p0 + lane < n ? __ldg(part_lse + row_of(p0 + lane)) : -INFINITY;
+      float top = fmaxf(st.M, l_own);  // (NaN counts as nothing here and makes the sum NaN)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      const float fade = st.scale_to(top);
+      st.M = top;
+      st.S *= fade;
+      st.o = make_float4(st.o.x * fade, st.o.y * fade, st.o.z * fade, st.o.w * fade);
+      const float w_own = l_own == -INFINITY ? 0.f : ex2((l_own - top) * kLog2e);
+#pragma unroll
+      for (int u = 0; u < kFlight; ++u) {
+        const float w = __shfl_sync(kFull, w_own, u);
+        st.S += w;
+        st.o.x = fmaf(w, x[u].x, st.o.x);
+        st.o.y = fmaf(w, x[u].y, st.o.y);
+        st.o.z = fmaf(w, x[u].z, st.o.z);
+        st.o.w = fmaf(w, x[u].w, st.o.w);
+      }
+    }
+  }
+  if constexpr (kSplit > 1) {
+    s_o[part][head][lane] = st.o;
+    if (lane == 0) s_ms[part][head] = make_float2(st.M, st.S);
+    __syncthreads();
+    if (part > 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kSplit; ++k) top = fmaxf(top, s_ms[k][head].x);
+    Joined all;
+    all.M = top;
+#pragma unroll
+    for (int k = 0; k < kSplit; ++k) {
+      Joined one;
+      one.M = s_ms[k][head].x;
+      one.S = s_ms[k][head].y;
+      one.o = s_o[k][head][lane];
+      const float w = one.scale_to(top);
+      all.S = fmaf(w, one.S, all.S);
+      all.o.x = fmaf(w, one.o.x, all.o.x);
+      all.o.y = fmaf(w, one.o.y, all.o.y);
+      all.o.z = fmaf(w, one.o.z, all.o.z);
+      all.o.w = fmaf(w, one.o.w, all.o.w);
+    }
+    st = all;
+  }
+  // S = 0: no position, or no live page
+  const float inv = st.S == 0.f ? 0.f : 1.f / st.S;
+  const __half2 h[2] = {__floats2half2_rn(st.o.x * inv, st.o.y * inv),
+                        __floats2half2_rn(st.o.z * inv, st.o.w * inv)};
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kGroup + head;
+  *reinterpret_cast<uint2 *>(out + row * kHeadDim + lane * 4) = *reinterpret_cast<const uint2 *>(h);
+  if (lane == 0 && lse_out) lse_out[row] = st.S == 0.f ? -INFINITY : st.M + lg2(st.S) * kLn2;
+}
+
+template <int kSplit>
+static int32_t launch_merge(int32_t batch, int32_t hkv, const uint8_t *ws, size_t o_off,
+                            size_t lse_off, void *out, float *lse, cudaStream_t s) {
+  return k16v8_launch_pdl(merge_k8v8_kernel<kSplit>, dim3(static_cast<unsigned>(batch) * hkv),
+                          dim3(kGroup * kSplit * 32), 0, s,
+                          reinterpret_cast<const float *>(ws + o_off),
+                          reinterpret_cast<const float *>(ws + lse_off),
+                          reinterpret_cast<const int32_t *>(ws), hkv, static_cast<__half *>(out),
+                          lse);
+}
+
 }  // namespace decode8
 }  // namespace k16v8
 
@@ -590,7 +701,7 @@ extern "C" int32_t k16v8_paged_decode_attention_k8v8(
     return K16V8_ERR_INVALID_ARG;
   const int sms = k16v8_sm_count();
   if (sms <= 0) return K16V8_ERR_CUDA;
-  // the workspace and the merge are the balanced decode's
+  // the workspace is the balanced decode's
   const size_t need = k16v8_decode_balanced_workspace_size(batch, num_qo_heads, head_dim);
   if (need == 0) return K16V8_ERR_CUDA;
   if (workspace_bytes < need) return K16V8_ERR_WORKSPACE_TOO_SMALL;
@@ -622,6 +733,11 @@ extern "C" int32_t k16v8_paged_decode_attention_k8v8(
       reinterpret_cast<float *>(ws + o_off), reinterpret_cast<float *>(ws + lse_off),
       static_cast<__half *>(out), lse, dev_error);
   if (st != K16V8_OK) return st;
-  return k16v8_merge_balanced(workspace, workspace_bytes, batch, num_qo_heads, num_kv_heads,
-                              head_dim, out, lse, stream);
+  // Few segments are cut by many CTAs each (61 for one sequence of 128K and 10 heads),
+  // many by a few.  4 warps a row and 1, both kernels: 1 x 1K 7.4 and 9.0 us, 1 x 128K
+  // 58.2 and 63.5; 32 x 1K 21.2 and 19.8, 256 x 0.5K 55.4 and 49.9.
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return batch * num_kv_heads <= 64
+             ? decode8::launch_merge<4>(batch, num_kv_heads, ws, o_off, lse_off, out, lse, s)
+             : decode8::launch_merge<1>(batch, num_kv_heads, ws, o_off, lse_off, out, lse, s);
 }
