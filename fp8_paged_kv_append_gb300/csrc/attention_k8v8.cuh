@@ -209,13 +209,11 @@ __device__ __forceinline__ uint64_t visible(int rel, uint64_t m) {
   return m >> rel;
 }
 
-// Page id of page `lane` of half tile h: -1 outside the pool, -2 behind the last
-// position (and for lanes without a page).
-__device__ __forceinline__ int page_id(const Args &a, const Piece &p, int h, int lane) {
-  const int page = h * kPagesPerHalf + lane;
-  if (lane >= kPagesPerHalf || page * kPage >= p.L) return -2;
-  const int pid = __ldg(a.block_table + static_cast<int64_t>(p.b) * a.maxp + page);
-  return pid >= 0 && pid < a.num_pages ? pid : -1;
+// Entry `page` of a piece's block table (anything behind the last position).
+__device__ __forceinline__ int table_entry(const Args &a, const Piece &p, int page) {
+  int id = -1;
+  if (page * kPage < p.L) id = __ldg(a.block_table + static_cast<int64_t>(p.b) * a.maxp + page);
+  return id;
 }
 
 // Registers of a thread of this warpgroup from here on.
@@ -793,7 +791,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     Pair uses;  // of the query buffers
     bool ok = true;
     uint32_t p_idx = 0, tiles = 0;
-    int h = 0, pid = -2;
+    int h = 0;
+    // page ids of eight half tiles, a lane each, and of the eight behind: their loads
+    // take longer than a step
+    int ids = -1, ids_next = -1;
     pc.t0 = pc.h1 = 0;
     bool start = true;  // a description is due (V), at the start and behind a first tile
     while (true) {
@@ -818,10 +819,18 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       if (h == pc.h1) {
         if (!get_piece(pc, ring)) break;
         h = 2 * pc.t0;
-        pid = page_id(a, pc, h, lane);
+        ids = table_entry(a, pc, h * kPagesPerHalf + lane);
+        ids_next = table_entry(a, pc, h * kPagesPerHalf + 32 + lane);
       }
       if (dst.wrapped) ok = __all_sync(kFull, wait(bar_read + dst.s, dst.phase ^ 1));
       if (!ok) break;
+      const int at = (h - 2 * pc.t0) & 7;
+      int pid = __shfl_sync(kFull, ids, at * kPagesPerHalf + (lane & 3));
+      // -2: behind the last position (and lanes without a page), -1: outside the pool
+      if (lane >= kPagesPerHalf || (h * kPagesPerHalf + lane) * kPage >= pc.L)
+        pid = -2;
+      else if (pid < 0 || pid >= a.num_pages)
+        pid = -1;
       const uint32_t bad = __ballot_sync(kFull, pid == -1);
       const uint32_t bytes = __popc(__ballot_sync(kFull, pid >= 0)) * 2048u;
       const bool withheld = withholds && !is_v && issued == 0;
@@ -850,7 +859,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       const bool first = h == 2 * pc.t0;
       ++h;
       if (!(h & 1) || h == pc.h1) ++tiles;
-      if (h < pc.h1) pid = page_id(a, pc, h, lane);
+      if (at == 7) {
+        ids = ids_next;
+        ids_next = table_entry(a, pc, (h + 8) * kPagesPerHalf + lane);
+      }
       __syncwarp();
       dst.next(M::kStages);
       ++issued;
