@@ -86,8 +86,8 @@ __device__ __forceinline__ void merge_rows(const Args &a, const int4 &cut, int f
   if (chunk == 0 && a.lse) a.lse[orow] = dead ? -INFINITY : M + lg2(S) * kLn2;
 }
 
-// One CTA: 32 rows by 16 kMerge dims.  Latency-bound: the cut, lengths and rows,
-// stores.
+// One CTA: 32 rows by 16 kMerge dims.  Latency-bound: the cut, then LSEs and rows
+// together, then stores.
 constexpr int kMergeWarps = 4;
 template <int kMerge>
 __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const Args a) {
@@ -204,7 +204,6 @@ static int32_t attention_k8v8(bool causal, const void *q, const int32_t *qo_indp
                       total_q,
                       max_qlen,
                       causal ? 1 : 0,
-                      k_cache,
                       v_cache,
                       kv_scale,
                       block_table,
@@ -231,6 +230,10 @@ static int32_t attention_k8v8(bool causal, const void *q, const int32_t *qo_indp
   st = max_qlen > attn8::kTileTokens ? attn8::launch_split<true, kTest>(mq, mk, mv, a, w.ctas, s)
                                      : attn8::launch_split<false, kTest>(mq, mk, mv, a, w.ctas, s);
   if (st != K16V8_OK) return st;
+  // Short segments are cut by many CTAs each and want pieces in flight (8), tall ones
+  // fewer CTAs (8 per 32 rows or 2).  64 and 32 dims to a CTA, both kernels: 5 rows over
+  // 1,500 13.8 and 13.3 us, 8 rows at 128K 117.2 and 116.0; 20 over 8,000 121.7 and
+  // 122.3, 64 x 40 of 300 42.4 and 43.1, 8 x 1024 131.9 and 133.4.
   return max_qlen > 16 ? attn8::launch_merge<4>(a, w.ctas, s)
                        : attn8::launch_merge<2>(a, w.ctas, s);
 }

@@ -7,25 +7,48 @@
 // The 4 query heads of the GQA group times 32 tokens are the 128 rows of an MMA
 // tile (row = token * 4 + head).  Two score tiles S_0, S_1 and two output tiles
 // O_0, O_1 (128 columns each; P, fp16, over the first half of its S columns) let
-// one tile's softmax overlap the other's MMAs:
+// one slot's softmax overlap the other's MMAs:
 //  * groups of up to 32 tokens: one row tile; KV tiles alternate between slots 0
 //    and 1, each with its own running max, sum and O, joined at the end of the
 //    piece;
 //  * larger groups: two row tiles, both over every KV tile.
-// A unit is one (KV tile, slot): S = Q K^T, softmax, O += P V.  It is worked on in
-// two parts of 64 positions, each with half of the slot's S columns, so that one
-// part's S and P V run under the other's softmax.
+// A unit is one (KV tile, slot): S = Q K^T (128 x 128 x 128), the row maximum, the
+// exponentials in two parts of 64 positions, O += P V of either part.  Each slot
+// has a warp that issues both products: MMAs of one thread execute in the order
+// of their issue, so the next S may follow the P V that reads its columns without
+// a wait between them.  (One part's S under the other's softmax, 64 columns each:
+// 159 against 151 us for 8 x 1024.)
 //
 // Keys and values arrive as codes (TMA boxes of 2 KB, a page and head) with
-// their pages' scales (4-byte asynchronous copies on the same barrier), and are
-// widened to fp16 half tiles of 64 positions in the layouts the MMAs read: a code
-// times a power of two in the cache's range is an fp16 number, so the MMAs see
-// the cache's values exactly and nothing is scaled afterwards.
+// their pages' scales (4-byte asynchronous copies on the same barrier) in half
+// tiles of 64 positions, and are widened to fp16 in the layouts the MMAs read: a
+// code times a power of two in the cache's range is an fp16 number, so the MMAs
+// see the cache's values exactly and nothing is scaled afterwards.  (The e4m3 MMA
+// would take the codes as they are, but wants one scale for all positions of P V
+// and P itself in e4m3: 2^-4 of a weight instead of 2^-11.)
 //
 // Warp roles (16 warps): 0-3 / 4-7 softmax of slot 0 / 1, one thread per row; 8,
 // 10 widen keys, 11, 14 values; 9 / 15 issue the MMAs of slot 0 / 1; 13 loads Q
 // (TMA) and key pages; 12 loads value pages, walks the CTA's pieces and hands them
 // to the others.  Every hand-off is an mbarrier, every wait is bounded.
+//
+// What bounds it.  With two row tiles: the chain S -> maximum -> exponentials -> P V,
+// 2,140 cycles a unit in long pieces where the MMAs take 1,270 at the cuBLAS rate,
+// and in short ones the start and end of a piece: 1,024 rows of 8,192 143 us (1.13
+// PFLOP/s, 0.59 of that rate), 8 x 1024 causal 132 us (651 TFLOP/s), 16 x 448 rows
+// over 1,500 178 us (696).  With one row tile: the hand-offs from loads to widening
+// to MMAs (time stamps show no role busy for much more than half of the time); 8
+// rows at 128K 116 us (2.9 TB/s of codes, 0.43 of the copy rate), 5 rows over 1,500
+// 13.3 us, nearly all of it the latency of one piece and the merge.
+// Code size matters throughout: the roles' loops together are about as large as
+// the instruction cache near the SM, and every variant below that added code lost
+// more than it won.
+// Measured and left out (us, against what was kept at the time): a thread's 128
+// scores held in registers between maximum and exponentials (156 / 133: 56
+// registers are left to the other roles), an epilogue that turns rows through
+// shuffles (151 / 146), widening by four warps per side instead of two, as
+// neighbouring rows or as alternate halves (122 / 116 for 8 rows at 128K), a ring
+// of codes and fp16 tiles for either slot (127 / 116).
 #pragma once
 
 #include "k16v8_device.cuh"
@@ -45,7 +68,13 @@ constexpr int kMmaWarp0 = 9, kMmaWarp1 = 15, kLoadVWarp = 12, kLoadKWarp = 13;
 constexpr int kWidenWarps = 2;               // for keys, and for values
 constexpr int kPieceRing = 4;
 constexpr int kPieceReaders = 16;            // every warp
-constexpr int kTurnTiles = 5;
+// From this many KV tiles on, the slots of two row tiles exponentiate in turn, so that
+// one's exponentials run under the other's MMAs instead of both waiting for both.
+// 1,024 rows of 8,192 (64 tiles) 158.8 -> 142.7 us, 16 x 448 over 1,500 (12 tiles)
+// 186.6 -> 177.8.  In short pieces it only delays a slot: always, 8 x 1024 (1 to 8)
+// 132.1 -> 134.1 and 64 x 40 of 300 42.4 -> 43.6; from 5 or 9 on, 1 x 4,000 191.7 ->
+// 195.5 and 202.2.
+constexpr int kTurnTiles = 3;
 constexpr int kKTiles = 2;                   // fp16 tiles of keys
 constexpr int kVHalves = 3;                  // fp16 half tiles of values
 
@@ -55,7 +84,8 @@ constexpr uint32_t kVBlk = kHalf * 128;      // [64 pos][64 dims] fp16
 constexpr uint32_t kVBytes = 2 * kVBlk;
 constexpr uint32_t kKBlk = kKv * 128;        // [128 pos][64 dims] fp16
 constexpr uint32_t kKBytes = 2 * kKBlk;
-// registers, together what the block was launched with
+// registers, together what the block was launched with; 136 + 120 and 152 + 104 are
+// both 1 us slower in 130 (the first spills in softmax, the second in the others)
 constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 static_assert(kSoftmaxRegs + kOtherRegs == 2 * (65536 / kThreads), "two warpgroups each");
 
@@ -67,7 +97,9 @@ constexpr uint32_t kBarBytes = 512;
 template <bool kWide>
 struct Smem {
   static constexpr int kQSlots = kWide ? 2 : 1;
-  static constexpr int kStages = kWide ? 3 : 5;  // of codes, keys and values each
+  // of codes, keys and values each; what is left beside Q.  (8 rows at 128K: 3 121.3 us,
+  // 4 118.4, 5 116.0)
+  static constexpr int kStages = kWide ? 3 : 5;
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kKst = kQ + kQSlots * kQBytes;
   static constexpr uint32_t kVst = kKst + kStages * kStage;

@@ -33,7 +33,7 @@ constexpr int kGroupTokens = 2 * kTileTokens;
 struct Args {  // (queries come through their tensor map)
   const int32_t *qo_indptr;
   int32_t total_q, max_q, causal;
-  const uint8_t *k_cache, *v_cache;
+  const uint8_t *v_cache;  // (codes come through their tensor maps; NaN ones are looked up)
   const float *kv_scale;
   const int32_t *block_table;
   int32_t maxp;

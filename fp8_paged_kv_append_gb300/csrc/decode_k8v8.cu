@@ -10,9 +10,9 @@
 // scales are constant over a page, which is a warp's unit of work, so kappa
 // joins the score's factor and nu the weight: no element is multiplied by one.
 //
-// The cut into equal tile ranges, its plan and the workspace are those of the
-// K16/V8 balanced decode (decode_balanced.cu): CTA i of one full wave takes flat
-// (sequence, KV head, page) tiles [i W, (i + 1) W), warps take tiles in turn.
+// The cut is that of the K16/V8 balanced decode (decode_balanced.cu): CTA i of one
+// full wave takes flat (sequence, KV head, page) tiles [i W, (i + 1) W), warps take
+// tiles in turn, and a merge joins the segments that were cut.
 //
 // HBM-bound: 4,096 bytes of codes and 8 of scales per tile.  What a tile costs in
 // instructions decides whether the stream stays full (the K16/V8 kernel spends
@@ -28,6 +28,9 @@
 //    needs one vote instead of a reduction over its tokens.
 // Tiles are staged by TMA with the 128-byte swizzle: a row is 128 bytes, and the
 // lanes that read one column of 16-byte chunks would meet in the same banks.
+// Both kernels: 16 sequences of 8K 58.3 us (5.86 TB/s of the bytes it cannot do
+// without, 0.86 of the copy rate), one of 128K 58.2, 32 of up to 1K 19.7 (0.53), one
+// of 1K 7.4.  Some 7 us are fixed: plan, first loads, the cut segments' merge.
 #include <math.h>
 
 #include "k8v8_device.cuh"
@@ -652,13 +655,32 @@ __global__ void __launch_bounds__(kGroup * kSplit * 32) merge_k8v8_kernel(
   if (lane == 0 && lse_out) lse_out[row] = st.S == 0.f ? -INFINITY : st.M + lg2(st.S) * kLn2;
 }
 
+// Workspace: plan int32 [T, W, P(0 .. batch)], partial rows fp32 [CTA][2][4][128], their
+// LSEs fp32 [CTA][2][4], each on 256 bytes.
+struct Layout {
+  int ctas;
+  size_t o_off, lse_off, total;
+};
+
+static bool layout(int32_t batch, Layout *w) {
+  const int sms = k16v8_sm_count();
+  if (sms <= 0) return false;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  w->ctas = sms * kCtasPerSm;
+  const size_t rows = static_cast<size_t>(w->ctas) * 2 * kGroup;
+  w->o_off = up((static_cast<size_t>(batch) + 3) * sizeof(int32_t));
+  w->lse_off = w->o_off + up(rows * kHeadDim * sizeof(float));
+  w->total = w->lse_off + up(rows * sizeof(float));
+  return true;
+}
+
 template <int kSplit>
-static int32_t launch_merge(int32_t batch, int32_t hkv, const uint8_t *ws, size_t o_off,
-                            size_t lse_off, void *out, float *lse, cudaStream_t s) {
+static int32_t launch_merge(int32_t batch, int32_t hkv, const uint8_t *ws, const Layout &w,
+                            void *out, float *lse, cudaStream_t s) {
   return k16v8_launch_pdl(merge_k8v8_kernel<kSplit>, dim3(static_cast<unsigned>(batch) * hkv),
                           dim3(kGroup * kSplit * 32), 0, s,
-                          reinterpret_cast<const float *>(ws + o_off),
-                          reinterpret_cast<const float *>(ws + lse_off),
+                          reinterpret_cast<const float *>(ws + w.o_off),
+                          reinterpret_cast<const float *>(ws + w.lse_off),
                           reinterpret_cast<const int32_t *>(ws), hkv, static_cast<__half *>(out),
                           lse);
 }
@@ -670,7 +692,11 @@ using namespace k16v8;
 
 extern "C" size_t k16v8_decode_workspace_size_k8v8(int32_t batch, int32_t num_qo_heads,
                                                    int32_t head_dim) {
-  return k16v8_decode_balanced_workspace_size(batch, num_qo_heads, head_dim);
+  decode8::Layout w;
+  if (batch < 0 || batch > decode8::kMaxBatch || num_qo_heads <= 0 || head_dim != kHeadDim ||
+      !decode8::layout(batch, &w))
+    return 0;
+  return w.total;
 }
 
 extern "C" int32_t k16v8_paged_decode_attention_k8v8(
@@ -692,25 +718,18 @@ extern "C" int32_t k16v8_paged_decode_attention_k8v8(
       static_cast<int64_t>(max_pages_per_seq) * kPage >= (1LL << 31))
     return K16V8_ERR_INVALID_ARG;
   if (batch == 0) return K16V8_OK;
-  if (!q || !k_cache || !v_cache || !kv_scale || !block_table || !seq_lens || !workspace || !out)
+  if (!q || !k_cache || !v_cache || !kv_scale || (!block_table && max_pages_per_seq > 0) ||
+      !seq_lens || !workspace || !out)
     return K16V8_ERR_INVALID_ARG;
   if (!k16v8_aligned(q, 16) || !k16v8_aligned(k_cache, 16) || !k16v8_aligned(v_cache, 16) ||
       !k16v8_aligned(kv_scale, 8) || !k16v8_aligned(workspace, 256) ||
       !k16v8_aligned(block_table, 4) || !k16v8_aligned(seq_lens, 4) || !k16v8_aligned(out, 16) ||
       (lse && !k16v8_aligned(lse, 4)))
     return K16V8_ERR_INVALID_ARG;
-  const int sms = k16v8_sm_count();
-  if (sms <= 0) return K16V8_ERR_CUDA;
-  // the workspace is the balanced decode's
-  const size_t need = k16v8_decode_balanced_workspace_size(batch, num_qo_heads, head_dim);
-  if (need == 0) return K16V8_ERR_CUDA;
-  if (workspace_bytes < need) return K16V8_ERR_WORKSPACE_TOO_SMALL;
-  const int ctas = sms * decode8::kCtasPerSm;
+  decode8::Layout w;
+  if (!decode8::layout(batch, &w)) return K16V8_ERR_CUDA;
+  if (workspace_bytes < w.total) return K16V8_ERR_WORKSPACE_TOO_SMALL;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
-  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t o_off = up((static_cast<size_t>(batch) + 3) * sizeof(int32_t));
-  const size_t lse_off =
-      o_off + up(static_cast<size_t>(ctas) * 2 * kGroup * kHeadDim * sizeof(float));
 
   CUtensorMap mk, mv;
   const uint64_t rows = static_cast<uint64_t>(num_pages) * num_kv_heads * kPage;
@@ -726,11 +745,11 @@ extern "C" int32_t k16v8_paged_decode_attention_k8v8(
     if (dev >= 0 && dev < 64) configured[dev] = true;
   }
   const int32_t st = k16v8_launch_pdl(
-      decode8::decode_k8v8_kernel, dim3(ctas), dim3(decode8::kWarps * 32), decode8::kSmemBytes,
+      decode8::decode_k8v8_kernel, dim3(w.ctas), dim3(decode8::kWarps * 32), decode8::kSmemBytes,
       static_cast<cudaStream_t>(stream), mk, mv, static_cast<const __half *>(q),
       reinterpret_cast<const float2 *>(kv_scale), block_table, max_pages_per_seq, seq_lens, batch,
       num_kv_heads, num_pages, sm_scale, reinterpret_cast<int32_t *>(ws),
-      reinterpret_cast<float *>(ws + o_off), reinterpret_cast<float *>(ws + lse_off),
+      reinterpret_cast<float *>(ws + w.o_off), reinterpret_cast<float *>(ws + w.lse_off),
       static_cast<__half *>(out), lse, dev_error);
   if (st != K16V8_OK) return st;
   // Few segments are cut by many CTAs each (61 for one sequence of 128K and 10 heads),
@@ -738,6 +757,6 @@ extern "C" int32_t k16v8_paged_decode_attention_k8v8(
   // 58.2 and 63.5; 32 x 1K 21.2 and 19.8, 256 x 0.5K 55.4 and 49.9.
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return batch * num_kv_heads <= 64
-             ? decode8::launch_merge<4>(batch, num_kv_heads, ws, o_off, lse_off, out, lse, s)
-             : decode8::launch_merge<1>(batch, num_kv_heads, ws, o_off, lse_off, out, lse, s);
+             ? decode8::launch_merge<4>(batch, num_kv_heads, ws, w, out, lse, s)
+             : decode8::launch_merge<1>(batch, num_kv_heads, ws, w, out, lse, s);
 }

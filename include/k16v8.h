@@ -756,7 +756,9 @@ int32_t k16v8_rope_axes_kv_append(
  *                as in k16v8_rope_axes_kv_append (num_qo_heads = 0: K and V only)
  *   rotary_dim   0 or a multiple of 16 up to head_dim; 0: positions, pair_axis
  *                and inv_freq are not read
- *   qo_indptr    device int32 [batch+1]
+ *   qo_indptr    device int32 [batch+1], not decreasing (where it does, the
+ *                sequence flags K16V8_DEVERR_SEQLEN and rows of others may be
+ *                left out)
  *   seq_lens     device int32 [batch], the new tokens included
  *   block_table  device int32 [batch][max_pages_per_seq]; only entries of pages
  *                that get rows are read.  A page that gets rows belongs to one
@@ -780,6 +782,8 @@ int32_t k16v8_rope_kv_append_k8v8(
  * paged_decode_attention_k8v8 -- k16v8_paged_decode_attention_balanced over the
  * K8/V8 cache: one query row per sequence, every position of it seen.
  *   sm_scale   finite, >= 0
+ *   block_table  device int32 [batch][max_pages_per_seq] (may be NULL where that
+ *              is 0)
  *   workspace  k16v8_decode_workspace_size_k8v8(...) bytes, 256-B aligned, needs
  *              no initialisation; calls that overlap on the GPU, replays of
  *              captured ones too, must not share one
