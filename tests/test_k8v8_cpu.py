@@ -86,3 +86,34 @@ def decode(lib, **kw):
     (dict(ws=X + 128), 1), (dict(out=X + 8), 1), (dict(sc=X + 4), 1), (dict(lse=X + 2), 1), (dict(B=0), 0)])
 def test_decode_refusals(lib, kw, status):
     assert decode(lib, **kw) == status
+
+
+def attention(lib, name, **kw):
+    a = dict(q=X, indptr=X, T=8, max_q=8, kc=X, vc=X, sc=X, table=X, maxp=4, lens=X, max_len=64, B=2, hq=8,
+             hkv=2, d=128, P=4, scale=0.1, ws=X, wb=1 << 30, out=X, lse=X, err=None, stream=None)
+    a.update(kw)
+    return getattr(lib, name)(*a.values())
+
+
+@pytest.mark.parametrize("name", ["k16v8_paged_prefill_attention_k8v8", "k16v8_paged_cross_attention_k8v8"])
+@pytest.mark.parametrize("kw,status", [
+    (dict(d=64), 2), (dict(hq=6), 2), (dict(hq=16), 2), (dict(hq=0), 1), (dict(hkv=0), 1),
+    (dict(hq=16384, hkv=4096), 1), (dict(max_q=-1), 1), (dict(T=-1), 1), (dict(B=-1), 1), (dict(B=8193), 1),
+    (dict(P=0), 1), (dict(P=1 << 26), 1), (dict(maxp=-1), 1), (dict(max_len=-1), 1), (dict(max_len=65), 1),
+    (dict(max_len=(1 << 30) + 1, maxp=1 << 27), 1), (dict(scale=-0.1), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(q=None), 1), (dict(indptr=None), 1), (dict(kc=None), 1),
+    (dict(vc=None), 1), (dict(sc=None), 1), (dict(table=None), 1), (dict(lens=None), 1), (dict(ws=None), 1),
+    (dict(out=None), 1), (dict(ws=X + 128), 1), (dict(q=X + 8), 1), (dict(kc=X + 8), 1), (dict(vc=X + 8), 1),
+    (dict(out=X + 8), 1), (dict(sc=X + 4), 1), (dict(lse=X + 2), 1), (dict(indptr=X + 2), 1),
+    (dict(lens=X + 2), 1), (dict(table=X + 2), 1), (dict(B=0), 0), (dict(T=0), 0), (dict(max_q=0), 0)])
+def test_attention_refusals(lib, name, kw, status):
+    assert attention(lib, name, **kw) == status
+
+
+def test_workspace_sizes_of_refused_calls(lib):
+    assert lib.k16v8_attention_workspace_size_k8v8(-1, 8, 2, 128) == 0
+    assert lib.k16v8_attention_workspace_size_k8v8(8, 8, 2, 64) == 0
+    assert lib.k16v8_attention_workspace_size_k8v8(8, 9, 2, 128) == 0
+    assert lib.k16v8_decode_workspace_size_k8v8(-1, 8, 128) == 0
+    assert lib.k16v8_decode_workspace_size_k8v8(8193, 8, 128) == 0
+    assert lib.k16v8_decode_workspace_size_k8v8(1, 8, 64) == 0
