@@ -101,11 +101,11 @@ static inline bool pack_axes(const int8_t *pair_axis, int32_t pairs, int32_t cou
 // Token t's positions [count][num_tokens] are all in range.
 __device__ __forceinline__ bool positions_ok(const int32_t *positions, int64_t num_tokens,
                                              int32_t count, int64_t t) {
-  bool ok = true;
-  for (int a = 0; a < count; ++a)
-    ok &= static_cast<uint32_t>(__ldg(positions + a * num_tokens + t)) <
-          static_cast<uint32_t>(kMaxPosition);
-  return ok;
+  uint32_t top = 0;
+#pragma unroll
+  for (int a = 0; a < K16V8_MAX_ROPE_AXES; ++a)
+    if (a < count) top |= static_cast<uint32_t>(__ldg(positions + a * num_tokens + t));
+  return top < static_cast<uint32_t>(kMaxPosition);
 }
 
 }  // namespace rope
