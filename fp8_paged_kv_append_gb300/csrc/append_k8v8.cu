@@ -24,10 +24,11 @@
 // and some KV heads (with their share of the query heads) and shares the
 // cosines and sines of the page's tokens.
 //
-// HBM-bound where there are many tokens: 45.0 us for 8,192 bf16 tokens of 40 + 10
-// heads, 5.1 TB/s of the bytes it cannot do without (0.75 of the copy rate), 36.8
-// for 4,096 fp32 ones (0.74).  A step of 32 sequences takes 5.0 us, one launch
-// with four dependent loads (rows, table entry, positions, held scale).
+// HBM-bound where there are many tokens: 41.7 us for 8,192 bf16 tokens of 40 + 10
+// heads, 5.5 TB/s of the bytes it cannot do without (0.81 of the copy rate; without
+// rotation 37.3, 0.91), 34.6 for 4,096 fp32 ones (0.76).  A step of 32 sequences
+// takes 5.0 us, one launch with four dependent loads (rows, table entry, positions,
+// held scale).
 #include "k8v8_device.cuh"
 #include "rope_device.cuh"
 
@@ -43,9 +44,10 @@ using rope::widen8;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-// 16-bit rows: 80 registers and 24 warps per SM, 45.4 us for 8,192 tokens of 40 + 10
-// heads (5: 46.7, 7: 47.6; the turned rows kept in registers, 128 of them: 49.8).
-// fp32 rows take 164 (2 to 4 per SM alike: 36.8 us for 4,096 tokens).
+// 16-bit rows: 80 registers and 24 warps per SM, 41.7 us for 8,192 tokens of 40 + 10
+// heads (5: 43.5, 7: 44.2; the turned rows kept in registers, 128 of them, 4 us more;
+// the next task's rows loaded into each unit's registers as it is stored 48.0).  fp32
+// rows take 164 (2 to 4 per SM alike).
 template <typename T>
 constexpr int kCtasPerSm = sizeof(T) == 2 ? 6 : 3;
 constexpr int kUnits = kPage * kUnitsPerRow / 32;  // of a lane and task
@@ -226,11 +228,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<T>) append_k8v8_kernel(co
     const uint32_t live = __ballot_sync(kFull, ok);
     if (lane == 0) s_live = live;
   }
-  for (int i = tid; i < rows * half; i += kThreads) {
-    const int t = i / half, f = i - t * half;
-    const int32_t pos = __ldg(a.positions + static_cast<int64_t>(a.axes[f]) * a.num_tokens + t0 + t);
-    table[t * half + ((f & 7) >> 1) * (half >> 2) + (f >> 3) * 2 + (f & 1)] =
-        rope::turn(pos, __ldg(a.inv_freq + f), a.factor);
+  if (half > 0) {  // a thread's frequency stays (half <= 64: a pass takes two tokens or more)
+    const int per_pass = kThreads / half, f = tid % half;
+    if (tid < per_pass * half) {
+      const int32_t *pos = a.positions + static_cast<int64_t>(a.axes[f]) * a.num_tokens + t0;
+      const float freq = __ldg(a.inv_freq + f);
+      float2 *to = table + ((f & 7) >> 1) * (half >> 2) + (f >> 3) * 2 + (f & 1);
+#pragma unroll 2
+      for (int t = tid / half; t < rows; t += per_pass)
+        to[t * half] = rope::turn(__ldg(pos + t), freq, a.factor);
+    }
   }
   __syncthreads();
   const uint32_t live = s_live;
@@ -342,8 +349,8 @@ static int32_t launch(const Args &a, cudaStream_t stream) {
   const int sms = k16v8_sm_count();
   if (sms <= 0) return K16V8_ERR_CUDA;
   // Two KV heads share a table where there are pages enough.  Two and one: 8,192 bf16
-  // tokens 45.1 and 56.3 us, 64 x 64 fp16 21.4 and 25.2; 5 x 311 fp32 of 2 heads (210
-  // items) 7.8 and 6.8.
+  // tokens 41.7 and 48.7 us, 64 x 64 fp16 20.5 and 22.5; 5 x 311 fp32 of 2 heads (210
+  // items) 7.7 and 6.6.  (Three to five: 44 to 51 for the first.)
   const int kv_per_cta = items * a.hkv >= 8LL * sms ? 2 : 1;
   const int parts = (a.hkv + kv_per_cta - 1) / kv_per_cta;
   const int q_per_cta = (a.hq + parts - 1) / parts;
