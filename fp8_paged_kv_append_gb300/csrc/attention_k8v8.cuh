@@ -27,10 +27,10 @@
 // would take the codes as they are, but wants one scale for all positions of P V
 // and P itself in e4m3: 2^-4 of a weight instead of 2^-11.)
 //
-// Warp roles (16 warps): 0-3 / 4-7 softmax of slot 0 / 1, one thread per row; 8,
-// 10 widen keys, 11, 14 values; 9 / 15 issue the MMAs of slot 0 / 1; 13 loads Q
-// (TMA) and key pages; 12 loads value pages, walks the CTA's pieces and hands them
-// to the others.  Every hand-off is an mbarrier, every wait is bounded.
+// Warp roles (16 warps): 0-3 / 4-7 softmax of slot 0 / 1, one thread per row; 9 / 13
+// issue the MMAs of slot 0 / 1; 10, 11 widen keys, 14, 15 values; 12 loads Q (TMA)
+// and key pages; 8 loads value pages, walks the CTA's pieces and hands them to the
+// others.  Every hand-off is an mbarrier, every wait is bounded.
 //
 // What bounds it.  With two row tiles: the chain S -> maximum -> exponentials -> P V,
 // 2,140 cycles a unit in long pieces where the MMAs take 1,270 at the cuBLAS rate,
@@ -64,17 +64,15 @@ constexpr int kRows = kTileTokens * kGroup;  // 128
 constexpr int kHalf = kKv / 2;               // positions of a half tile
 constexpr int kPagesPerHalf = kHalf / kPage; // 4
 constexpr int kThreads = 512;
-constexpr int kMmaWarp0 = 9, kMmaWarp1 = 15, kLoadVWarp = 12, kLoadKWarp = 13;
+// Warps i, i + 4, .. share a scheduler.  The loads' warps share one, the MMAs' another,
+// a widening warp of keys and one of values each of the others: 8 x 1024 122.3 us (with
+// a widening warp beside an MMA warp 127 to 137, loads beside the MMAs or the widening
+// 125.7), 8 rows at 128K 113.6 (with widening beside softmax warp 0, which has all the
+// rows then, 122 to 123).
+constexpr int kMmaWarp0 = 9, kMmaWarp1 = 13, kLoadVWarp = 8, kLoadKWarp = 12;
 constexpr int kWidenWarps = 2;               // for keys, and for values
 constexpr int kPieceRing = 4;
 constexpr int kPieceReaders = 16;            // every warp
-// From this many KV tiles on, the slots of two row tiles exponentiate in turn, so that
-// one's exponentials run under the other's MMAs instead of both waiting for both.
-// 1,024 rows of 8,192 (64 tiles) 158.8 -> 142.7 us, 16 x 448 over 1,500 (12 tiles)
-// 186.6 -> 177.8.  In short pieces it only delays a slot: always, 8 x 1024 (1 to 8)
-// 132.1 -> 134.1 and 64 x 40 of 300 42.4 -> 43.6; from 5 or 9 on, 1 x 4,000 191.7 ->
-// 195.5 and 202.2.
-constexpr int kTurnTiles = 3;
 constexpr int kKTiles = 2;                   // fp16 tiles of keys
 constexpr int kVHalves = 3;                  // fp16 half tiles of values
 
@@ -85,7 +83,7 @@ constexpr uint32_t kVBytes = 2 * kVBlk;
 constexpr uint32_t kKBlk = kKv * 128;        // [128 pos][64 dims] fp16
 constexpr uint32_t kKBytes = 2 * kKBlk;
 // registers, together what the block was launched with; 136 + 120 and 152 + 104 are
-// both 1 us slower in 130 (the first spills in softmax, the second in the others)
+// 0.5% slower or no faster
 constexpr int kSoftmaxRegs = 144, kOtherRegs = 112;
 static_assert(kSoftmaxRegs + kOtherRegs == 2 * (65536 / kThreads), "two warpgroups each");
 
@@ -498,7 +496,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       const int after = two ? 0 : w ^ pc.turn;  // the slot's first tile
       const int mine = two ? pc.tiles : (pc.tiles + 1 - after) / 2;
       const int n_tiles = pc.tiles, d0 = pc.base - pc.t0 * kKv;
-      const bool in_turn = two && pc.tiles >= kTurnTiles;
       const int theirs = two ? 0 : (pc.tiles + after) / 2;  // units of the other slot to join
       float m_used = -INFINITY, l = 0.f;
       for (int k = 0; k < mine; ++k, ++units) {
@@ -511,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             arrive(bar0 + 8 * (kBarPFull + w));
             if (parts > 1) arrive(bar0 + 8 * (kBarPFull + w + 2));
           }
-          if (in_turn) {
+          if (two) {
             ok = __all_sync(kFull, wait(kBarTurn + w, (turns++ + 1 - w) & 1));
             if (!ok) break;
             if (lane == 0) arrive(bar0 + 8 * (kBarTurn + (w ^ 1)));
@@ -581,7 +578,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             tc::tmem_st32(tO + lane_base + c * 32, o);
           }
         }
-        if (in_turn) {
+        // The slots of two row tiles exponentiate in turn, one under the other's MMAs,
+        // or both would wait for both.  1,024 rows of 8,192 158.8 -> 143 us, 16 x 448
+        // over 1,500 186.6 -> 178, 4,000 rows 201 -> 190; 64 x 40 of 300 42.6 -> 43.2.
+        if (two) {
           ok = __all_sync(kFull, wait(kBarTurn + w, (turns++ + 1 - w) & 1));
           if (!ok) break;
         }
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
             hand_over(part);
           }
         }
-        if (in_turn && lane == 0) arrive(bar0 + 8 * (kBarTurn + (w ^ 1)));
+        if (two && lane == 0) arrive(bar0 + 8 * (kBarTurn + (w ^ 1)));
         l = l * alpha + (ps2.x + ps2.y);
       }
       if (!ok) break;
@@ -740,11 +740,11 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       ring.next(kPieceRing);
     }
     pdl_launch_dependents();
-  } else if (warp == 8 || warp == 10 || warp == 11 || warp == 14) {
+  } else if (warp & 2) {
     // ================= codes to fp16: two warps for keys, two for values =================
     // (one code for both: the instruction cache holds little more than the roles' loops)
-    const bool is_v = warp & 1 || warp == 14;
-    const Lanes at(warp == 10 || warp == 14, lane, is_v ? kVBlk : kKBlk);
+    const bool is_v = warp & 4;
+    const Lanes at(warp & 1, lane, is_v ? kVBlk : kKBlk);
     const int bar_staged = is_v ? kBarVstFull : kBarKstFull, bar_read = is_v ? kBarVstEmpty : kBarKstEmpty;
     const int bar_full = is_v ? kBarVFull : kBarKFull, bar_empty = is_v ? kBarVEmpty : kBarKEmpty;
     const uint8_t *stages = is_v ? sVst : sKst;
