@@ -418,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
     tc::tmem_alloc(tmem_slot, kTmemCols);
     tc::tmem_relinquish();
   }
-  if (tid == 32) {
-    for (int i = 0; i < kNumBars; ++i) {
+  if (warp == 1) {
+    for (int i = lane; i < kNumBars; i += 32) {
       uint32_t count = 1;
       if ((i >= kBarKstFull && i < kBarKstEmpty) || (i >= kBarVstFull && i < kBarVstEmpty)) count = 33;
       if ((i >= kBarKstEmpty && i < kBarVstFull) || (i >= kBarVstEmpty && i < kBarKEmpty))
@@ -432,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
       if (i >= kBarTaken && i < kBarDrain) count = kPieceReaders;
       mbar_init(&bars[i], count);
     }
-    *abort_flag = 0;
+    if (lane == 0) *abort_flag = 0;
     fence_barrier_init();
   }
   pdl_wait();
@@ -569,13 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         // (S was issued behind the slot's P V so far: O is at rest)
         if (k > 0 && __any_sync(kFull, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tc::tmem_ld32(tO + lane_base + c * 32, o);
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tc::tmem_ld16(tO + lane_base + c * 16, o);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st32(tO + lane_base + c * 32, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st16(tO + lane_base + c * 16, o);
           }
         }
         // The slots of two row tiles exponentiate in turn, one under the other's MMAs,
