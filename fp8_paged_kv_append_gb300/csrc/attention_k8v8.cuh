@@ -32,23 +32,28 @@
 // and key pages; 8 loads value pages, walks the CTA's pieces and hands them to the
 // others.  Every hand-off is an mbarrier, every wait is bounded.
 //
-// What bounds it.  With two row tiles: the chain S -> maximum -> exponentials -> P V,
-// 2,140 cycles a unit in long pieces where the MMAs take 1,270 at the cuBLAS rate,
-// and in short ones the start and end of a piece: 1,024 rows of 8,192 143 us (1.13
-// PFLOP/s, 0.59 of that rate), 8 x 1024 causal 132 us (651 TFLOP/s), 16 x 448 rows
-// over 1,500 178 us (696).  With one row tile: the hand-offs from loads to widening
-// to MMAs (time stamps show no role busy for much more than half of the time); 8
-// rows at 128K 116 us (2.9 TB/s of codes, 0.43 of the copy rate), 5 rows over 1,500
-// 13.3 us, nearly all of it the latency of one piece and the merge.
+// What bounds it.  With two row tiles: hand-offs and shared memory, not arithmetic.
+// 1,024 rows of 8,192 take 143 us (1.13 PFLOP/s, 0.59 of the cuBLAS rate, tensor pipe
+// 51% active), 2,140 cycles a unit, in which operands, codes and widened tiles move
+// some 160 KB through shared memory (1,280 cycles); without the exponentials' ex2 it
+// is 140, without the row maxima 142, without the widening's arithmetic 138.  In short
+// pieces their starts and ends come to that: 8 x 1024 causal 121.5 us (708 TFLOP/s),
+// 16 x 448 rows over 1,500 171.5 us (722).  With one row tile: the widening warps, at
+// work 0.6 of the time, and the hand-offs on either side of them: 8 rows at 128K 114
+// us (2.9 TB/s of codes, 0.43 of the copy rate); 5 rows over 1,500 13.2 us, nearly all
+// of it the latency of one piece and the merge.
 // Code size matters throughout: the roles' loops together are about as large as
 // the instruction cache near the SM, and every variant below that added code lost
 // more than it won.
 // Measured and left out (us, against what was kept at the time): a thread's 128
 // scores held in registers between maximum and exponentials (156 / 133: 56
-// registers are left to the other roles), an epilogue that turns rows through
-// shuffles (151 / 146), widening by four warps per side instead of two, as
-// neighbouring rows or as alternate halves (122 / 116 for 8 rows at 128K), a ring
-// of codes and fp16 tiles for either slot (127 / 116).
+// registers are left to the other roles), two warps to a row with 64 scores each
+// (145 / 121.5: exchanging the maxima takes 500 cycles a unit), an epilogue that turns
+// rows through shuffles (151 / 146) or tensor memory (144 / 132) to fill the lines it
+// stores, queries loaded without holding up the key tiles behind them (132 / 122),
+// widening by four warps per side instead of two, as neighbouring rows or as
+// alternate halves (122 / 116 for 8 rows at 128K), a ring of codes and fp16 tiles for
+// either slot (127 / 116).
 #pragma once
 
 #include "k16v8_device.cuh"
