@@ -27,8 +27,10 @@
 // HBM-bound where there are many tokens: 41.7 us for 8,192 bf16 tokens of 40 + 10
 // heads, 5.5 TB/s of the bytes it cannot do without (0.81 of the copy rate; without
 // rotation 37.3, 0.91), 34.6 for 4,096 fp32 ones (0.76).  A step of 32 sequences
-// takes 5.0 us, one launch with four dependent loads (rows, table entry, positions,
-// held scale).
+// takes 4.8 us, one launch with four dependent loads (rows, table entry, positions,
+// held scale), of 8,192 66 (0.51 of the copy rate).
+#include <algorithm>
+
 #include "k8v8_device.cuh"
 #include "rope_device.cuh"
 
@@ -46,10 +48,11 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 // 16-bit rows: 80 registers and 24 warps per SM, 41.7 us for 8,192 tokens of 40 + 10
 // heads (5: 43.5, 7: 44.2; the turned rows kept in registers, 128 of them, 4 us more;
-// the next task's rows loaded into each unit's registers as it is stored 48.0).  fp32
-// rows take 164 (2 to 4 per SM alike).
-template <typename T>
-constexpr int kCtasPerSm = sizeof(T) == 2 ? 6 : 3;
+// the next task's rows loaded into each unit's registers as it is stored 48.0); steps
+// spill in 80 (256 sequences 5.6 us, with 6 5.8).  fp32 rows take 164 (2 to 4 per SM
+// alike).
+template <typename T, bool kStep>
+constexpr int kCtasPerSm = sizeof(T) == 2 ? (kStep ? 5 : 6) : 3;
 constexpr int kUnits = kPage * kUnitsPerRow / 32;  // of a lane and task
 
 struct Args {
@@ -128,52 +131,71 @@ __device__ __forceinline__ uint32_t rescaled(uint32_t w, float ratio) {
          (static_cast<uint32_t>(e4m3x2_from_f32(b.x * ratio, b.y * ratio)) << 16);
 }
 
-// grid: (pages that sequences may write, an upper bound; parts of the heads).
-template <typename T, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<T>) append_k8v8_kernel(const Args a, int kv_per_cta,
-                                                               int q_per_cta) {
+// Items: the pages that sequences may write, an upper bound.  Those of sequence b start
+// at item
+//   qo_indptr[b] / 16 + 2b  -- room for every page that its rows can touch, or
+//   qo_indptr[b]            -- kStep: a page per token, for calls of about one each.
+template <bool kStep>
+__device__ __forceinline__ int first_item(const Args &a, int b) {
+  const int q0 = __ldg(a.qo_indptr + b);
+  return kStep ? q0 : (q0 >> 4) + 2 * b;
+}
+
+// grid: (items; parts of the heads).  kStep: a part is kStepTasks tasks, which pages of
+// one new row take at once, 8 lanes each.
+constexpr int kStepTasks = kWarps * 4 * kUnits;
+
+template <typename T, bool kInterleaved, bool kStep>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<T, kStep>)
+    append_k8v8_kernel(const Args a, int kv_per_cta, int q_per_cta) {
   extern __shared__ __align__(16) float2 table[];  // pair 8c + 2i + e of a token at [i][c][e]
-  __shared__ int s_last[kWarps];
-  __shared__ int s_seq[3][kThreads];  // q0, n, L of the first sequences
+  __shared__ int s_last[2][kWarps];
+  __shared__ int s_seq[3][kThreads];  // q0, n, L of the sequences looked at
   __shared__ uint32_t s_live;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int item = blockIdx.x;
   pdl_wait();
   pdl_launch_dependents();
 
-  // Items of sequence b start at qo_indptr[b] / 16 + 2b, which leaves room for
-  // every page that its rows can touch: the item's sequence is the last (of those
-  // in range) that starts at or before it.
-  int last = -1;
-  for (int b = tid; b < a.batch; b += kThreads) {
+  if (blockIdx.y == 0 && item <= a.batch / kThreads && item * kThreads + tid < a.batch) {
     int q0, n, L;
-    const bool ok = sequence(a, b, q0, n, L);
-    if (!ok && item == 0 && blockIdx.y == 0) flag_error(a.dev_error, K16V8_DEVERR_SEQLEN);
-    if (ok && (q0 >> 4) + 2 * b <= item) last = b;
-    if (b < kThreads) {
-      s_seq[0][b] = q0;
-      s_seq[1][b] = n;
-      s_seq[2][b] = L;
-    }
+    if (!sequence(a, item * kThreads + tid, q0, n, L)) flag_error(a.dev_error, K16V8_DEVERR_SEQLEN);
   }
-  last = __reduce_max_sync(kFull, last);
-  if (lane == 0) s_last[warp] = last;
-  __syncthreads();
-  int b = -1;
+  // The item's sequence is the last (of those in range) that starts at or before it: by
+  // the start alone down to as many as there are threads, then among those in range.
+  int low = 0, count = a.batch, round = 0;
+  auto last_of = [&](bool before) {  // the last thread for which it holds, -1: none
+    const int mine = __reduce_max_sync(kFull, before ? tid : -1);
+    if (lane == 0) s_last[round & 1][warp] = mine;
+    __syncthreads();
+    int last = -1;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) b = max(b, s_last[w]);
-  if (b < 0) return;
-  int q0, n, L;
-  if (b < kThreads) {
-    q0 = s_seq[0][b];
-    n = s_seq[1][b];
-    L = s_seq[2][b];
-  } else {
-    sequence(a, b, q0, n, L);
+    for (int w = 0; w < kWarps; ++w) last = max(last, s_last[round & 1][w]);
+    ++round;
+    return last;
+  };
+  while (count > kThreads) {
+    const int step = (count + kThreads - 1) / kThreads, at = tid * step;
+    const int last = last_of(at < count && first_item<kStep>(a, low + at) <= item);
+    if (last < 0) return;
+    low += last * step;
+    count = min(step, count - last * step);
   }
+  bool before = false;
+  if (tid < count) {
+    int q0, n, L;
+    before = sequence(a, low + tid, q0, n, L) && first_item<kStep>(a, low + tid) <= item;
+    s_seq[0][tid] = q0;
+    s_seq[1][tid] = n;
+    s_seq[2][tid] = L;
+  }
+  const int at = last_of(before);
+  if (at < 0) return;
+  const int b = low + at;
+  const int q0 = s_seq[0][at], n = s_seq[1][at], L = s_seq[2][at];
   if (n == 0) return;
   const int first = L - n;  // the first new position
-  const int page = first / kPage + (item - (q0 >> 4) - 2 * b);
+  const int page = first / kPage + (item - (kStep ? q0 : (q0 >> 4) + 2 * b));
   if (page > (L - 1) / kPage || page < first / kPage) return;
   const int p0 = max(page * kPage, first), p1 = min(page * kPage + kPage, L);
   const int rows = p1 - p0, lo = p0 - page * kPage;  // new rows, from this offset on
@@ -181,18 +203,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<T>) append_k8v8_kernel(co
   const int pid = __ldg(a.block_table + static_cast<int64_t>(b) * a.maxp + page);
 
   // Tasks: keys and values of the part's KV heads, then its query heads.
-  const int h0 = blockIdx.y * kv_per_cta, nh = min(kv_per_cta, a.hkv - h0);
-  const int qh0 = blockIdx.y * q_per_cta, nq = max(0, min(q_per_cta, a.hq - qh0));
-  const int tasks = 2 * max(nh, 0) + nq;
+  const int h0 = kStep ? 0 : blockIdx.y * kv_per_cta, nh = min(kStep ? a.hkv : kv_per_cta, a.hkv - h0);
+  const int qh0 = kStep ? 0 : blockIdx.y * q_per_cta;
+  const int nq = max(0, min(kStep ? a.hq : q_per_cta, a.hq - qh0));
+  const int all = 2 * max(nh, 0) + nq;
+  // of this warp
+  const int task0 = kStep ? blockIdx.y * kStepTasks + warp * (kStepTasks / kWarps) : warp;
+  const int task1 = kStep ? min(all, task0 + kStepTasks / kWarps) : all;
+  const int stride = kStep ? 1 : kWarps;
   const int half = a.rotary >> 1;
   const int c = lane % kUnitsPerRow, r0 = lane / kUnitsPerRow;  // rows r0, r0 + 4, ...
   const bool turned_unit = 16 * c < a.rotary;
 
   Raw<T> raw[kUnits];
-  auto load = [&](int task) {
+  // row 0 of a task's 16 dims c (and, where a pair's halves are apart, their partners)
+  auto rows_of = [&](int task, const T *&src, int64_t &ts, bool &apart) {
     const bool is_v = task >= nh && task < 2 * nh;
-    const T *src;
-    int64_t ts;
     if (task < nh) {
       src = static_cast<const T *>(a.k) + (h0 + task) * kHeadDim;
       ts = a.k_ts;
@@ -203,7 +229,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<T>) append_k8v8_kernel(co
       src = static_cast<const T *>(a.q) + (qh0 + task - 2 * nh) * kHeadDim;
       ts = a.q_ts;
     }
-    const bool apart = !kInterleaved && !is_v && turned_unit;
+    apart = !kInterleaved && !is_v && turned_unit;
+  };
+  auto load = [&](int task) {
+    const T *src;
+    int64_t ts;
+    bool apart;
+    rows_of(task, src, ts, apart);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int r = r0 + 4 * i;
@@ -213,7 +245,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<T>) append_k8v8_kernel(co
       load8(p + (apart ? 8 * c + half : 16 * c + 8), raw[i].w + sizeof(T) / 2);
     }
   };
-  if (warp < tasks) load(warp);
+  const bool single = kStep && rows == 1;  // unit i of a lane: task task0 + 4i + r0
+  if (single) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      if (task0 + 4 * i + r0 >= task1) continue;
+      const T *src;
+      int64_t ts;
+      bool apart;
+      rows_of(task0 + 4 * i + r0, src, ts, apart);
+      src += t0 * ts;
+      load8(src + (apart ? 8 : 16) * c, raw[i].w);
+      load8(src + (apart ? 8 * c + half : 16 * c + 8), raw[i].w + sizeof(T) / 2);
+    }
+  } else if (task0 < task1) {
+    load(task0);
+  }
   if (pid < 0 || pid >= a.num_pages) {
     if (tid == 0 && blockIdx.y == 0) flag_error(a.dev_error, K16V8_DEVERR_PAGE);
     return;
@@ -243,8 +290,66 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<T>) append_k8v8_kernel(co
   const uint32_t live = s_live;
   if (live == 0) return;
 
-  for (int task = warp; task < tasks; task += kWarps) {
-    if (task != warp) load(task);
+  if (single) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int task = task0 + 4 * i + r0;
+      const bool is_v = task >= nh && task < 2 * nh, turns = !is_v && turned_unit;
+      const bool apart = !kInterleaved && turns, on = task < task1;
+      float x[8], y[8], top = 0.f;
+      if (on) {
+        widen8(raw[i].w, x, static_cast<const T *>(nullptr));
+        widen8(raw[i].w + sizeof(T) / 2, y, static_cast<const T *>(nullptr));
+        if (turns) turn_unit<kInterleaved>(x, y, reinterpret_cast<const float4 *>(table) + c, half);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float ax = fabsf(x[e]), ay = fabsf(y[e]);
+          top = fmaxf(top, fmaxf(ax < INFINITY ? ax : 0.f, ay < INFINITY ? ay : 0.f));
+        }
+      }
+#pragma unroll
+      for (int o = kUnitsPerRow / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      const bool cached = on && task < 2 * nh;
+      const int64_t tile = static_cast<int64_t>(pid) * a.hkv + (is_v ? task - nh : task);
+      float *scale = a.kv_scale + tile * 2 + (is_v ? 1 : 0);
+      const float held = cached && lo > 0 ? *scale : 0.f;
+      __syncwarp();  // every lane of the row has read the old scale
+      if (on && !cached) {
+        __half *dst = a.q_out + (t0 * a.hq + task - 2 * nh) * kHeadDim;
+        *reinterpret_cast<uint4 *>(dst + (apart ? 8 : 16) * c) = narrow8(x);
+        *reinterpret_cast<uint4 *>(dst + (apart ? 8 * c + half : 16 * c + 8)) = narrow8(y);
+      }
+      if (!cached) continue;
+      uint8_t *codes = (is_v ? a.v_cache : a.k_cache) + tile * k8v8::kTileBytes;
+      int e = k8v8::scale_exponent(top);
+      if (lo > 0) {
+        e = max(e, k8v8::stored_exponent(held));
+        const float ratio = held / k8v8::exp2_int(e);
+        if (ratio != 1.f) {
+          for (int r = 0; r < lo; ++r) {
+            uint4 *p = reinterpret_cast<uint4 *>(codes + r * kHeadDim) + c;
+            const uint4 w = *p;
+            *p = make_uint4(rescaled(w.x, ratio), rescaled(w.y, ratio), rescaled(w.z, ratio),
+                            rescaled(w.w, ratio));
+          }
+        }
+      }
+      if (c == 0) *scale = k8v8::exp2_int(e);
+      const float inv = k8v8::exp2_int(-e);
+      uint8_t *dst = codes + lo * kHeadDim;
+      const uint2 cx = codes8(x, inv), cy = codes8(y, inv);
+      if (apart) {
+        *reinterpret_cast<uint2 *>(dst + 8 * c) = cx;
+        *reinterpret_cast<uint2 *>(dst + 8 * c + half) = cy;
+      } else {
+        *reinterpret_cast<uint4 *>(dst + 16 * c) = make_uint4(cx.x, cx.y, cy.x, cy.y);
+      }
+    }
+    return;
+  }
+
+  for (int task = task0; task < task1; task += stride) {
+    if (task != task0) load(task);
     const bool is_k = task < nh, is_v = !is_k && task < 2 * nh;
     const bool turns = !is_v && turned_unit;
     const bool apart = !kInterleaved && turns;
@@ -345,17 +450,28 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<T>) append_k8v8_kernel(co
 
 template <typename T, bool kInterleaved>
 static int32_t launch(const Args &a, cudaStream_t stream) {
-  const int64_t items = a.num_tokens / kPage + 2LL * a.batch;
   const int sms = k16v8_sm_count();
   if (sms <= 0) return K16V8_ERR_CUDA;
+  const size_t smem = static_cast<size_t>(kPage) * (a.rotary / 2) * sizeof(float2);
+  const int checks = (a.batch + kThreads - 1) / kThreads;  // CTAs that look for bad sequences
+  // Calls of about a token per sequence: a CTA holds all heads of a token's page.  So and
+  // by pages with parts of the heads: 32 sequences 4.8 and 5.1 us, 256 5.6 and 12.0, 1,024
+  // 13.2 and 42, 8,192 66 and 321; two tokens each, where its rows wait for one another,
+  // 256 26.7 and 13.8, 1,024 53 and 46.
+  if (4LL * a.num_tokens <= 5LL * a.batch) {
+    const int parts = (2 * a.hkv + a.hq + kStepTasks - 1) / kStepTasks;
+    return k16v8_launch_pdl(append_k8v8_kernel<T, kInterleaved, true>,
+                            dim3(static_cast<unsigned>(std::max(a.num_tokens, checks)), parts),
+                            dim3(kThreads), smem, stream, a, 0, 0);
+  }
+  const int64_t items = a.num_tokens / kPage + 2LL * a.batch;
   // Two KV heads share a table where there are pages enough.  Two and one: 8,192 bf16
   // tokens 41.7 and 48.7 us, 64 x 64 fp16 20.5 and 22.5; 5 x 311 fp32 of 2 heads (210
   // items) 7.7 and 6.6.  (Three to five: 44 to 51 for the first.)
   const int kv_per_cta = items * a.hkv >= 8LL * sms ? 2 : 1;
   const int parts = (a.hkv + kv_per_cta - 1) / kv_per_cta;
   const int q_per_cta = (a.hq + parts - 1) / parts;
-  const size_t smem = static_cast<size_t>(kPage) * (a.rotary / 2) * sizeof(float2);
-  return k16v8_launch_pdl(append_k8v8_kernel<T, kInterleaved>,
+  return k16v8_launch_pdl(append_k8v8_kernel<T, kInterleaved, false>,
                           dim3(static_cast<unsigned>(items), parts), dim3(kThreads), smem, stream,
                           a, kv_per_cta, q_per_cta);
 }

@@ -232,6 +232,48 @@ def test_append_steps(K, batch):
     run_append(K, rng, [1] * batch, [int(x) for x in rng.integers(0, 100, batch)], 2, 64, 1, False, "fp16")
 
 
+def many_counts(kind, rng):
+    counts = rng.integers(0, 2, 300) if kind != "few each" else rng.integers(0, 6, 300)
+    if kind == "a long one":
+        counts[170], counts[171] = 40, 2
+    if kind == "empty ends":
+        counts[:140] = counts[250:] = 0
+    return [int(n) for n in counts]
+
+
+@pytest.mark.parametrize("kind", ["at most one", "a long one", "empty ends", "few each"])
+@pytest.mark.parametrize("dtype,interleaved,hkv,hq", [("fp16", False, 1, 4), ("fp32", True, 2, 3),
+                                                      ("bf16", False, 20, 30)])
+def test_append_many_sequences(K, kind, dtype, interleaved, hkv, hq):
+    """More sequences than a CTA has threads, of no, one or a few new tokens."""
+    rng = np.random.default_rng(hkv)
+    counts = many_counts(kind, rng)
+    run_append(K, rng, counts, [int(x) for x in rng.integers(0, 40, 300)], hkv, 64, 3, interleaved, dtype,
+               pad=7, hq=hq)
+
+
+def test_append_bad_sequences_among_many(K):
+    """Lengths below their new tokens: flagged and skipped, the others written."""
+    B = 700
+    g = torch.ones((B, 3, 128), dtype=torch.float16, device=dev())
+    kc = torch.full((B, 1, 16, 128), 0x31, dtype=torch.uint8, device=dev())
+    vc, sc = kc.clone(), torch.ones((B, 1, 2), dtype=torch.float32, device=dev())
+    qo = torch.full((B, 1, 128), 7.5, dtype=torch.float16, device=dev())
+    err = torch.zeros(1, dtype=torch.int32, device=dev())
+    lens = np.full(B, 5, np.int32)
+    bad = [0, 3, 127, 128, 400, 699]
+    lens[bad] = [0, 17, -1, 0, 2 ** 31 - 1, 0]
+    K.k16v8_rope_kv_append_k8v8(g[:, :1], g[:, 1:2], g[:, 2:], to_dev(np.arange(B + 1, dtype=np.int32)), None, None,
+                                None, to_dev(np.arange(B, dtype=np.int32)[:, None]), to_dev(lens), qo, kc, vc, sc,
+                                dev_error=err)
+    assert K.k16v8_read_device_error(err) == K.DEVERR_SEQLEN
+    want = np.ones(B, bool)
+    want[bad] = False
+    touched = (kc.cpu() != 0x31).any(-1).any(1).numpy()
+    assert np.array_equal(touched[:, 4], want) and not touched[:, [0, 1, 2, 3, 5, 15]].any()
+    assert np.array_equal((qo.cpu() == 1).all(-1).all(-1).numpy(), want)
+
+
 def test_append_long(K):
     run_append(K, np.random.default_rng(1), [2000], [3], 10, 96, 3, False, "bf16", pad=1)
 
