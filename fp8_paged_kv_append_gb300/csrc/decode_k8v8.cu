@@ -11,8 +11,10 @@
 // joins the score's factor and nu the weight: no element is multiplied by one.
 //
 // The cut is that of the K16/V8 balanced decode (decode_balanced.cu): CTA i of one
-// full wave takes flat (sequence, KV head, page) tiles [i W, (i + 1) W), warps take
-// tiles in turn, and a merge joins the segments that were cut.
+// full wave takes flat (sequence, KV head, page) tiles [i W, (i + 1) W), and a merge
+// joins the segments that were cut.  A warp takes a run of its CTA's tiles and writes
+// the rows of segments that lie in it by itself; what warps share is joined once, at
+// the end.
 //
 // HBM-bound: 4,096 bytes of codes and 8 of scales per tile.  What a tile costs in
 // instructions decides whether the stream stays full (the K16/V8 kernel spends
@@ -28,9 +30,12 @@
 //    needs one vote instead of a reduction over its tokens.
 // Tiles are staged by TMA with the 128-byte swizzle: a row is 128 bytes, and the
 // lanes that read one column of 16-byte chunks would meet in the same banks.
-// Both kernels: 16 sequences of 8K 58.3 us (5.86 TB/s of the bytes it cannot do
-// without, 0.86 of the copy rate), one of 128K 58.2, 32 of up to 1K 19.7 (0.53), one
-// of 1K 7.4.  Some 7 us are fixed: plan, first loads, the cut segments' merge.
+// Both kernels: 16 sequences of 8K 59 us (5.8 TB/s of the bytes it cannot do
+// without, 0.85 of the copy rate), one of 128K 58.8, 32 of up to 1K 19.8 (0.53), one
+// of 1K 7.0, 1,024 of 100 54 (0.59), 8,192 of 40 281 (0.42).  Some 7 us are fixed:
+// plan, first loads, the cut segments' merge.  (Warps that take a CTA's tiles in turn
+// and join at the end of every segment: 7.4 us for one of 1K, 70.6 for 1,024 of 100,
+// 447 for 8,192 of 40, 0.5% less for the long ones.)
 #include <math.h>
 
 #include "k8v8_device.cuh"
@@ -95,12 +100,6 @@ __device__ __forceinline__ void tma_load_evict_first(void *dst, const CUtensorMa
 
 __device__ __forceinline__ int clamped_len(const int32_t *seq_lens, int b, int cap) {
   return max(0, min(__ldg(seq_lens + b), cap));
-}
-__device__ __forceinline__ void named_bar_sync(int id, int threads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-__device__ __forceinline__ void named_bar_arrive(int id, int threads) {
-  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // A warp's running state, lane 4g + t: heads 2t and 2t + 1 (t < 2; the padding
@@ -283,7 +282,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
   const int W = max((T + G - 1) / G, kMinTiles);
   const int a = static_cast<int>(blockIdx.x) * W;
   const int e = min(a + W, T);
-  const int n_my = e - a > warp ? (e - a - warp + kWarps - 1) / kWarps : 0;
+  // of them a run of each warp
+  const int run = e > a ? (e - a + kWarps - 1) / kWarps : 0;
+  const int aw = a + warp * run, ew = min(aw + run, e);
+  const int n_my = max(ew - aw, 0);
 
   auto segment_of = [&](int f) {  // largest b with ps[b] * hkv <= f
     int lo = 0, hi = batch;
@@ -309,7 +311,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
     scale = make_float2(0.f, 0.f);
     Segment sg = walk;
     if (k < n_my) {
-      const int f = a + warp + kWarps * k;
+      const int f = aw + k;
       if (scratch_live) {
         sg = segment_of(f);
       } else {
@@ -334,8 +336,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
   };
 
   Segment seg0{0, 0, 0, 0, 0};
-  if (a < T) {
-    seg0 = segment_of(a);
+  if (n_my > 0) {
+    seg0 = segment_of(aw);
     seg0.L = clamped_len(seq_lens, seg0.b, cap);
   }
   Segment walk = seg0;
@@ -389,13 +391,99 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
   const int g = lane >> 2, t = lane & 3;
   const float qs = sm_scale * kLog2e;
   Segment cs = seg0;  // of the current piece
-  int fc = a + warp;  // this warp's next flat tile to consume
+  int fc = aw;        // this warp's next flat tile to consume
   int kc = 0, sc = 0;
   uint32_t phase = 0;
   int fail_k = -1;    // first tile whose wait gave up
   bool ok = true;
-  int piece = 0;
-  while (true) {
+  State st;
+  // Writes the rows of segment cs: this warp's state, joined with those staged by the
+  // warps behind it up to w_end.
+  auto finish = [&](int w_end) {
+    if (t >= 2) return;
+    const bool whole = cs.s0 >= a && cs.s0 + cs.np <= e;
+    float f[kWarps][2], lse[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float M = st.m[h];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w)
+        if (w > warp && w < w_end) M = fmaxf(M, stg.m[w - 1][2 * t + h]);
+      // a warp without a finite score counts for nothing, unless its sum is NaN
+      auto factor = [&](float m, float l) {
+        return m == -INFINITY ? (l != l ? l : 0.f) : ex2(m - M);
+      };
+      f[0][h] = factor(st.m[h], st.l[h]);
+      float sum = f[0][h] * st.l[h];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        f[w][h] = 0.f;
+        if (w > warp && w < w_end) {
+          const float l = stg.l[w - 1][2 * t + h];
+          f[w][h] = factor(stg.m[w - 1][2 * t + h], l);
+          sum += f[w][h] * l;
+        }
+      }
+      const bool none = sum == 0.f;  // no live page
+      const float inv = none ? 0.f : 1.f / sum;
+      // (the lift comes off the sum, whose logarithm is most accurate near 1)
+      lse[h] = none ? -INFINITY : (M + kLift + lg2(sum * 0x1p-7f)) * kLn2;
+      static_assert(kLift == 7.f, "the factor of the sum");
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) f[w][h] *= inv;
+      f[0][h] *= st.nu;
+    }
+    float r[2][16];  // of either head
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        r[h][2 * i] = f[0][h] * st.o[i][h];
+        r[h][2 * i + 1] = f[0][h] * st.o[i][h + 2];
+      }
+    }
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) {
+      if (w <= warp || w >= w_end) continue;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 x = stg.o[w - 1][i][2 * g + t];
+        r[0][2 * i] = fmaf(f[w][0], x.x, r[0][2 * i]);
+        r[1][2 * i] = fmaf(f[w][1], x.y, r[1][2 * i]);
+        r[0][2 * i + 1] = fmaf(f[w][0], x.z, r[0][2 * i + 1]);
+        r[1][2 * i + 1] = fmaf(f[w][1], x.w, r[1][2 * i + 1]);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (whole) {
+        const int64_t row = static_cast<int64_t>(cs.b) * hq + cs.g * kGroup + 2 * t + h;
+        uint4 *po = reinterpret_cast<uint4 *>(out + row * kHeadDim + 16 * g);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __half2 x = __floats2half2_rn(r[h][8 * i + 2 * j], r[h][8 * i + 2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t *>(&x);
+          }
+          po[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        if (g == 0 && lse_out) lse_out[row] = lse[h];
+      } else {  // slot 0: of the segment that the CTA begins in
+        const int64_t row =
+            (static_cast<int64_t>(blockIdx.x) * 2 + (cs.s0 > a ? 1 : 0)) * kGroup + 2 * t + h;
+        float4 *po = reinterpret_cast<float4 *>(part_o + row * kHeadDim + 16 * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          po[i] = make_float4(r[h][4 * i], r[h][4 * i + 1], r[h][4 * i + 2], r[h][4 * i + 3]);
+        if (g == 0) part_lse[row] = lse[h];
+      }
+    }
+  };
+
+  bool lead = false;  // the warp's last segment goes on in the next warp
+  while (n_my > 0) {
     uint32_t qf[16];
     {
       const __half *qrow =
@@ -410,11 +498,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
         qf[4 * i + 3] = raw.w;
       }
     }
-    State st;
     st.reset();
     const int seg_end = cs.s0 + cs.np;
-    const int pe = min(seg_end, e);
-    for (; fc < pe; fc += kWarps) {
+    const int pe = min(seg_end, ew);
+    for (; fc < pe; ++fc) {
       if (ok) {
         ok = __all_sync(kFull, mbar_wait_bounded(&bars[sc], phase));
         if (!ok) fail_k = kc;
@@ -434,18 +521,13 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
       }
       if ((++kc & 31) == 0) sc_use = sc_cur;  // (the issue side is in that batch by now)
     }
-    const bool last = pe >= e;
-    if (last) pdl_launch_dependents();
-
-    // ---- combine the four warps' states ----
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       st.l[h] += __shfl_xor_sync(kFull, st.l[h], 4);
       st.l[h] += __shfl_xor_sync(kFull, st.l[h], 8);
       st.l[h] += __shfl_xor_sync(kFull, st.l[h], 16);
     }
-    if (warp > 0) {
-      if (piece > 0) named_bar_sync(2, kWarps * 32);  // warp 0 has read the last staging
+    if (max(cs.s0, a) < aw) {  // begun by a warp before this one, which joins it
       if (t < 2) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -459,90 +541,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
           }
         }
       }
-      named_bar_arrive(1, kWarps * 32);
+    } else if (min(seg_end, e) > ew) {
+      lead = true;
     } else {
-      named_bar_sync(1, kWarps * 32);
-      if (t < 2) {
-        const bool whole = cs.s0 >= a && seg_end <= e;
-        float f[kWarps][2], lse[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float mw[kWarps], lw[kWarps];
-          mw[0] = st.m[h];
-          lw[0] = st.l[h];
-#pragma unroll
-          for (int w = 1; w < kWarps; ++w) {
-            mw[w] = stg.m[w - 1][2 * t + h];
-            lw[w] = stg.l[w - 1][2 * t + h];
-          }
-          const float M = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
-          float sum = 0.f;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            // a warp without a finite score counts for nothing, unless its sum is NaN
-            f[w][h] = mw[w] == -INFINITY ? (lw[w] != lw[w] ? lw[w] : 0.f) : ex2(mw[w] - M);
-            sum += f[w][h] * lw[w];
-          }
-          const bool none = sum == 0.f;  // no live page
-          const float inv = none ? 0.f : 1.f / sum;
-          // (the lift comes off the sum, whose logarithm is most accurate near 1)
-          lse[h] = none ? -INFINITY : (M + kLift + lg2(sum * 0x1p-7f)) * kLn2;
-          static_assert(kLift == 7.f, "the factor of the sum");
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) f[w][h] *= inv;
-          f[0][h] *= st.nu;
-        }
-        float r[2][16];  // of either head
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            r[h][2 * i] = f[0][h] * st.o[i][h];
-            r[h][2 * i + 1] = f[0][h] * st.o[i][h + 2];
-          }
-#pragma unroll
-          for (int w = 1; w < kWarps; ++w) {
-            const float4 x = stg.o[w - 1][i][2 * g + t];
-            r[0][2 * i] = fmaf(f[w][0], x.x, r[0][2 * i]);
-            r[1][2 * i] = fmaf(f[w][1], x.y, r[1][2 * i]);
-            r[0][2 * i + 1] = fmaf(f[w][0], x.z, r[0][2 * i + 1]);
-            r[1][2 * i + 1] = fmaf(f[w][1], x.w, r[1][2 * i + 1]);
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (whole) {
-            const int64_t row = static_cast<int64_t>(cs.b) * hq + cs.g * kGroup + 2 * t + h;
-            uint4 *po = reinterpret_cast<uint4 *>(out + row * kHeadDim + 16 * g);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const __half2 x = __floats2half2_rn(r[h][8 * i + 2 * j], r[h][8 * i + 2 * j + 1]);
-                w[j] = *reinterpret_cast<const uint32_t *>(&x);
-              }
-              po[i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            if (g == 0 && lse_out) lse_out[row] = lse[h];
-          } else {
-            const int64_t row =
-                (static_cast<int64_t>(blockIdx.x) * 2 + (piece == 0 ? 0 : 1)) * kGroup + 2 * t + h;
-            float4 *po = reinterpret_cast<float4 *>(part_o + row * kHeadDim + 16 * g);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              po[i] = make_float4(r[h][4 * i], r[h][4 * i + 1], r[h][4 * i + 2], r[h][4 * i + 3]);
-            if (g == 0) part_lse[row] = lse[h];
-          }
-        }
-      }
-      __syncwarp();
-      if (!last) named_bar_arrive(2, kWarps * 32);
+      finish(0);
     }
-    if (last) break;
+    if (pe >= ew) break;
     cs.next(seq_lens, hkv, cap);
-    ++piece;
   }
+  pdl_launch_dependents();
+  __syncthreads();
+  if (lead) finish((min(cs.s0 + cs.np, e) - a + run - 1) / run);
 
   if (!ok) {
     // let the copies in flight land (bounded) before the CTA's memory is released
