@@ -787,7 +787,8 @@ int32_t k16v8_rope_kv_append_k8v8(
  *   workspace  k16v8_decode_workspace_size_k8v8(...) bytes, 256-B aligned, needs
  *              no initialisation; calls that overlap on the GPU, replays of
  *              captured ones too, must not share one
- *   q, out     device fp16 [batch][num_qo_heads][head_dim], 16-B aligned;
+ *   q, out     device fp16 [batch][num_qo_heads][head_dim], 16-B aligned; out may
+ *              be q
  *   lse        device fp32 [batch][num_qo_heads] or NULL
  * A sequence of length 0 gives out = 0, lse = -inf.  Lengths outside [0, 16 *
  * max_pages_per_seq] flag K16V8_DEVERR_SEQLEN and are clamped; a page id outside
@@ -828,7 +829,7 @@ int32_t k16v8_paged_decode_attention_k8v8(
  *                bytes for the same arguments on the same device (0 only where
  *                they are refused); needs no initialisation.  Calls that overlap
  *                on the GPU, replays of captured ones too, must not share one.
- *   out          device fp16 like q; lse device fp32 [total_q][num_qo_heads] or
+ *   out          device fp16 like q, or q itself; lse device fp32 [total_q][num_qo_heads] or
  *                NULL.  Rows of no sequence are left as they are
  * A sequence with rows outside [0, total_q), n > max_qlen, a length outside [0,
  * max_seq_len] or (prefill) n > L flags K16V8_DEVERR_SEQLEN and is skipped; a

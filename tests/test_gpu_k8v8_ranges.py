@@ -149,3 +149,25 @@ def test_overlapping_calls(K):
     for i, outs in got:
         for a, b in zip(outs, want[i]):
             assert torch.equal(a, b)
+
+
+def test_outputs_over_the_queries(K):
+    """Rows may be written over the queries they were read from: whole and cut
+    segments, many and few rows."""
+    rng = np.random.default_rng(3)
+    lens = [900, 64, 2500]
+    table, kc, vc, sc = R.poisoned_pool(rng, lens, 2)
+    cache, dtable, dlens = [to_dev(x) for x in (kc, vc, sc)], to_dev(table), i32(lens)
+    q = to_dev(rng.standard_normal((180, 8, 128)).astype(np.float16))
+    ws = empty(max(K.k16v8_attention_workspace_size_k8v8(100, 8, 2, 128), K.k16v8_decode_workspace_size_k8v8(3, 8, 128)))
+    for name, rows, most, indptr in (("decode", 3, 1, None), ("prefill", 180, 100, i32([0, 100, 120, 180])),
+                                     ("cross", 180, 100, i32([0, 100, 120, 180])), ("cross", 9, 4, i32([0, 3, 5, 9]))):
+        got = q[:rows].clone()
+        want = torch.empty_like(got)
+        for src, out in ((got, want), (got, got)):
+            if name == "decode":
+                K.k16v8_paged_decode_attention_k8v8(src, *cache, dtable, dlens, SCALE, ws, out)
+            else:
+                getattr(K, f"k16v8_paged_{name}_attention_k8v8")(src, indptr, most, *cache, dtable, dlens, max(lens),
+                                                                 SCALE, ws, out)
+        assert torch.equal(got, want)
