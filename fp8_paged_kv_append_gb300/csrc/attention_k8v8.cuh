@@ -37,8 +37,8 @@
 // 51% active), 2,140 cycles a unit, in which operands, codes and widened tiles move
 // some 160 KB through shared memory (1,280 cycles); without the exponentials' ex2 it
 // is 140, without the row maxima 142, without the widening's arithmetic 138.  In short
-// pieces their starts and ends come to that: 8 x 1024 causal 121.5 us (708 TFLOP/s),
-// 16 x 448 rows over 1,500 171.5 us (722).  With one row tile: the widening warps, at
+// pieces their starts and ends come to that: 8 x 1024 causal 120.5 us (713 TFLOP/s),
+// 16 x 448 rows over 1,500 171 us (724).  With one row tile: the widening warps, at
 // work 0.6 of the time, and the hand-offs on either side of them: 8 rows at 128K 114
 // us (2.9 TB/s of codes, 0.43 of the copy rate); 5 rows over 1,500 13.2 us, nearly all
 // of it the latency of one piece and the merge.
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
   } else if (warp == kLoadVWarp || warp == kLoadKWarp) {
     // ================= loads; V's: the CTA's pieces, K's: the queries =================
     // V's lane 0 walks the pieces: the first at the start, the next one behind the
-    // copies of a piece's first tile.
+    // copies of a piece's first half tile.
     const bool is_v = warp == kLoadVWarp;
     const int bar_staged = is_v ? kBarVstFull : kBarKstFull, bar_read = is_v ? kBarVstEmpty : kBarKstEmpty;
     const CUtensorMap *map = is_v ? &tmap_v : &tmap_k;
@@ -893,7 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
         }
         arrive_behind_copies(bar0 + 8 * (bar_staged + dst.s));
       }
-      const bool first = h == 2 * pc.t0;
+      // (K: the first tile's copies are out, whose loads do not wait for the queries')
+      const bool first = h == (is_v ? 2 * pc.t0 : min(2 * pc.t0 + 1, pc.h1 - 1));
       ++h;
       if (!(h & 1) || h == pc.h1) ++tiles;
       if (at == 7) {

@@ -813,6 +813,8 @@ int32_t k16v8_paged_decode_attention_k8v8(
  *   cross:   every row sees all L positions (an encoder's states, written with
  *            k16v8_rope_kv_append_k8v8 and num_qo_heads = 0); n and L are
  *            unrelated, L may be 0
+ * One row per sequence is better served by k16v8_paged_decode_attention_k8v8,
+ * which sees all positions too (1,024 sequences of 100: 54 against 260 us).
  * Over what a row sees: lse = ln sum exp(s_j), out = sum exp(s_j - lse) v_j, s_j
  * = sm_scale * q.k_j.  A row that sees nothing gives out = 0, lse = -inf.  What
  * is stored at a position that a row does not see (NaN, inf) does not reach it.
