@@ -6,9 +6,14 @@
 // keys in 8 bits and scales per page are this library's.
 //
 // Mathematics.  With kappa, nu the scales of a page: scores sm_scale * kappa *
-// (q . code_k), softmax over all positions, out = sum p * nu * code_v.  Both
-// scales are constant over a page, which is a warp's unit of work, so kappa
-// joins the score's factor and nu the weight: no element is multiplied by one.
+// (q . code_k), softmax over all positions, out = sum p * nu * code_v.  kappa is
+// constant over a page, which is a warp's unit of work, and joins the score's
+// factor.  nu multiplies the widened values, which is exact: a code times a scale
+// of the cache's range is an fp16 number.  (It is not joined to the weight: in fp16
+// the weights would have to be held against the largest nu of a run, and pages of
+// small nu beside a page of large nu would lose their bits.  Pages' products scaled
+// in fp32 behind the MMAs instead: registers spill, 1,024 sequences of 50 to 100
+// positions 57 against 54 us.)
 //
 // The cut is that of the K16/V8 balanced decode (decode_balanced.cu): CTA i of one
 // full wave takes flat (sequence, KV head, page) tiles [i W, (i + 1) W), and a merge
@@ -23,9 +28,10 @@
 //    a step; codes are widened to fp16 pairs in registers.
 //  * O^T += V^T p: 16 dims as M, the 16 tokens as K, heads as N.  A lane reads 16
 //    dims of its 4 tokens, interleaves the bytes of two tokens (prmt) and widens
-//    the pairs.  The weights change hands by two 8x8 transposes (movmatrix), and
-//    the accumulators' columns are the heads whose scores the lane holds, so the
-//    rescale factors need no exchange.
+//    the pairs.  A weight, in fp16, is off by 2^-11 of itself, or by 2^-32 of the
+//    row's largest where that is more, as in attention_k8v8.cuh.  The weights change
+//    hands by two 8x8 transposes (movmatrix), and the accumulators' columns are the
+//    heads whose scores the lane holds, so the rescale factors need no exchange.
 //  * The running maximum moves only when a score exceeds it by 2^8: a tile
 //    needs one vote instead of a reduction over its tokens.
 // Tiles are staged by TMA with the 128-byte swizzle: a row is 128 bytes, and the
@@ -89,6 +95,11 @@ __device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
   const __half2 h = e4m3x2_to_half2(static_cast<uint16_t>(w >> 16));
   return *reinterpret_cast<const uint32_t *>(&h);
 }
+// Two fp16 times a scale.
+__device__ __forceinline__ uint32_t times(uint32_t x, __half2 s) {
+  const __half2 h = __hmul2(*reinterpret_cast<const __half2 *>(&x), s);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
 __device__ __forceinline__ void tma_load_evict_first(void *dst, const CUtensorMap *map, int y,
                                                      uint64_t *bar, uint64_t policy) {
   asm volatile(
@@ -104,14 +115,13 @@ __device__ __forceinline__ int clamped_len(const int32_t *seq_lens, int b, int c
 
 // A warp's running state, lane 4g + t: heads 2t and 2t + 1 (t < 2; the padding
 // heads of the others hold zeros).  m is kLift below a maximum of the scores so
-// far, l the sum over the lane's tokens, o the 16 dims from 16g in units of the
-// largest value scale so far.
+// far, l the sum over the lane's tokens, o the 16 dims from 16g.
 struct State {
-  float m[2], l[2], nu;
+  float m[2], l[2];
   float o[8][4];  // dims 16g + 2i (heads 2t, 2t + 1), 16g + 2i + 1
   __device__ __forceinline__ void reset() {
     m[0] = m[1] = -INFINITY;
-    l[0] = l[1] = nu = 0.f;
+    l[0] = l[1] = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
@@ -153,13 +163,10 @@ __device__ __forceinline__ void attend(const uint8_t *kp, const uint8_t *vp, int
     if (2 * t + 8 >= valid) v2 = none;
     if (2 * t + 9 >= valid) v3 = none;
   }
-  // ---- the maximum and the value scale move seldom ----
+  // ---- the maximum moves seldom ----
   const bool up = fmaxf(s[0], s[2]) > st.m[0] + (kLift + kSlack) ||
                   fmaxf(s[1], s[3]) > st.m[1] + (kLift + kSlack);
-  if (__any_sync(kFull, up) || nu > st.nu) {
-    const float nu_new = fmaxf(nu, st.nu);
-    const float fade = st.nu / nu_new;  // both powers of two
-    st.nu = nu_new;
+  if (__any_sync(kFull, up)) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       float top = fmaxf(s[e], s[e + 2]);
@@ -170,34 +177,34 @@ __device__ __forceinline__ void attend(const uint8_t *kp, const uint8_t *vp, int
       const float alpha = m_new == st.m[e] ? 1.f : ex2(st.m[e] - m_new);
       st.m[e] = m_new;
       st.l[e] *= alpha;
-      const float f = alpha * fade;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        st.o[i][e] *= f;
-        st.o[i][e + 2] *= f;
+        st.o[i][e] *= alpha;
+        st.o[i][e + 2] *= alpha;
       }
     }
   }
-  const float share = nu / st.nu;
   float p[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) p[e] = ex2(s[e] - st.m[e & 1]);
   st.l[0] += p[0] + p[2];
   st.l[1] += p[1] + p[3];
-  const __half2 p01 = __floats2half2_rn(p[0] * share, p[1] * share);
-  const __half2 p23 = __floats2half2_rn(p[2] * share, p[3] * share);
+  const __half2 p01 = __floats2half2_rn(p[0], p[1]);
+  const __half2 p23 = __floats2half2_rn(p[2], p[3]);
   const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t *>(&p01));
   const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t *>(&p23));
   // ---- values ----
+  const __half2 sv = __float2half2_rn(nu);
   const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
   const uint32_t w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t lo01 = __byte_perm(w0[j], w1[j], 0x5140), hi01 = __byte_perm(w0[j], w1[j], 0x7362);
     const uint32_t lo23 = __byte_perm(w2[j], w3[j], 0x5140), hi23 = __byte_perm(w2[j], w3[j], 0x7362);
-    mma_16816(st.o[2 * j], widen_lo(lo01), widen_hi(lo01), widen_lo(lo23), widen_hi(lo23), b0, b1);
-    mma_16816(st.o[2 * j + 1], widen_lo(hi01), widen_hi(hi01), widen_lo(hi23), widen_hi(hi23), b0,
-              b1);
+    mma_16816(st.o[2 * j], times(widen_lo(lo01), sv), times(widen_hi(lo01), sv),
+              times(widen_lo(lo23), sv), times(widen_hi(lo23), sv), b0, b1);
+    mma_16816(st.o[2 * j + 1], times(widen_lo(hi01), sv), times(widen_hi(hi01), sv),
+              times(widen_lo(hi23), sv), times(widen_hi(hi23), sv), b0, b1);
   }
 }
 
@@ -431,7 +438,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
       static_assert(kLift == 7.f, "the factor of the sum");
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) f[w][h] *= inv;
-      f[0][h] *= st.nu;
     }
     float r[2][16];  // of either head
 #pragma unroll
@@ -531,8 +537,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_k8v8_kernel(
       if (t < 2) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          stg.o[warp - 1][i][2 * g + t] = make_float4(st.o[i][0] * st.nu, st.o[i][1] * st.nu,
-                                                      st.o[i][2] * st.nu, st.o[i][3] * st.nu);
+          stg.o[warp - 1][i][2 * g + t] = make_float4(st.o[i][0], st.o[i][1], st.o[i][2], st.o[i][3]);
         if (g == 0) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {

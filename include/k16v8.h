@@ -792,7 +792,10 @@ int32_t k16v8_rope_kv_append_k8v8(
  *   lse        device fp32 [batch][num_qo_heads] or NULL
  * A sequence of length 0 gives out = 0, lse = -inf.  Lengths outside [0, 16 *
  * max_pages_per_seq] flag K16V8_DEVERR_SEQLEN and are clamped; a page id outside
- * the pool flags K16V8_DEVERR_PAGE and its positions are left out.
+ * the pool flags K16V8_DEVERR_PAGE and its positions are left out.  The weights are
+ * rounded to fp16 before they meet the values, as in the prefill call: 2^-11
+ * relative, or 2^-32 of the row's largest weight where that is more, whatever the
+ * pages' scales.
  */
 size_t k16v8_decode_workspace_size_k8v8(int32_t batch, int32_t num_qo_heads, int32_t head_dim);
 
