@@ -707,8 +707,8 @@ using namespace k16v8;
 extern "C" size_t k16v8_decode_workspace_size_k8v8(int32_t batch, int32_t num_qo_heads,
                                                    int32_t head_dim) {
   decode8::Layout w;
-  if (batch < 0 || batch > decode8::kMaxBatch || num_qo_heads <= 0 || head_dim != kHeadDim ||
-      !decode8::layout(batch, &w))
+  if (batch < 0 || batch > decode8::kMaxBatch || num_qo_heads <= 0 || num_qo_heads % kGroup ||
+      head_dim != kHeadDim || !decode8::layout(batch, &w))
     return 0;
   return w.total;
 }

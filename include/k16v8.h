@@ -784,9 +784,9 @@ int32_t k16v8_rope_kv_append_k8v8(
  *   sm_scale   finite, >= 0
  *   block_table  device int32 [batch][max_pages_per_seq] (may be NULL where that
  *              is 0)
- *   workspace  k16v8_decode_workspace_size_k8v8(...) bytes, 256-B aligned, needs
- *              no initialisation; calls that overlap on the GPU, replays of
- *              captured ones too, must not share one
+ *   workspace  k16v8_decode_workspace_size_k8v8(...) bytes (0 only where the sizes
+ *              are refused), 256-B aligned, needs no initialisation; calls that
+ *              overlap on the GPU, replays of captured ones too, must not share one
  *   q, out     device fp16 [batch][num_qo_heads][head_dim], 16-B aligned; out may
  *              be q
  *   lse        device fp32 [batch][num_qo_heads] or NULL
