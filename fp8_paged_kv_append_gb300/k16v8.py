@@ -709,7 +709,8 @@ def _axes(pair_axis, half: int) -> bytes:
     """The axis of each pair as the host array of the C ABI (bytes are taken as
     they are)."""
     if type(pair_axis) is not bytes:
-        pair_axis = bytes(pair_axis)
+        # (by its entries: bytes() of an array would be its memory, of a number zeros)
+        pair_axis = bytes(list(pair_axis))
     if len(pair_axis) != half:
         raise ValueError(f"pair_axis must have an entry for each of {half} pairs, got "
                          f"{len(pair_axis)}")
