@@ -26,9 +26,12 @@
 //
 // HBM-bound where there are many tokens: 41.7 us for 8,192 bf16 tokens of 40 + 10
 // heads, 5.5 TB/s of the bytes it cannot do without (0.81 of the copy rate; without
-// rotation 37.3, 0.91), 34.6 for 4,096 fp32 ones (0.76).  A step of 32 sequences
-// takes 4.8 us, one launch with four dependent loads (rows, table entry, positions,
-// held scale), of 8,192 66 (0.51 of the copy rate).
+// rotation 37.3, 0.91), 45 for as many fp16 ones (0.75), 34.6 for 4,096 fp32 ones
+// (0.76); 24,000 bf16 states without queries and rotation 33.1 (0.82).  A step of 32
+// sequences takes 4.8 us, one launch with four dependent loads (rows, table entry,
+// positions, held scale), of 8,192 66 (0.51 of the copy rate).  A step in which every
+// page's scales grow codes the held rows again one after another, a load and a store
+// each: 32 sequences 11.3 us, 256 12.1, 1,024 23.6 (4.7, 5.6 and 10.4 without).
 #include <algorithm>
 
 #include "k8v8_device.cuh"
@@ -48,9 +51,10 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 // 16-bit rows: 80 registers and 24 warps per SM, 41.7 us for 8,192 tokens of 40 + 10
 // heads (5: 43.5, 7: 44.2; the turned rows kept in registers, 128 of them, 4 us more;
-// the next task's rows loaded into each unit's registers as it is stored 48.0); steps
-// spill in 80 (256 sequences 5.6 us, with 6 5.8).  fp32 rows take 164 (2 to 4 per SM
-// alike).
+// the next task's rows loaded into each unit's registers as it is stored 48.0).  In 80,
+// fp16 prompts spill 28 to 36 bytes of a thread and interleaved bf16 ones 24; steps take
+// 96 (256 sequences 5.6 us, with 6 per SM 5.8; the bf16 form of apart halves spills 4
+// bytes in them).  fp32 rows take 162 to 168 (2 to 4 per SM alike).
 template <typename T, bool kStep>
 constexpr int kCtasPerSm = sizeof(T) == 2 ? (kStep ? 5 : 6) : 3;
 constexpr int kUnits = kPage * kUnitsPerRow / 32;  // of a lane and task
@@ -457,7 +461,8 @@ static int32_t launch(const Args &a, cudaStream_t stream) {
   // Calls of about a token per sequence: a CTA holds all heads of a token's page.  So and
   // by pages with parts of the heads: 32 sequences 4.8 and 5.1 us, 256 5.6 and 12.0, 1,024
   // 13.2 and 42, 8,192 66 and 321; two tokens each, where its rows wait for one another,
-  // 256 26.7 and 13.8, 1,024 53 and 46.
+  // 256 26.7 and 13.8, 1,024 53 and 46.  (The average decides: 256 single rows beside a
+  // chunk of 512 tokens go by pages, 15.7 us, alone they take 5.6 and 7.2.)
   if (4LL * a.num_tokens <= 5LL * a.batch) {
     const int parts = (2 * a.hkv + a.hq + kStepTasks - 1) / kStepTasks;
     return k16v8_launch_pdl(append_k8v8_kernel<T, kInterleaved, true>,
@@ -466,7 +471,7 @@ static int32_t launch(const Args &a, cudaStream_t stream) {
   }
   const int64_t items = a.num_tokens / kPage + 2LL * a.batch;
   // Two KV heads share a table where there are pages enough.  Two and one: 8,192 bf16
-  // tokens 41.7 and 48.7 us, 64 x 64 fp16 20.5 and 22.5; 5 x 311 fp32 of 2 heads (210
+  // tokens 41.7 and 48.7 us, 64 of 32 to 64 fp16 20.5 and 22.5; 5 x 300 fp32 of 2 heads (about 100
   // items) 7.7 and 6.6.  (Three to five: 44 to 51 for the first.)
   const int kv_per_cta = items * a.hkv >= 8LL * sms ? 2 : 1;
   const int parts = (a.hkv + kv_per_cta - 1) / kv_per_cta;

@@ -233,7 +233,7 @@ static int32_t attention_k8v8(bool causal, const void *q, const int32_t *qo_indp
   // Short segments are cut by many CTAs each and want pieces in flight (8), tall ones
   // fewer CTAs (8 per 32 rows or 2).  64 and 32 dims to a CTA, both kernels: 5 rows over
   // 1,500 13.8 and 13.3 us, 8 rows at 128K 117.2 and 116.0; 20 over 8,000 121.7 and
-  // 122.3, 64 x 40 of 300 42.4 and 43.1, 8 x 1024 131.9 and 133.4.
+  // 122.3, 64 x 20 to 40 of 150 to 300 42.4 and 43.1, 8 x 1024 131.9 and 133.4.
   return max_qlen > 16 ? attn8::launch_merge<4>(a, w.ctas, s)
                        : attn8::launch_merge<2>(a, w.ctas, s);
 }

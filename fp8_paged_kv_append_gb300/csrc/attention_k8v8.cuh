@@ -38,8 +38,8 @@
 // some 160 KB through shared memory (1,280 cycles); without the exponentials' ex2 it
 // is 140, without the row maxima 142, without the widening's arithmetic 138.  In short
 // pieces their starts and ends come to that: 8 x 1024 causal 120.5 us (713 TFLOP/s),
-// 16 x 448 rows over 1,500 171 us (724).  With one row tile: the widening warps, at
-// work 0.6 of the time, and the hand-offs on either side of them: 8 rows at 128K 114
+// 16 x 283 to 448 rows over 945 to 1,500 171 us (871).  With one row tile: the widening warps, at
+// work 0.6 of the time, and the hand-offs on either side of them: 8 rows at 128K 115
 // us (2.9 TB/s of codes, 0.43 of the copy rate); 5 rows over 1,500 13.2 us, nearly all
 // of it the latency of one piece and the merge.
 // Code size matters throughout: the roles' loops together are about as large as
@@ -584,8 +584,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(
           }
         }
         // The slots of two row tiles exponentiate in turn, one under the other's MMAs,
-        // or both would wait for both.  1,024 rows of 8,192 158.8 -> 143 us, 16 x 448
-        // over 1,500 186.6 -> 178, 4,000 rows 201 -> 190; 64 x 40 of 300 42.6 -> 43.2.
+        // or both would wait for both.  1,024 rows of 8,192 158.8 -> 143 us, 16 x 283
+        // to 448 over 945 to 1,500 186.6 -> 178, 3,800 rows 201 -> 190; 64 x 20 to 40 of 150
+        // to 300 42.6 -> 43.2.
         if (two) {
           ok = __all_sync(kFull, wait(kBarTurn + w, (turns++ + 1 - w) & 1));
           if (!ok) break;

@@ -36,12 +36,14 @@
 //    needs one vote instead of a reduction over its tokens.
 // Tiles are staged by TMA with the 128-byte swizzle: a row is 128 bytes, and the
 // lanes that read one column of 16-byte chunks would meet in the same banks.
-// Both kernels: 16 sequences of 8K 59 us (5.8 TB/s of the bytes it cannot do
-// without, 0.85 of the copy rate), one of 128K 58.8, 32 of up to 1K 19.8 (0.53), one
-// of 1K 7.0, 1,024 of 100 54 (0.59), 8,192 of 40 281 (0.42).  Some 7 us are fixed:
-// plan, first loads, the cut segments' merge.  (Warps that take a CTA's tiles in turn
-// and join at the end of every segment: 7.4 us for one of 1K, 70.6 for 1,024 of 100,
-// 447 for 8,192 of 40, 0.5% less for the long ones.)
+// Both kernels: 16 sequences of 8.3K 58.5 us (5.8 TB/s of the bytes it cannot do
+// without, 0.86 of the copy rate), one of 128K 58.2, 32 of 0.6K to 1.15K 18.9 (0.56),
+// one of 1.1K 6.8, 1,024 of 50 to 100 54 (0.59; all of 100 70, 0.60), 8,192 of 20 to 40
+// 273 (0.43; all of 40 304, 0.49).  Some 7 us are fixed: plan, first loads, the cut
+// segments' merge.  (With value scales joined to the weights, which cost more than the
+// products do now: warps that take a CTA's tiles in turn and join at the end of every
+// segment 7.4 / 7.0 us for one of 1.1K, 70.6 / 54 for 1,024 of 50 to 100, 447 / 281 for
+// 8,192 of 20 to 40, 0.5% less for the long ones.)
 #include <math.h>
 
 #include "k8v8_device.cuh"
@@ -767,8 +769,8 @@ extern "C" int32_t k16v8_paged_decode_attention_k8v8(
       static_cast<__half *>(out), lse, dev_error);
   if (st != K16V8_OK) return st;
   // Few segments are cut by many CTAs each (61 for one sequence of 128K and 10 heads),
-  // many by a few.  4 warps a row and 1, both kernels: 1 x 1K 7.4 and 9.0 us, 1 x 128K
-  // 58.2 and 63.5; 32 x 1K 21.2 and 19.8, 256 x 0.5K 55.4 and 49.9.
+  // many by a few.  4 warps a row and 1, both kernels: one of 1.1K 6.7 and 7.6 us, one of
+  // 128K 58.4 and 60.4; 32 of 0.6K to 1.15K 20.2 and 18.9, 256 of 250 to 500 54.2 and 48.5.
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return batch * num_kv_heads <= 64
              ? decode8::launch_merge<4>(batch, num_kv_heads, ws, w, out, lse, s)
